@@ -368,6 +368,136 @@ int wq_linear_w4a8(const uint16_t* x, int64_t M, int64_t K, const int32_t* outli
                    const uint32_t* packed, const uint16_t* scales, const uint16_t* zeros, int64_t N, int32_t group,
                    void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The same product of activations that are already INT8 (from wq_quantize_act_int8 or
+ * wq_add_rmsnorm_int8, with the same outliers). Two launches: the outlier weights, the
+ * INT8 MFMA product; results equal wq_linear_w4a8's on the same xq, sx, xo.
+ *  workspace  required for M >= 1, 256-byte aligned,
+ *             wq_linear_w4a8_quantized_workspace_bytes(N) bytes (the outlier weights).
+ */
+size_t wq_linear_w4a8_quantized_workspace_bytes(int64_t N);
+int wq_linear_w4a8_quantized(const int8_t* xq, const float* sx, const uint16_t* xo, int64_t M, int64_t K,
+                             const int32_t* outliers, int64_t n_out, const uint32_t* packed, const uint16_t* scales,
+                             const uint16_t* zeros, int64_t N, int32_t group, void* y, int32_t y_dtype,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, before a quantized product. With
+ * float32 inside and one rounding at each output:
+ *   h = x + residual,   y = h / sqrt(mean over the row of h^2 + eps) * weight.
+ * K is a positive multiple of 16 here (products need a multiple of 128), eps >= 0 and
+ * finite (WQ_ERR_UNSUPPORTED otherwise); a row of zeros with eps = 0 gives NaN.
+ *  x         [M, K] fp16, 16-byte aligned.
+ *  residual  [M, K] fp16, 16-byte aligned, or NULL (h = x).
+ *  weight    [K] fp16, 16-byte aligned.
+ *  h         [M, K] fp16 out, 16-byte aligned, or NULL: the sum, the next block's
+ *            residual. It may be x or residual itself.
+ */
+
+/* wq_add_rmsnorm - y [M, K] fp16 out, 16-byte aligned. */
+int wq_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                   float eps, uint16_t* h, uint16_t* y, void* stream);
+
+/*
+ * wq_add_rmsnorm_int8 - y in 8 bits, as wq_linear_w4a8_quantized reads it: with
+ * s = amax / 127 over the row's channels that are not outliers (1 when amax is 0),
+ *  xq  [M, K] int8 out, 16-byte aligned: rint(y / s) in the byte order of
+ *      wq_quantize_act_int8, 0 on outlier channels (y is not rounded to fp16 first, and
+ *      1 / s is applied as a factor, so a value within a few float32 roundings of a
+ *      half may come out one step from wq_quantize_act_int8 of wq_add_rmsnorm).
+ *  sx  [M] float32 out: s.   xo  [M, 16] fp16 out, 16-byte aligned: y of the outlier
+ *      channels, then zeros.   outliers, n_out as in wq_linear_w4a8.
+ */
+int wq_add_rmsnorm_int8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                        float eps, const int32_t* outliers, int64_t n_out, uint16_t* h, int8_t* xq, float* sx,
+                        uint16_t* xo, void* stream);
+
+/* wq_dequantize_act_int8 - out [M, K] fp16 (16-byte aligned): xq * sx in channel order,
+ * xo on the outlier channels. xo may be NULL when n_out == 0. K a multiple of 16. */
+int wq_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo, const int32_t* outliers,
+                           int64_t n_out, int64_t M, int64_t K, uint16_t* out, void* stream);
+
+/*
+ * Key/value cache in 4 bits, in pages, and causal attention over it (the KV4 of the
+ * W4A8KV4 rows in the DeepCompressor README). Each token's head_dim keys (values) of a
+ * head are one group of asymmetric 4-bit codes with an fp16 scale and zero-point, the
+ * form of wq_quantize_rtn with the range widened to hold 0:
+ *   hi = max(x, 0), lo = min(x, 0),   s = fp16(max(fl32(fl32(hi - lo) / 15), 2^-14)),
+ *   z = clamp(rint(-lo / s), 0, 15),  q = clamp(rint(x / s) + z, 0, 15),  x ~ (q - z) * s,
+ * head_dim + 8 bytes a token and head for both. Common arguments:
+ *  cache       [num_pages][kv_heads][wq_kv4_page_bytes(page_tokens, head_dim)] bytes,
+ *              16-byte aligned, the caller's; its contents on entry do not matter. The
+ *              layout inside a page is the library's own.
+ *  page_tokens tokens of a page: a positive multiple of 32 (WQ_ERR_UNSUPPORTED otherwise).
+ *  page_table  [B, max_pages] int32: token t of sequence b is in page
+ *              page_table[b][t / page_tokens]. Only entries of pages that hold a token in
+ *              use are read. Sequences may share pages that are only read.
+ *  seq_start   [B + 1] int32, not falling: sequence b's new tokens are the rows
+ *              seq_start[b] .. seq_start[b + 1] - 1 of q, k, v and out.
+ *  ctx_len     [B] int32: tokens of sequence b, the new ones last. With fewer tokens
+ *              than rows (a padded slot: one row, ctx_len 0) the first rows stand for
+ *              nothing: they are not appended, read as 0, and attend to nothing.
+ *  head_dim    64 or 128 (WQ_ERR_UNSUPPORTED otherwise).
+ *  max_new, max_q, max_ctx  the largest number of new tokens, and of tokens, of a
+ *              sequence. They only shape the launch: every sequence is handled in full
+ *              whatever they are, only slower when they are far off.
+ * Lengths, starts and page numbers outside their arrays are clamped on the device (wrong
+ * values, never an invalid access). B up to 2^20, kv_heads up to 65535, T = rows of the
+ * token-wise arrays below 2^31 / heads, max_pages * page_tokens up to 2^30. T = 0 or
+ * B = 0 returns WQ_OK without a launch.
+ */
+
+/* Bytes of one head's page; 0 for sizes the cache does not take. */
+size_t wq_kv4_page_bytes(int64_t page_tokens, int64_t head_dim);
+
+/*
+ * wq_kv4_append - quantizes the new tokens' keys and values into the cache.
+ *  k, v  [T, kv_heads, head_dim] fp16, 16-byte aligned; k_stride, v_stride elements from
+ *        one token to the next (a multiple of 8, at least kv_heads * head_dim), so that
+ *        they may be slices of one projection's output. Inputs are finite.
+ * A page that is written belongs to one sequence.
+ */
+int wq_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t T,
+                  int64_t kv_heads, int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B,
+                  int64_t max_new, const int32_t* page_table, int64_t max_pages, void* cache, int64_t num_pages,
+                  int64_t page_tokens, void* stream);
+
+/* wq_kv4_read - the new tokens' keys and values as the cache holds them: k, v
+ * [T, kv_heads, head_dim] fp16 out, contiguous, 16-byte aligned. */
+int wq_kv4_read(const void* cache, int64_t num_pages, int64_t page_tokens, int64_t T, int64_t kv_heads,
+                int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B, int64_t max_new,
+                const int32_t* page_table, int64_t max_pages, uint16_t* k, uint16_t* v, void* stream);
+
+/* Bytes of device workspace wq_kv4_attention needs (0 when no sequence is split; enough
+ * for any window, and for every smaller max_ctx). 0 for invalid sizes. */
+size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                        int64_t max_q, int64_t max_ctx);
+
+/*
+ * wq_kv4_attention - causal attention of the new tokens (already appended) over the
+ * cache: row i of sequence b, at position p = ctx_len[b] - (its rows) + i, sees tokens
+ * t <= p, and with window > 0 only t > p - window.
+ *   out = softmax over the seen t of (scale * q . k_t), times v_t;   0 where none is seen.
+ *  q       [T, q_heads, head_dim] fp16, 16-byte aligned, q_stride elements from one token
+ *          to the next (a multiple of 8, at least q_heads * head_dim). q_heads is a
+ *          multiple of kv_heads: query head j reads key/value head j / (q_heads / kv_heads).
+ *  scale   positive and finite (WQ_ERR_UNSUPPORTED otherwise), 1 / sqrt(head_dim) usually.
+ *  window  0 for none, else >= 1.
+ *  out     [T, q_heads, head_dim] fp16 out, contiguous, 8-byte aligned.
+ *  lse     [T, q_heads] float32 out, or NULL: log of the sum of exp(scale * q . k_t)
+ *          (-infinity where no token is seen).
+ *  workspace  256-byte aligned, wq_kv4_attention_workspace_bytes bytes for the same
+ *          sizes (may be NULL when that is 0); contents on entry do not matter.
+ * Scores, maxima and sums are fp32; a weight is rounded once to fp16, times its value
+ * scale, as an MFMA operand. Deterministic: a fixed order for the same sizes. Rows of q
+ * that belong to no sequence leave their rows of out and lse unwritten.
+ */
+int wq_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
+                     int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B, int64_t max_q,
+                     int64_t max_ctx, const int32_t* page_table, int64_t max_pages, const void* cache,
+                     int64_t num_pages, int64_t page_tokens, float scale, int64_t window, uint16_t* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* The kernel WQ_KERNEL_AUTO picks for an M x N x K product (WQ_KERNEL_GEMV or
  * WQ_KERNEL_GEMM; see wq_kernel). */
 int wq_auto_kernel(int64_t M, int64_t N, int64_t K);

@@ -16,6 +16,12 @@ Entry points (the same names as the C ABI, without the ``wq_`` prefix):
   act-order layers, kept in the permuted channel order
 * ``quantize_act_int8(x, outliers)``, ``linear_w4a8(x, outliers, ...)``
   INT8 activations with fp16 outlier channels on the same INT4 layer
+* ``add_rmsnorm(x, weight, residual)``, ``add_rmsnorm_int8(...)``
+  root-mean-square norm of x + residual, in fp16 or as the INT8 activations of
+  ``linear_w4a8_quantized``; ``dequantize_act_int8`` gives their values
+* ``kv4_cache(...)``, ``kv4_append(k, v, cache, ...)``, ``kv4_read(cache, ...)``,
+  ``kv4_attention(q, cache, ...)``
+  a paged key/value cache in 4 bits and causal attention over it
 """
 from __future__ import annotations
 
@@ -61,6 +67,21 @@ SIGNATURES = {
     "wq_linear_w4a8_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "wq_linear_w4a8": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _i32, _vp, _sz,
                                       _vp]),
+    "wq_linear_w4a8_quantized_workspace_bytes": (_sz, [_i64]),
+    "wq_linear_w4a8_quantized": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _vp,
+                                                _i32, _vp, _sz, _vp]),
+    "wq_add_rmsnorm": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, ctypes.c_float, _vp, _vp, _vp]),
+    "wq_add_rmsnorm_int8": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, ctypes.c_float, _vp, _i64, _vp, _vp, _vp, _vp,
+                                           _vp]),
+    "wq_dequantize_act_int8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "wq_kv4_page_bytes": (_sz, [_i64, _i64]),
+    "wq_kv4_append": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp,
+                                     _i64, _i64, _vp]),
+    "wq_kv4_read": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                   _vp]),
+    "wq_kv4_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "wq_kv4_attention": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
+                                        _i64, _i64, ctypes.c_float, _i64, _vp, _vp, _vp, _sz, _vp]),
     "wq_linear_sparse_noalloc": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64,
                                                 _vp, _i32, _vp]),
     "wq_auto_kernel": (ctypes.c_int, [_i64, _i64, _i64]),
@@ -473,6 +494,251 @@ def linear_w4a8(x, outliers, packed, scales, zeros, out_dtype=None, out=None, gr
                             _stream(x))
     _check("wq_linear_w4a8", rc)
     return out
+
+
+def linear_w4a8_quantized(xq, sx, xo, outliers, packed, scales, zeros, out_dtype=None, out=None, group: int = GROUP,
+                          workspace=None):
+    """``linear_w4a8`` of activations that are already INT8: ``xq``, ``sx``, ``xo`` from
+    ``quantize_act_int8`` or ``add_rmsnorm_int8`` with the same ``outliers``."""
+    import torch
+    lib = load()
+    out_dtype = torch.float16 if out_dtype is None else out_dtype
+    _need(xq, torch.int8, "xq")
+    _need(sx, torch.float32, "sx")
+    _need(xo, torch.float16, "xo")
+    _need(outliers, torch.int32, "outliers")
+    _need(packed, torch.int32, "packed")
+    _need(scales, torch.float16, "scales")
+    _need(zeros, torch.float16, "zeros")
+    M, K = xq.shape
+    N = packed.shape[0]
+    if packed.shape[1] * 8 != K or scales.shape != (N, K // group) or zeros.shape != scales.shape:
+        raise ValueError("inconsistent shapes")
+    if sx.numel() != M or tuple(xo.shape) != (M, 16):
+        raise ValueError("sx must be [M] and xo [M, 16]")
+    if out_dtype not in (torch.float16, torch.float32):
+        raise TypeError("out_dtype must be float16 or float32")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=xq.device)
+    else:
+        _need(out, out_dtype, "out")
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be [M, N]")
+    if workspace is None:
+        workspace = torch.empty(int(lib.wq_linear_w4a8_quantized_workspace_bytes(N)), dtype=torch.uint8,
+                                device=xq.device)
+    wbytes = workspace.numel() * workspace.element_size()
+    n_out = outliers.numel()
+    rc = lib.wq_linear_w4a8_quantized(_p(xq), _p(sx), _p(xo), M, K, _p(outliers) if n_out else None, n_out,
+                                      _p(packed), _p(scales), _p(zeros), N, group, _p(out),
+                                      1 if out_dtype == torch.float32 else 0, _p(workspace), wbytes, _stream(xq))
+    _check("wq_linear_w4a8_quantized", rc)
+    return out
+
+
+def _norm_args(x, weight, residual, h):
+    import torch
+    _need(x, torch.float16, "x")
+    _need(weight, torch.float16, "weight")
+    M, K = x.shape
+    if weight.numel() != K:
+        raise ValueError("weight must have K entries")
+    for t, name in ((residual, "residual"), (h, "h")):
+        if t is not None:
+            _need(t, torch.float16, name)
+            if t.shape != x.shape:
+                raise ValueError(f"{name} must have the shape of x")
+    # the sum is only written where there is something to add, or a place for it is given
+    return M, K, torch.empty_like(x) if h is None and residual is not None else h
+
+
+def add_rmsnorm(x, weight, residual=None, eps: float = 1e-5, out=None, h=None):
+    """Root-mean-square norm of ``x + residual`` (float16 [M, K]): returns ``(y, h)``,
+    y = h / sqrt(mean(h^2) + eps) * weight and h the sum, the next block's residual
+    (``x`` itself when ``residual`` is None). ``h`` may be ``x`` or ``residual``, to
+    update it in place."""
+    import torch
+    lib = load()
+    M, K, h = _norm_args(x, weight, residual, h)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, torch.float16, "out")
+        if out.shape != x.shape:
+            raise ValueError("out must have the shape of x")
+    _check("wq_add_rmsnorm", lib.wq_add_rmsnorm(_p(x), _p(residual), _p(weight), M, K, eps, _p(h), _p(out),
+                                                _stream(x)))
+    return out, x if h is None else h
+
+
+def add_rmsnorm_int8(x, weight, residual=None, eps: float = 1e-5, outliers=None, h=None):
+    """``add_rmsnorm`` with its output in 8 bits, as ``linear_w4a8_quantized`` reads it:
+    returns ``(xq, sx, xo, h)``, int8 [M, K] in the products' byte order, one float32
+    scale per row, and the float16 values [M, 16] of the ``outliers`` channels (int32,
+    at most 16)."""
+    import torch
+    lib = load()
+    M, K, h = _norm_args(x, weight, residual, h)
+    n_out = 0
+    if outliers is not None:
+        _need(outliers, torch.int32, "outliers")
+        n_out = outliers.numel()
+    xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    sx = torch.empty(M, dtype=torch.float32, device=x.device)
+    xo = torch.empty((M, 16), dtype=torch.float16, device=x.device)
+    rc = lib.wq_add_rmsnorm_int8(_p(x), _p(residual), _p(weight), M, K, eps, _p(outliers) if n_out else None, n_out,
+                                 _p(h), _p(xq), _p(sx), _p(xo), _stream(x))
+    _check("wq_add_rmsnorm_int8", rc)
+    return xq, sx, xo, x if h is None else h
+
+
+def dequantize_act_int8(xq, sx, xo=None, outliers=None):
+    """The float16 values [M, K] that INT8 activations stand for, in channel order."""
+    import torch
+    lib = load()
+    _need(xq, torch.int8, "xq")
+    _need(sx, torch.float32, "sx")
+    M, K = xq.shape
+    n_out = 0 if outliers is None else outliers.numel()
+    if n_out:
+        _need(outliers, torch.int32, "outliers")
+        _need(xo, torch.float16, "xo")
+    if sx.numel() != M or (n_out and tuple(xo.shape) != (M, 16)):
+        raise ValueError("sx must be [M] and xo [M, 16]")
+    out = torch.empty((M, K), dtype=torch.float16, device=xq.device)
+    rc = lib.wq_dequantize_act_int8(_p(xq), _p(sx), _p(xo) if n_out else None, _p(outliers) if n_out else None, n_out,
+                                    M, K, _p(out), _stream(xq))
+    _check("wq_dequantize_act_int8", rc)
+    return out
+
+
+def kv4_page_bytes(page_tokens, head_dim):
+    return int(load().wq_kv4_page_bytes(page_tokens, head_dim))
+
+
+def kv4_cache(num_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
+    """An empty 4-bit key/value cache: uint8 [num_pages, kv_heads, page bytes], for pages
+    of ``page_tokens`` tokens (a multiple of 32) and ``head_dim`` 64 or 128."""
+    import torch
+    nbytes = kv4_page_bytes(page_tokens, head_dim)
+    if nbytes == 0:
+        raise ValueError("page_tokens must be a multiple of 32 and head_dim 64 or 128")
+    return torch.empty((num_pages, kv_heads, nbytes), dtype=torch.uint8, device=device)
+
+
+def _rows(t, name, heads, head_dim):
+    """Elements between the tokens of ``t`` [T, heads, head_dim], whose heads must be
+    contiguous (a slice of a wider projection's output is)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}]")
+    if (t.stride(2) != 1 and head_dim > 1) or (t.stride(1) != head_dim and heads > 1):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def _kv4_view(cache, page_table, seq_start, ctx_len, head_dim):
+    """(B, max_pages, num_pages, page_tokens, kv_heads) of a batch and its cache."""
+    import torch
+    _need(cache, torch.uint8, "cache")
+    _need(page_table, torch.int32, "page_table")
+    _need(seq_start, torch.int32, "seq_start")
+    _need(ctx_len, torch.int32, "ctx_len")
+    if cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, kv_heads, page bytes], as kv4_cache makes it")
+    num_pages, kv_heads, nbytes = cache.shape
+    B = ctx_len.numel()
+    tile = kv4_page_bytes(32, head_dim)
+    if tile == 0 or nbytes == 0 or nbytes % tile:
+        raise ValueError(f"the cache's pages of {nbytes} bytes do not hold whole tiles of head_dim {head_dim}")
+    if seq_start.numel() != B + 1:
+        raise ValueError("seq_start must have one entry more than ctx_len")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, pages]")
+    return B, page_table.shape[1], num_pages, nbytes // tile * 32, kv_heads
+
+
+def kv4_append(k, v, cache, page_table, seq_start, ctx_len, max_new=None):
+    """Quantizes new tokens' keys and values (float16 [T, kv_heads, head_dim]; slices of a
+    wider projection's output are fine) into ``cache``.
+
+    Sequence b's tokens are the rows ``seq_start[b]`` to ``seq_start[b + 1]`` (int32
+    [B + 1]), the last of its ``ctx_len[b]`` (int32 [B]) tokens; token t is in page
+    ``page_table[b, t // page_tokens]`` (int32 [B, pages]). ``max_new``: the most new
+    tokens of a sequence, if known (it shapes the launch only)."""
+    lib = load()
+    T, head_dim = k.shape[0], k.shape[-1]
+    B, max_pages, num_pages, page_tokens, kv_heads = _kv4_view(cache, page_table, seq_start, ctx_len, head_dim)
+    ks, vs = _rows(k, "k", kv_heads, head_dim), _rows(v, "v", kv_heads, head_dim)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    rc = lib.wq_kv4_append(_p(k), ks, _p(v), vs, T, kv_heads, head_dim, _p(seq_start), _p(ctx_len), B,
+                           T if max_new is None else max_new, _p(page_table), max_pages, _p(cache), num_pages,
+                           page_tokens, _stream(k))
+    _check("wq_kv4_append", rc)
+
+
+def kv4_read(cache, page_table, seq_start, ctx_len, tokens: int, head_dim: int, max_new=None):
+    """The keys and values of each sequence's last tokens as ``cache`` holds them: float16
+    [tokens, kv_heads, head_dim] each, rows as in ``kv4_append``."""
+    import torch
+    lib = load()
+    B, max_pages, num_pages, page_tokens, kv_heads = _kv4_view(cache, page_table, seq_start, ctx_len, head_dim)
+    k = torch.empty((tokens, kv_heads, head_dim), dtype=torch.float16, device=cache.device)
+    v = torch.empty_like(k)
+    rc = lib.wq_kv4_read(_p(cache), num_pages, page_tokens, tokens, kv_heads, head_dim, _p(seq_start), _p(ctx_len), B,
+                         tokens if max_new is None else max_new, _p(page_table), max_pages, _p(k), _p(v),
+                         _stream(cache))
+    _check("wq_kv4_read", rc)
+    return k, v
+
+
+def kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx):
+    return int(load().wq_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx))
+
+
+def kv4_attention(q, cache, page_table, seq_start, ctx_len, max_q=None, max_ctx=None, scale=None, window: int = 0,
+                  out=None, return_lse: bool = False, workspace=None):
+    """Causal attention of new tokens' queries (float16 [T, q_heads, head_dim]; a slice of
+    a wider projection's output is fine) over ``cache``, to which their keys and values
+    are already appended; sequences and pages as in ``kv4_append``.
+
+    A row sees the tokens up to its own, with ``window`` > 0 only the last ``window`` of
+    them; a row that sees none gives 0. ``scale`` is 1 / sqrt(head_dim) when omitted.
+    ``max_q`` and ``max_ctx``, the most new tokens and the most tokens of a sequence,
+    shape the launch only (the largest possible when omitted). Returns the float16
+    output [T, q_heads, head_dim], with ``return_lse`` also float32 [T, q_heads], the log
+    of each row's sum of exponentials. ``workspace`` (uint8 device tensor of
+    ``kv4_attention_workspace_bytes`` bytes) is allocated per call when omitted."""
+    import torch
+    lib = load()
+    T, q_heads, head_dim = q.shape
+    B, max_pages, num_pages, page_tokens, kv_heads = _kv4_view(cache, page_table, seq_start, ctx_len, head_dim)
+    qs = _rows(q, "q", q_heads, head_dim)
+    max_q = T if max_q is None else max_q
+    max_ctx = max_pages * page_tokens if max_ctx is None else max_ctx
+    if out is None:
+        out = torch.empty((T, q_heads, head_dim), dtype=torch.float16, device=q.device)
+    else:
+        _need(out, torch.float16, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    lse = torch.empty((T, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        nbytes = int(lib.wq_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx))
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = lib.wq_kv4_attention(_p(q), qs, T, q_heads, kv_heads, head_dim, _p(seq_start), _p(ctx_len), B, max_q, max_ctx,
+                              _p(page_table), max_pages, _p(cache), num_pages, page_tokens,
+                              head_dim ** -0.5 if scale is None else scale, window, _p(out), _p(lse), _p(workspace),
+                              wbytes, _stream(q))
+    _check("wq_kv4_attention", rc)
+    return (out, lse) if return_lse else out
 
 
 def auto_kernel(M, N, K) -> str:

@@ -1,0 +1,747 @@
+// Causal attention over the 4-bit key/value cache, for gfx950.
+//
+// For a new token at position p of its sequence and a query head with query vector q,
+// over the tokens t <= p (and t > p - window), with the cache's k_t ~ (a_t - y_t) s_t and
+// v_t ~ (c_t - z_t) u_t (4-bit codes a, c, integer zero-points y, z, scales s, u):
+//   x_t = scale q . k_t = scale s_t (q . a_t - y_t sum(q)),
+//   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(x_t - r),
+// in one pass over the tokens, r a running reference of the row. A row that sees no
+// token gives 0 (and -inf for log sum exp).
+//
+// Both products run on matrix cores in fp16 with fp32 sums, transposed: keys . queries^T
+// gives a lane several tokens' scores of one query row, and those are, as they stand,
+// the lane's operand of values^T . weights^T, so the weights never leave registers and a
+// row's statistics are one lane's scalars. The codes enter the products exactly, less
+// their zero-points (as fp16 subnormals, which matrix cores keep, the codes themselves
+// need half the unpacking, but their sums then carry 2^-18 of the largest term instead of
+// 2^-24, and the zero-points come off as differences of large sums: measured, 1e-4 in a
+// score of 50); the one rounding is that of w_t u_t to fp16 (an operand of the second product). Scores,
+// maxima, sums and outputs are fp32.
+//
+// The reference r keeps the fp16 operands in range and precise: weights times value
+// scales, 2^(x - r) u, are held near 2^10 at the row's largest, at most 2^14. It only
+// moves (and everything summed so far is only rescaled) when a tile's scores or value
+// scales would pass that bound, which any lane can see without asking the others.
+//
+//  kv4_decode_kernel   few query rows (16 or 32 a block): one block per sequence, head and
+//    chunk of the cache, whose four waves take its tiles of 32 tokens in turn, straight
+//    from memory into registers, and join through LDS at the end.
+//  kv4_tile_kernel     many query rows: 128 a block; a tile of codes is turned into exact
+//    fp16 integers once, in LDS, for all of them.
+//  kv4_combine_kernel  joins the chunks of a row where a sequence was split.
+#include "kv4.h"
+#include "wq_launch.h"
+
+namespace wq {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNoRef = -1e30f;      // reference of a row that has seen nothing
+constexpr float kTop = 10.0f;         // log2 of the largest weight times value scale after a move of r,
+constexpr float kSlack = 4.0f;        // and how far it may grow before the next
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kDecodeRows = 16;       // query rows of one column tile
+constexpr int kTileRows = 128;        // query rows of a block of kv4_tile_kernel
+
+struct AttnArgs {
+  const f16* q;
+  int64_t q_stride;
+  const uint8_t* cache;
+  f16* out;
+  float* lse;        // may be null
+  float* part_o;     // [slots][nsplit][D]
+  float2* part_s;    // [slots][nsplit]: r, sum
+  float* tpart_o;    // the same for the tile kernel
+  float2* tpart_s;
+  int hq, group;     // query heads, and those of one key/value head
+  int window;        // 0: none
+  float c;           // scale * log2(e)
+  int nsplit, chunk_tiles;    // of the decode kernel
+  int tnsplit, tchunk_tiles;  // of the tile kernel
+  int decode_rows;            // rows a block of the decode kernel takes (16 or 32)
+  int row_limit;     // sequences with more rows of a head belong to the tile kernel
+  int compact;       // partials of the decode kernel by (sequence, head, row): see decode_slot
+};
+
+// Tiles [t0, t1) of a sequence that rows row0 .. row1 (of one head group) can see, and
+// how they are split.
+struct TileRange {
+  int t0, t1, chunk, splits;
+};
+__device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& p, int row0, int row1, int nsplit,
+                                                int chunk_tiles) {
+  const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
+  const int lo = p.window > 0 ? max(p0 - p.window + 1, 0) : 0;
+  TileRange r;
+  r.t0 = lo / kKvTile;
+  r.t1 = p1 < lo ? r.t0 : p1 / kKvTile + 1;
+  const int n = r.t1 - r.t0;
+  r.chunk = max(chunk_tiles, (n + nsplit - 1) / nsplit);
+  r.splits = (n + r.chunk - 1) / r.chunk;
+  return r;
+}
+
+// Row of the decode kernel's partials. Where the tile kernel runs too, only sequences with
+// few rows come here, and the partials are laid out by sequence; else by token.
+__device__ __forceinline__ int64_t decode_slot(const KvCache& a, const AttnArgs& p, const KvSeq& s, int b, int h,
+                                               int row) {
+  if (p.compact) return ((int64_t)b * a.hkv + h) * p.row_limit + row;
+  return (int64_t)(s.first_row + row / p.group) * p.hq + h * p.group + row % p.group;
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// largest of eight positive fp16 values, as bits (positive fp16 order like integers)
+__device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
+  const uint4 d = __builtin_bit_cast(uint4, v);
+  const u16x2 a = __builtin_elementwise_max(__builtin_bit_cast(u16x2, d.x), __builtin_bit_cast(u16x2, d.y));
+  const u16x2 b = __builtin_elementwise_max(__builtin_bit_cast(u16x2, d.z), __builtin_bit_cast(u16x2, d.w));
+  const u16x2 m = __builtin_elementwise_max(a, b);
+  return max((uint32_t)m.x, (uint32_t)m.y);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(256)
+kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
+  constexpr int KW = D / 32;   // steps of the first product
+  constexpr int CT = D / 16;   // channel tiles of the second
+  constexpr int RUNS = D / 64; // 16-byte runs a lane loads of keys, and of values
+  constexpr int ROWS = kDecodeRows * NT;
+  __shared__ __align__(16) float merged[4][kDecodeRows][D + 4];
+  __shared__ float ref_s[4][kDecodeRows], sum_s[4][kDecodeRows];
+  const int b = blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;
+  const int h = blockIdx.y / row_tiles;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const KvSeq s = kv_sequence(a, b);
+  const int rows = s.rows * p.group;
+  if (rows > p.row_limit) return;
+  for (int rt = blockIdx.y % row_tiles; rt * ROWS < rows; rt += row_tiles) {
+    const int row0 = rt * ROWS, row1 = min(rows, row0 + ROWS) - 1;
+    const TileRange range = tile_range(s, p, row0, row1, p.nsplit, p.chunk_tiles);
+    if (split > 0 && split >= range.splits) continue;
+    const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
+
+    // the lane's query rows: operands of the first product, and position
+    f16x8 qf[NT][KW];
+    int pos[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row0 + kDecodeRows * n + c;
+      const bool valid = row < rows;
+      const int tok = valid ? row / p.group : 0;
+      const int head = h * p.group + (valid ? row - tok * p.group : 0);
+      pos[n] = valid ? s.ctx - s.rows + tok : -1;
+      const f16* qp = p.q + (int64_t)(s.first_row + tok) * p.q_stride + head * D + (D / 4) * g;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint4 d = *reinterpret_cast<const uint4*>(qp + 8 * w);
+        if (!valid) d = uint4{0, 0, 0, 0};
+        qf[n][w] = as_f16x8(perm_x8(d));
+      }
+    }
+    const uint32_t magic = magic_1024x2();
+
+    f32x4 acc[NT][CT];
+    float ref[NT], sum[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      ref[n] = kNoRef;
+      sum[n] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < CT; ++t) acc[n][t] = f32x4{};
+    }
+    float vexp = 0.0f;          // value scales seen are at most 2^vexp, the fp16 with bits vbits
+    uint32_t vbits = 0;
+
+    const int begin = range.t0 + split * range.chunk, end = min(range.t1, begin + range.chunk);
+    int tile = begin + wave;
+    int page = tile / a.page_tiles, in_page = tile - page * a.page_tiles;
+    struct Data {
+      uint4 k[RUNS], v[RUNS], ks, vs, vz;
+      uint32_t kz;
+    };
+    Data cur, next;
+    const auto load = [&](Data& d) {
+      const uint8_t* base = p.cache + kv_page_offset(a, b, h, page) + (int64_t)in_page * kv_tile_bytes<D>();
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) {
+        d.k[i] = *reinterpret_cast<const uint4*>(base + kv_key_offset<D>() + 1024 * i + 16 * lane);
+        d.v[i] = *reinterpret_cast<const uint4*>(base + kv_value_offset<D>() + 1024 * i + 16 * lane);
+      }
+      d.ks = *reinterpret_cast<const uint4*>(base + kv_meta_offset<D>(0) + 16 * g);
+      d.kz = *reinterpret_cast<const uint32_t*>(base + kv_meta_offset<D>(1) + 4 * c);
+      d.vs = *reinterpret_cast<const uint4*>(base + kv_meta_offset<D>(2) + 16 * g);
+      d.vz = *reinterpret_cast<const uint4*>(base + kv_meta_offset<D>(3) + 16 * g);
+    };
+    const auto advance = [&]() {
+      in_page += 4;
+      while (in_page >= a.page_tiles) {
+        in_page -= a.page_tiles;
+        ++page;
+      }
+    };
+    if (tile < end) load(cur);
+    for (; tile < end; tile += 4) {
+      advance();
+      if (tile + 4 < end) load(next);
+
+      // scores: lane's tokens 4 g + i + 16 half of the tile at index i + 4 half
+      const f16x8 ks = as_f16x8(cur.ks);
+      const KeyZeros kz = kv_key_zeros(cur.kz);
+      f16x8 vs = as_f16x8(cur.vs);
+      uint4 vz = cur.vz;
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(&cur.k[0]);
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(&cur.v[0]);
+      float x[NT][8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        f32x4 sc[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n] = f32x4{};
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const f16x8 k = as_f16x8(codes_minus_zero_x16(kw[KW * half + w], magic, kz.bias[half], kz.nbias16[half]));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sc[n] = mfma_16x16x32(k, qf[n][w], sc[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[n][i + 4 * half] = sc[n][i] * (float)ks[i + 4 * half];
+      }
+
+      const int first = tile * kKvTile;
+      const bool edge = first + kKvTile - 1 > p0 || (p.window > 0 && first <= p1 - p.window);
+      uint32_t seen[NT];
+      if (edge) {
+        // tokens past a row's own, before its window or past the cache's end: whatever
+        // stands there, codes, scales or zero-points, has no part in the row
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          seen[n] = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int t = first + 4 * g + (e & 3) + 16 * (e >> 2);
+            const bool see = t <= pos[n] && (p.window == 0 || t > pos[n] - p.window);
+            x[n][e] = see ? x[n][e] : -INFINITY;
+            seen[n] |= see ? 1u << e : 0u;
+          }
+        }
+        uint32_t any = seen[0];
+#pragma unroll
+        for (int n = 1; n < NT; ++n) any |= seen[n];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vs[e] = (any >> e) & 1u ? vs[e] : (f16)0.0f;
+        vz = kv_value_zeros_finite(vz);
+      }
+
+      float mx[NT];
+      const uint32_t vmax = max_bits8(vs);
+      bool move = vmax > vbits;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mx[n] = x[n][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) mx[n] = fmaxf(mx[n], x[n][e]);
+        mx[n] *= p.c;
+        move |= mx[n] + vexp - kTop > ref[n] + kSlack;
+      }
+      if (__any(move)) {
+        uint32_t top = vmax;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+        float grown = 0.0f;
+        if (top > vbits) {
+          // the next power of two: exponent field + 1, mantissa 0 (scales are normal fp16)
+          const float ve = (float)((int)(top >> 10) + 1 - 15);
+          grown = vbits == 0 ? 0.0f : ve - vexp;
+          vexp = ve;
+          vbits = ((top >> 10) << 10) | 0x3FFu;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float m = mx[n];
+          m = fmaxf(m, __shfl_xor(m, 16));
+          m = fmaxf(m, __shfl_xor(m, 32));
+          const float to = fmaxf(ref[n] + grown, m + vexp - kTop);
+          const float f = exp2_hw(ref[n] - to);
+          ref[n] = to;
+          sum[n] *= f;
+#pragma unroll
+          for (int t = 0; t < CT; ++t) acc[n][t] *= f;
+        }
+      }
+
+      // weights, and weights times value scales as the operand of the second product
+      f16x8 wf[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = exp2_hw(__builtin_fmaf(x[n][e], p.c, -ref[n]));
+          sum[n] += w;
+          wf[n][2 * (e & 3) + (e >> 2)] = (f16)(w * (float)vs[e]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        const f16x8 v = kv_value_operand(vw[t], magic, vz);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][t] = mfma_16x16x32(v, wf[n], acc[n][t]);
+      }
+      cur = next;
+    }
+
+    // join the four waves
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float su = sum[n];
+      su += __shfl_xor(su, 16);
+      su += __shfl_xor(su, 32);
+      __syncthreads();  // the previous column tile has been read
+      if (g == 0) {
+        ref_s[wave][c] = ref[n];
+        sum_s[wave][c] = su;
+      }
+      __syncthreads();
+      float top = ref_s[0][c];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) top = fmaxf(top, ref_s[w][c]);
+      const float f = exp2_hw(ref[n] - top);
+#pragma unroll
+      for (int t = 0; t < CT; ++t) *reinterpret_cast<f32x4*>(&merged[wave][c][16 * t + 4 * g]) = acc[n][t] * f;
+      __syncthreads();
+      // 16 threads a row, D / 16 channels each
+      const int r = threadIdx.x >> 4, part = threadIdx.x & 15;
+      const int row = row0 + kDecodeRows * n + r;
+      if (row < rows) {
+        float best = ref_s[0][r];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) best = fmaxf(best, ref_s[w][r]);
+        float total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) total = __builtin_fmaf(sum_s[w][r], exp2_hw(ref_s[w][r] - best), total);
+        float o[CT];
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+          o[i] = (merged[0][r][CT * part + i] + merged[1][r][CT * part + i]) +
+                 (merged[2][r][CT * part + i] + merged[3][r][CT * part + i]);
+        if (range.splits > 1) {
+          const int64_t at = decode_slot(a, p, s, b, h, row) * p.nsplit + split;
+          float* dst = p.part_o + at * D + CT * part;
+#pragma unroll
+          for (int i = 0; i < CT; i += 4) *reinterpret_cast<f32x4*>(dst + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+          if (part == 0) p.part_s[at] = make_float2(best, total);
+        } else {
+          const int tok = row / p.group;
+          const int64_t at = (int64_t)(s.first_row + tok) * p.hq + h * p.group + (row - tok * p.group);
+          const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+          f16* dst = p.out + at * D + CT * part;
+#pragma unroll
+          for (int i = 0; i < CT; i += 4) {
+            typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<f16x4*>(dst + i) =
+                f16x4{(f16)(o[i] * inv), (f16)(o[i + 1] * inv), (f16)(o[i + 2] * inv), (f16)(o[i + 3] * inv)};
+          }
+          if (part == 0 && p.lse != nullptr) p.lse[at] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256)
+kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
+  constexpr int KS = D / 16;   // steps of the first product
+  constexpr int CT = D / 32;   // channel tiles of the second
+  constexpr int RUNS = D / 64;
+  // two tiles of 32 tokens: keys [step][lane], values [step][channel tile][lane], 16
+  // bytes each, and the tiles' scales
+  __shared__ __align__(16) uint4 kl[2][KS][64], vl[2][2][CT][64];
+  __shared__ __align__(16) uint4 ksl[2][4], vsl[2][4];
+  const int lane = threadIdx.x & 63, c = lane & 31, hl = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.y;
+  const int split = blockIdx.x % p.tnsplit;
+  const int rest = blockIdx.x / p.tnsplit;
+  const int b = rest / row_tiles;
+  const KvSeq s = kv_sequence(a, b);
+  const int rows = s.rows * p.group;
+  if (rows <= p.row_limit) return;
+  const int have = (rows + kTileRows - 1) / kTileRows;
+  // the last rows see the most tokens: they start first
+  for (int back = rest % row_tiles; back < have; back += row_tiles) {
+    const int rt = have - 1 - back;
+    const int row0 = rt * kTileRows, row1 = min(rows, row0 + kTileRows) - 1;
+    const TileRange range = tile_range(s, p, row0, row1, p.tnsplit, p.tchunk_tiles);
+    if (split > 0 && split >= range.splits) continue;
+    const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
+    const int row = row0 + 32 * wave + c;
+    const bool valid = row < rows;
+    const int tok = valid ? row / p.group : 0;
+    const int head = h * p.group + (valid ? row - tok * p.group : 0);
+    const int pos = valid ? s.ctx - s.rows + tok : -1;
+    f16x8 qf[KS];
+    const f16* qp = p.q + (int64_t)(s.first_row + tok) * p.q_stride + head * D + 8 * hl;
+#pragma unroll
+    for (int w = 0; w < KS; ++w) {
+      uint4 d = *reinterpret_cast<const uint4*>(qp + 16 * w);
+      if (!valid) d = uint4{0, 0, 0, 0};
+      qf[w] = as_f16x8(perm_x8(d));
+    }
+    f32x16 acc[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) acc[t] = f32x16{};
+    float ref = kNoRef, sum = 0.0f, vexp = 0.0f;
+    uint32_t vbits = 0;
+
+    const int begin = range.t0 + split * range.chunk, end = min(range.t1, begin + range.chunk);
+    // each wave turns one tile's keys or values into LDS operands: waves 0, 1 the first
+    // tile's, waves 2, 3 the second's
+    const int sub = wave >> 1;
+    const bool is_v = wave & 1;
+    const int g = lane >> 4, c16 = lane & 15;
+    uint4 data[RUNS], scales, zeros;
+    const auto load = [&](int tile) {
+      tile = min(tile, end - 1);  // past the range: loaded again, and masked by position
+      const int page = tile / a.page_tiles;
+      const uint8_t* base = p.cache + kv_page_offset(a, b, h, page) +
+                            (int64_t)(tile - page * a.page_tiles) * kv_tile_bytes<D>();
+      const int off = is_v ? kv_value_offset<D>() : kv_key_offset<D>();
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) data[i] = *reinterpret_cast<const uint4*>(base + off + 1024 * i + 16 * lane);
+      const uint8_t* meta = base + kv_meta_offset<D>(is_v ? 2 : 0);
+      scales = *reinterpret_cast<const uint4*>(meta + 16 * (lane & 3));
+      if (is_v)
+        zeros = *reinterpret_cast<const uint4*>(meta + 64 + 16 * g);
+      else
+        zeros.x = *reinterpret_cast<const uint32_t*>(meta + 64 + 4 * c16);
+    };
+    const uint32_t magic = magic_1024x2();
+    const auto stash = [&]() {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&data[0]);
+      if (!is_v) {
+        const KeyZeros kz = kv_key_zeros(zeros.x);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const int block = (D / 32) * g + i;  // eight channels
+            kl[sub][block >> 1][32 * (block & 1) + 16 * half + c16] =
+                codes_minus_zero_x16(w[(D / 32) * half + i], magic, kz.bias[half], kz.nbias16[half]);
+          }
+        if (lane < 4) ksl[sub][lane] = scales;
+      } else {
+        // what stands past the cache's end may be anything; its weight is 0
+        zeros = kv_value_zeros_finite(zeros);
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+          vl[sub][g >> 1][t >> 1][32 * (g & 1) + 16 * (t & 1) + c16] =
+              __builtin_bit_cast(uint4, kv_value_operand(w[t], magic, zeros));
+        if (lane < 4) vsl[sub][lane] = scales;
+      }
+    };
+
+    if (begin < end) load(begin + sub);
+    for (int tile = begin; tile < end; tile += 2) {
+      __syncthreads();  // the previous tiles have been read
+      stash();
+      __syncthreads();
+      if (tile + 2 < end) load(tile + 2 + sub);
+
+      f32x16 sc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        sc[u] = f32x16{};
+#pragma unroll
+        for (int w = 0; w < KS; ++w)
+          sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16x8(kl[u][w][lane]), qf[w], sc[u], 0, 0, 0);
+      }
+      // the lane's tokens: 8 q + 4 hl + i of a tile in register 4 q + i; quads q and
+      // q + 2 (q = 0, 1) are one run of scales
+      f16x8 vs[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const f16x8 ks = as_f16x8(ksl[u][2 * q + hl]);
+          vs[u][q] = as_f16x8(vsl[u][2 * q + hl]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)] *= (float)ks[e];
+        }
+      const int first = tile * kKvTile;
+      const bool edge = first + 2 * kKvTile - 1 > p0 || (p.window > 0 && first <= p1 - p.window) || tile + 1 >= end;
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int t = first + 32 * u + 8 * (e >> 2) + 4 * hl + (e & 3);
+            const bool see = t <= pos && (p.window == 0 || t > pos - p.window) && tile + u < end;
+            sc[u][e] = see ? sc[u][e] : -INFINITY;
+          }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              vs[u][q][e] = sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)] == -INFINITY ? (f16)0.0f : vs[u][q][e];
+      }
+      float mx = -INFINITY;
+      uint32_t vmax = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[u][e]);
+        vmax = max(vmax, max(max_bits8(vs[u][0]), max_bits8(vs[u][1])));
+      }
+      mx *= p.c;
+      if (__any(vmax > vbits || mx + vexp - kTop > ref + kSlack)) {
+        uint32_t top = vmax;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+        float grown = 0.0f;
+        if (top > vbits) {
+          const float ve = (float)((int)(top >> 10) + 1 - 15);
+          grown = vbits == 0 ? 0.0f : ve - vexp;
+          vexp = ve;
+          vbits = ((top >> 10) << 10) | 0x3FFu;
+        }
+        const float m = fmaxf(mx, __shfl_xor(mx, 32));
+        const float to = fmaxf(ref + grown, m + vexp - kTop);
+        const float f = exp2_hw(ref - to);
+        ref = to;
+        sum *= f;
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[t] *= f;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          f16x8 wf;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w = exp2_hw(__builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], p.c, -ref));
+            sum += w;
+            wf[2 * (e & 3) + (e >> 2)] = (f16)(w * (float)vs[u][q][e]);
+          }
+#pragma unroll
+          for (int t = 0; t < CT; ++t)
+            acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16x8(vl[u][q][t][lane]), wf, acc[t], 0, 0, 0);
+        }
+    }
+    sum += __shfl_xor(sum, 32);
+    if (valid) {
+      const int64_t slot = (int64_t)(s.first_row + tok) * p.hq + head;
+      if (range.splits > 1) {
+        const int64_t at = slot * p.tnsplit + split;
+        float* dst = p.tpart_o + at * D + 4 * hl;
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(dst + 32 * t + 8 * q) =
+                f32x4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]};
+        if (hl == 0) p.tpart_s[at] = make_float2(ref, sum);
+      } else {
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        f16* dst = p.out + slot * D + 4 * hl;
+        typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f16x4*>(dst + 32 * t + 8 * q) =
+                f16x4{(f16)(acc[t][4 * q] * inv), (f16)(acc[t][4 * q + 1] * inv), (f16)(acc[t][4 * q + 2] * inv),
+                      (f16)(acc[t][4 * q + 3] * inv)};
+        if (hl == 0 && p.lse != nullptr) p.lse[slot] = sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+}
+
+// One wave per row of the output; the rows of unsplit sequences are already written.
+template <int D>
+__global__ void __launch_bounds__(256)
+kv4_combine_kernel(KvCache a, AttnArgs p) {
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= (int64_t)a.T * p.hq) return;
+  const int lane = threadIdx.x & 63;
+  const int token = (int)(at / p.hq), head = (int)(at % p.hq);
+  // the token's sequence: the last one that starts at or before it
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.seq_start[mid] <= token)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const KvSeq s = kv_sequence(a, lo);
+  const int tok = token - s.first_row;
+  if (tok < 0 || tok >= s.rows) return;
+  const int h = head / p.group, row = tok * p.group + head % p.group, rows = s.rows * p.group;
+  const bool tiled = rows > p.row_limit;
+  const int block = tiled ? kTileRows : p.decode_rows;
+  const int row0 = row / block * block, row1 = min(rows, row0 + block) - 1;
+  const int nsplit = tiled ? p.tnsplit : p.nsplit;
+  const TileRange range = tile_range(s, p, row0, row1, nsplit, tiled ? p.tchunk_tiles : p.chunk_tiles);
+  if (range.splits <= 1) return;
+  const int64_t slot = (tiled ? at : decode_slot(a, p, s, lo, h, row)) * nsplit;
+  const float2* st = (tiled ? p.tpart_s : p.part_s) + slot;
+  const float* po = (tiled ? p.tpart_o : p.part_o) + slot * D;
+  float best = kNoRef;
+  for (int i = 0; i < range.splits; ++i) best = fmaxf(best, st[i].x);
+  constexpr int N = D / 64;  // channels of a lane
+  float total = 0.0f, o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = 0.0f;
+  for (int i = 0; i < range.splits; ++i) {
+    const float f = exp2_hw(st[i].x - best);
+    total = __builtin_fmaf(st[i].y, f, total);
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(po[(int64_t)i * D + N * lane + e], f, o[e]);
+  }
+  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) p.out[at * D + N * lane + e] = (f16)(o[e] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[at] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
+}
+
+namespace {
+
+constexpr int64_t kCus = 256;
+
+struct Plan {
+  bool decode, tile;    // which kernels run
+  int nt;               // column tiles of the decode kernel
+  int row_limit, row_tiles, trow_tiles;
+  int nsplit, chunk, tnsplit, tchunk;
+  int64_t slots, tslots;      // rows of the partials, each nsplit times; 0: not split
+  int64_t most, tmost;        // bounds of nsplit and tnsplit
+};
+
+int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+// Splits of `tiles` tiles so that `blocks` blocks become about `want`, each of at least
+// `least` tiles.
+// Returns the splits' bound, which never falls as `tiles` grows (a workspace sized for
+// longer sequences holds the partials of shorter ones).
+int64_t split_plan(int64_t tiles, int64_t blocks, int64_t want, int64_t least, int* nsplit, int* chunk) {
+  int64_t n = ceil_div(want, blocks);
+  const int64_t most = ceil_div(tiles, least);
+  n = n > most ? most : n;
+  *chunk = (int)ceil_div(tiles, n);
+  *nsplit = (int)ceil_div(tiles, *chunk);
+  return n;
+}
+
+Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int64_t max_ctx, int64_t window) {
+  Plan p = {};
+  const int64_t group = hq / hkv;
+  const int64_t q = max_q < 1 ? 1 : (max_q > T ? T : max_q);
+  const int64_t rows = q * group;
+  constexpr int64_t kLimit = 2 * kDecodeRows;
+  // a sequence's rows decide its kernel; from the host only the largest is known, and
+  // that all are alike where there is one sequence or B max_q new tokens
+  p.tile = rows > kLimit;
+  p.decode = !p.tile || (B > 1 && B * q > T);
+  p.row_limit = p.tile ? (p.decode ? (int)kLimit : 0) : 0x7FFFFFFF;
+  const int64_t drows = p.tile ? kLimit : rows;
+  p.nt = drows <= kDecodeRows ? 1 : 2;
+  p.row_tiles = (int)ceil_div(drows, kDecodeRows * p.nt);
+  if (p.row_tiles * hkv > 65535) p.row_tiles = (int)(65535 / hkv);
+  int64_t tiles = ceil_div(max_ctx < 1 ? 1 : max_ctx, kKvTile);
+  if (window > 0) {  // q rows see up to window + q - 1 tokens, which may begin inside a tile
+    const int64_t in_window = ceil_div(window + q - 1, kKvTile) + 1;
+    tiles = in_window < tiles ? in_window : tiles;
+  }
+  p.nsplit = p.tnsplit = 1;
+  p.chunk = p.tchunk = (int)tiles;
+  if (p.decode) {
+    p.most = split_plan(tiles, B * hkv * p.row_tiles, 4 * kCus, 8, &p.nsplit, &p.chunk);
+    if (p.most > 1) p.slots = p.tile ? B * hkv * kLimit : T * hq;
+  }
+  if (p.tile) {
+    const int64_t blocks = B * hkv * ceil_div(rows, kTileRows);
+    p.tmost = split_plan(tiles, blocks, 2 * kCus, 16, &p.tnsplit, &p.tchunk);
+    if (p.tmost > 1) p.tslots = T * hq;
+    const int64_t grid = 0x7FFFFFFF / (B * p.tnsplit);
+    p.trow_tiles = (int)(ceil_div(rows, kTileRows) < grid ? ceil_div(rows, kTileRows) : grid);
+  }
+  return p;
+}
+
+size_t part_bytes(int64_t slots, int64_t nsplit, int64_t D) { return (size_t)slots * nsplit * (D * 4 + 8); }
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+template <int D>
+hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, int64_t hkv, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (pl.tile) {
+    const dim3 grid((unsigned)(B * pl.trow_tiles * pl.tnsplit), (unsigned)hkv);
+    hipLaunchKernelGGL((kv4_tile_kernel<D>), grid, dim3(256), 0, stream, a, p, pl.trow_tiles);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && pl.decode) {
+    const dim3 grid((unsigned)(B * pl.nsplit), (unsigned)(hkv * pl.row_tiles));
+    if (pl.nt == 1)
+      hipLaunchKernelGGL((kv4_decode_kernel<D, 1>), grid, dim3(256), 0, stream, a, p, pl.row_tiles);
+    else
+      hipLaunchKernelGGL((kv4_decode_kernel<D, 2>), grid, dim3(256), 0, stream, a, p, pl.row_tiles);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && (pl.nsplit > 1 || pl.tnsplit > 1)) {
+    const dim3 grid((unsigned)(((int64_t)a.T * p.hq + 3) / 4));
+    hipLaunchKernelGGL((kv4_combine_kernel<D>), grid, dim3(256), 0, stream, a, p);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q,
+                                     int64_t max_ctx) {
+  const Plan pl = make_plan(T, B, hq, hkv, max_q, max_ctx, 0);
+  return round256(part_bytes(pl.slots, pl.most, head_dim)) + round256(part_bytes(pl.tslots, pl.tmost, head_dim));
+}
+
+hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
+                                int64_t max_q, int64_t max_ctx, int64_t window, float scale, const void* cache,
+                                const Kv4View& c, uint16_t* out, float* lse, void* workspace, hipStream_t stream) {
+  const Plan pl = make_plan(T, c.B, hq, c.kv_heads, max_q, max_ctx, window);
+  const KvCache a = kv4_cache_args(c, T, head_dim);
+  AttnArgs p = {};
+  p.q = reinterpret_cast<const f16*>(q);
+  p.q_stride = q_stride;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.out = reinterpret_cast<f16*>(out);
+  p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_s = reinterpret_cast<float2*>(ws + (size_t)pl.slots * pl.nsplit * head_dim * 4);
+  ws += round256(part_bytes(pl.slots, pl.most, head_dim));
+  p.tpart_o = reinterpret_cast<float*>(ws);
+  p.tpart_s = reinterpret_cast<float2*>(ws + (size_t)pl.tslots * pl.tnsplit * head_dim * 4);
+  p.hq = (int)hq;
+  p.group = (int)(hq / c.kv_heads);
+  p.window = (int)window;
+  p.c = scale * 1.44269504088896341f;
+  p.nsplit = pl.nsplit;
+  p.chunk_tiles = pl.chunk;
+  p.tnsplit = pl.tnsplit;
+  p.tchunk_tiles = pl.tchunk;
+  p.decode_rows = kDecodeRows * pl.nt;
+  p.row_limit = pl.row_limit;
+  p.compact = pl.tile;
+  return head_dim == 128 ? run<128>(a, p, pl, c.B, c.kv_heads, stream) : run<64>(a, p, pl, c.B, c.kv_heads, stream);
+}
+
+}  // namespace wq

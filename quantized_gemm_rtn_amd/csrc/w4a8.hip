@@ -322,24 +322,16 @@ hipError_t launch_act_int8(const uint16_t* x, int64_t M, int64_t K, const int32_
   return hipGetLastError();
 }
 
-hipError_t launch_w4a8(const uint16_t* x, int64_t M, int64_t K, const int32_t* outliers, int64_t n_out,
-                       const uint32_t* packed, const uint16_t* scales, const uint16_t* zeros, int64_t N, void* y,
-                       int y_f32, void* workspace, hipStream_t stream) {
-  const auto r256 = [](size_t b) { return (b + 255) / 256 * 256; };
-  char* ws = static_cast<char*>(workspace);
-  int8_t* xq = reinterpret_cast<int8_t*>(ws);
-  float* sx = reinterpret_cast<float*>(ws + r256((size_t)M * K));
-  uint16_t* xo = reinterpret_cast<uint16_t*>(ws + r256((size_t)M * K) + r256((size_t)M * 4));
-  uint16_t* wo = reinterpret_cast<uint16_t*>(ws + r256((size_t)M * K) + r256((size_t)M * 4) +
-                                             r256((size_t)M * kMaxOutliers * 2));
-  hipError_t e = launch_act_int8(x, M, K, outliers, n_out, xq, sx, xo, stream);
-  if (e != hipSuccess) return e;
+hipError_t launch_w4a8_product(const int8_t* xq, const float* sx, const uint16_t* xo, int64_t M, int64_t K,
+                               const int32_t* outliers, int64_t n_out, const uint32_t* packed, const uint16_t* scales,
+                               const uint16_t* zeros, int64_t N, void* y, int y_f32, uint16_t* wo,
+                               hipStream_t stream) {
   int64_t wblocks = (N * kMaxOutliers + 255) / 256;
   wblocks = wblocks > 65536 ? 65536 : wblocks;
   hipLaunchKernelGGL(outlier_weights_kernel, dim3((unsigned)wblocks), dim3(256), 0, stream, packed,
                      reinterpret_cast<const f16*>(scales), reinterpret_cast<const f16*>(zeros), N, (int)K, outliers,
                      (int)n_out, reinterpret_cast<f16*>(wo));
-  e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr int64_t kRowsPerLaunch = 65535 * 128;  // gridDim.y limit
   const size_t ysz = y_f32 ? 4 : 2;
@@ -354,6 +346,21 @@ hipError_t launch_w4a8(const uint16_t* x, int64_t M, int64_t K, const int32_t* o
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+hipError_t launch_w4a8(const uint16_t* x, int64_t M, int64_t K, const int32_t* outliers, int64_t n_out,
+                       const uint32_t* packed, const uint16_t* scales, const uint16_t* zeros, int64_t N, void* y,
+                       int y_f32, void* workspace, hipStream_t stream) {
+  const auto r256 = [](size_t b) { return (b + 255) / 256 * 256; };
+  char* ws = static_cast<char*>(workspace);
+  int8_t* xq = reinterpret_cast<int8_t*>(ws);
+  float* sx = reinterpret_cast<float*>(ws + r256((size_t)M * K));
+  uint16_t* xo = reinterpret_cast<uint16_t*>(ws + r256((size_t)M * K) + r256((size_t)M * 4));
+  uint16_t* wo = reinterpret_cast<uint16_t*>(ws + r256((size_t)M * K) + r256((size_t)M * 4) +
+                                             r256((size_t)M * kMaxOutliers * 2));
+  hipError_t e = launch_act_int8(x, M, K, outliers, n_out, xq, sx, xo, stream);
+  if (e != hipSuccess) return e;
+  return launch_w4a8_product(xq, sx, xo, M, K, outliers, n_out, packed, scales, zeros, N, y, y_f32, wo, stream);
 }
 
 }  // namespace wq

@@ -116,6 +116,43 @@ int check_quantize_args(const float* W, int64_t N, int64_t K, int32_t group, int
 // the permuted copy of W or x at the start of an act-order workspace
 size_t act_order_copy_bytes(int64_t rows, int64_t K, size_t elem) { return ((size_t)rows * K * elem + 255) / 256 * 256; }
 
+constexpr int64_t kKvTile = 32;                // tokens of a cache tile: pages hold whole tiles
+constexpr int64_t kMaxBatch = (int64_t)1 << 20;
+constexpr int64_t kMaxContext = (int64_t)1 << 30;
+constexpr int64_t kMaxHeads = 65535;           // heads are a grid dimension
+
+int check_norm_args(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                    float eps, const uint16_t* h) {
+  if (!weight || (M != 0 && !x)) return WQ_ERR_NULL;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return WQ_ERR_UNSUPPORTED;
+  if (M < 0 || K < 16 || K % 16 != 0 || K >= kMax32 || M >= kMax32 / K) return WQ_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16)) return WQ_ERR_ALIGN;
+  return WQ_OK;
+}
+
+int check_outliers(const int32_t* outliers, int64_t n_out) {
+  if (n_out > 0 && !outliers) return WQ_ERR_NULL;
+  if (n_out < 0 || n_out > kMaxOutliers) return WQ_ERR_UNSUPPORTED;
+  return aligned(outliers, 4) ? WQ_OK : WQ_ERR_ALIGN;
+}
+
+bool kv4_format(int64_t page_tokens, int64_t head_dim) {
+  return (head_dim == 64 || head_dim == 128) && page_tokens > 0 && page_tokens % kKvTile == 0;
+}
+
+// the arguments the cache's entry points share; heads: of the widest token-wise array
+int check_kv4_args(int64_t T, int64_t heads, const wq::Kv4View& c, int64_t head_dim, const void* cache) {
+  if (T != 0 && c.B != 0 && (!cache || !c.seq_start || !c.ctx_len || !c.page_table)) return WQ_ERR_NULL;
+  if (!kv4_format(c.page_tokens, head_dim)) return WQ_ERR_UNSUPPORTED;
+  if (T < 0 || c.B < 0 || c.B > kMaxBatch || c.kv_heads < 1 || c.kv_heads > kMaxHeads || heads < c.kv_heads ||
+      heads > kMaxHeads || c.num_pages < 1 || c.num_pages >= kMax32 || c.max_pages < 1 ||
+      c.max_pages > kMaxContext / c.page_tokens || T >= kMax32 / heads)
+    return WQ_ERR_SHAPE;
+  if (!aligned(cache, 16) || !aligned(c.seq_start, 4) || !aligned(c.ctx_len, 4) || !aligned(c.page_table, 4))
+    return WQ_ERR_ALIGN;
+  return WQ_OK;
+}
+
 // (kernel, device) -> the dynamic-LDS limit already set there
 std::mutex lds_mutex;
 std::map<std::pair<const void*, int>, size_t> lds_limit;
@@ -411,6 +448,130 @@ int wq_linear_w4a8(const uint16_t* x, int64_t M, int64_t K, const int32_t* outli
   if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
   return hip_status(wq::launch_w4a8(x, M, K, outliers, n_out, packed, scales, zeros, N, y, y_dtype == WQ_F32,
                                    workspace, as_stream(stream)));
+}
+
+size_t wq_linear_w4a8_quantized_workspace_bytes(int64_t N) {
+  return N < 1 || N >= kMax32 ? 0 : (size_t)N * kMaxOutliers * 2;
+}
+
+int wq_linear_w4a8_quantized(const int8_t* xq, const float* sx, const uint16_t* xo, int64_t M, int64_t K,
+                             const int32_t* outliers, int64_t n_out, const uint32_t* packed, const uint16_t* scales,
+                             const uint16_t* zeros, int64_t N, int32_t group, void* y, int32_t y_dtype,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  // xq stands in for x: the same alignment
+  int rc = check_linear_args(reinterpret_cast<const uint16_t*>(xq), M, K, packed, scales, zeros, N, group, nullptr,
+                             nullptr, nullptr, 0, y, y_dtype, WQ_KERNEL_AUTO);
+  if (rc != WQ_OK) return rc;
+  rc = check_outliers(outliers, n_out);
+  if (rc != WQ_OK) return rc;
+  if (M != 0 && (!sx || !xo)) return WQ_ERR_NULL;
+  if (!aligned(sx, 4) || !aligned(xo, 16)) return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  if (!workspace || workspace_bytes < wq_linear_w4a8_quantized_workspace_bytes(N)) return WQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  return hip_status(wq::launch_w4a8_product(xq, sx, xo, M, K, outliers, n_out, packed, scales, zeros, N, y,
+                                            y_dtype == WQ_F32, static_cast<uint16_t*>(workspace),
+                                            as_stream(stream)));
+}
+
+int wq_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                   float eps, uint16_t* h, uint16_t* y, void* stream) {
+  const int rc = check_norm_args(x, residual, weight, M, K, eps, h);
+  if (rc != WQ_OK) return rc;
+  if (M != 0 && !y) return WQ_ERR_NULL;
+  if (!aligned(y, 16)) return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  return hip_status(wq::launch_add_rmsnorm(x, residual, weight, M, K, eps, nullptr, 0, h, y, nullptr, nullptr,
+                                           nullptr, as_stream(stream)));
+}
+
+int wq_add_rmsnorm_int8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                        float eps, const int32_t* outliers, int64_t n_out, uint16_t* h, int8_t* xq, float* sx,
+                        uint16_t* xo, void* stream) {
+  int rc = check_norm_args(x, residual, weight, M, K, eps, h);
+  if (rc != WQ_OK) return rc;
+  rc = check_outliers(outliers, n_out);
+  if (rc != WQ_OK) return rc;
+  if (M != 0 && (!xq || !sx || !xo)) return WQ_ERR_NULL;
+  if (!aligned(xq, 16) || !aligned(sx, 4) || !aligned(xo, 16)) return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  return hip_status(wq::launch_add_rmsnorm(x, residual, weight, M, K, eps, outliers, n_out, h, nullptr, xq, sx, xo,
+                                           as_stream(stream)));
+}
+
+int wq_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo, const int32_t* outliers,
+                           int64_t n_out, int64_t M, int64_t K, uint16_t* out, void* stream) {
+  const int rc = check_outliers(outliers, n_out);
+  if (rc != WQ_OK) return rc;
+  if (M != 0 && (!xq || !sx || !out || (n_out > 0 && !xo))) return WQ_ERR_NULL;
+  if (M < 0 || K < 16 || K % 16 != 0 || K >= kMax32 || M >= kMax32 / K) return WQ_ERR_SHAPE;
+  if (!aligned(xq, 16) || !aligned(sx, 4) || !aligned(xo, 2) || !aligned(out, 16)) return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  return hip_status(wq::launch_dequantize_act_int8(xq, sx, xo, outliers, n_out, M, K, out, as_stream(stream)));
+}
+
+size_t wq_kv4_page_bytes(int64_t page_tokens, int64_t head_dim) {
+  if (!kv4_format(page_tokens, head_dim) || page_tokens > kMaxContext) return 0;
+  return (size_t)page_tokens * (size_t)(head_dim + 8);
+}
+
+int wq_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t T,
+                  int64_t kv_heads, int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B,
+                  int64_t max_new, const int32_t* page_table, int64_t max_pages, void* cache, int64_t num_pages,
+                  int64_t page_tokens, void* stream) {
+  const wq::Kv4View c{seq_start, ctx_len, page_table, B, max_pages, num_pages, page_tokens, kv_heads};
+  const int rc = check_kv4_args(T, kv_heads, c, head_dim, cache);
+  if (rc != WQ_OK) return rc;
+  if (T != 0 && B != 0 && (!k || !v)) return WQ_ERR_NULL;
+  if (k_stride < kv_heads * head_dim || v_stride < kv_heads * head_dim || max_new < 0) return WQ_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0) return WQ_ERR_ALIGN;
+  if (T == 0 || B == 0) return WQ_OK;
+  return hip_status(wq::launch_kv4_append(k, k_stride, v, v_stride, T, head_dim, max_new, c, cache,
+                                          as_stream(stream)));
+}
+
+int wq_kv4_read(const void* cache, int64_t num_pages, int64_t page_tokens, int64_t T, int64_t kv_heads,
+                int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B, int64_t max_new,
+                const int32_t* page_table, int64_t max_pages, uint16_t* k, uint16_t* v, void* stream) {
+  const wq::Kv4View c{seq_start, ctx_len, page_table, B, max_pages, num_pages, page_tokens, kv_heads};
+  const int rc = check_kv4_args(T, kv_heads, c, head_dim, cache);
+  if (rc != WQ_OK) return rc;
+  if (T != 0 && B != 0 && (!k || !v)) return WQ_ERR_NULL;
+  if (max_new < 0) return WQ_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16)) return WQ_ERR_ALIGN;
+  if (T == 0 || B == 0) return WQ_OK;
+  return hip_status(wq::launch_kv4_read(cache, T, head_dim, max_new, c, k, v, as_stream(stream)));
+}
+
+size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                        int64_t max_q, int64_t max_ctx) {
+  if (T < 1 || B < 1 || B > kMaxBatch || kv_heads < 1 || kv_heads > kMaxHeads || q_heads < kv_heads ||
+      q_heads > kMaxHeads || q_heads % kv_heads != 0 || T >= kMax32 / q_heads || (head_dim != 64 && head_dim != 128))
+    return 0;
+  if (max_q < 0 || max_ctx < 0 || max_ctx > kMaxContext) return 0;
+  return wq::kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx);
+}
+
+int wq_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
+                     int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B, int64_t max_q,
+                     int64_t max_ctx, const int32_t* page_table, int64_t max_pages, const void* cache,
+                     int64_t num_pages, int64_t page_tokens, float scale, int64_t window, uint16_t* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const wq::Kv4View c{seq_start, ctx_len, page_table, B, max_pages, num_pages, page_tokens, kv_heads};
+  const int rc = check_kv4_args(T, q_heads, c, head_dim, cache);
+  if (rc != WQ_OK) return rc;
+  if (T != 0 && B != 0 && (!q || !out)) return WQ_ERR_NULL;
+  if (!(scale > 0.0f) || scale > 3.0e38f) return WQ_ERR_UNSUPPORTED;
+  if (q_heads % kv_heads != 0 || q_stride < q_heads * head_dim || max_q < 0 || max_ctx < 0 || max_ctx > kMaxContext ||
+      window < 0 || window >= kMax32)
+    return WQ_ERR_SHAPE;
+  if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 8) || !aligned(lse, 4)) return WQ_ERR_ALIGN;
+  if (T == 0 || B == 0) return WQ_OK;
+  const size_t need = wq::kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx);
+  if (need != 0 && (!workspace || workspace_bytes < need)) return WQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  return hip_status(wq::launch_kv4_attention(q, q_stride, T, q_heads, head_dim, max_q, max_ctx, window, scale, cache, c,
+                                             out, lse, workspace, as_stream(stream)));
 }
 
 size_t wq_linear_act_order_workspace_bytes(int64_t M, int64_t N, int64_t K) {

@@ -42,6 +42,39 @@ hipError_t launch_w4a8(const uint16_t* x, int64_t M, int64_t K, const int32_t* o
                        const uint32_t* packed, const uint16_t* scales, const uint16_t* zeros, int64_t N, void* y,
                        int y_f32, void* workspace, hipStream_t stream);
 
+// Root-mean-square norm of x + residual (may be null): fp16 output y, or (xq not null) the
+// INT8 output of launch_act_int8 with sx and xo; h (may be null) takes the sum.
+hipError_t launch_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M,
+                              int64_t K, float eps, const int32_t* outliers, int64_t n_out, uint16_t* h, uint16_t* y,
+                              int8_t* xq, float* sx, uint16_t* xo, hipStream_t stream);
+hipError_t launch_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo, const int32_t* outliers,
+                                      int64_t n_out, int64_t M, int64_t K, uint16_t* out, hipStream_t stream);
+// The W4A8 product of activations that are already INT8; wo: [N, 16] fp16 scratch.
+hipError_t launch_w4a8_product(const int8_t* xq, const float* sx, const uint16_t* xo, int64_t M, int64_t K,
+                               const int32_t* outliers, int64_t n_out, const uint32_t* packed, const uint16_t* scales,
+                               const uint16_t* zeros, int64_t N, void* y, int y_f32, uint16_t* wo, hipStream_t stream);
+
+// A batch's view of a 4-bit key/value cache: B sequences, whose new tokens are the rows
+// seq_start[b] .. seq_start[b + 1] - 1 of the token-wise arrays and the last of ctx_len[b].
+struct Kv4View {
+  const int32_t* seq_start;   // [B + 1]
+  const int32_t* ctx_len;     // [B]
+  const int32_t* page_table;  // [B, max_pages]
+  int64_t B, max_pages, num_pages, page_tokens, kv_heads;
+};
+struct KvCache;
+KvCache kv4_cache_args(const Kv4View& c, int64_t T, int64_t head_dim);
+hipError_t launch_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t T,
+                             int64_t head_dim, int64_t max_new, const Kv4View& c, void* cache, hipStream_t stream);
+hipError_t launch_kv4_read(const void* cache, int64_t T, int64_t head_dim, int64_t max_new, const Kv4View& c,
+                           uint16_t* k, uint16_t* v, hipStream_t stream);
+// at least the bytes launch_kv4_attention uses with the same sizes and any window
+size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q,
+                                     int64_t max_ctx);
+hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
+                                int64_t max_q, int64_t max_ctx, int64_t window, float scale, const void* cache,
+                                const Kv4View& c, uint16_t* out, float* lse, void* workspace, hipStream_t stream);
+
 hipError_t launch_quantize(const float* W, const uint32_t* mask, int64_t N, int64_t K, int64_t group, int bits,
                            uint8_t* codes, uint16_t* scales, uint16_t* zeros, hipStream_t stream);
 hipError_t launch_pack(const uint8_t* codes, int64_t N, int64_t K, uint32_t* packed, hipStream_t stream);
