@@ -442,8 +442,8 @@ int wq_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo
  *              sequence. They only shape the launch: every sequence is handled in full
  *              whatever they are, only slower when they are far off.
  * Lengths, starts and page numbers outside their arrays are clamped on the device (wrong
- * values, never an invalid access). B up to 2^20, kv_heads up to 65535, T = rows of the
- * token-wise arrays below 2^31 / heads, max_pages * page_tokens up to 2^30. T = 0 or
+ * values, never an invalid access). B up to 2^20 and below 2^26 / heads, heads up to
+ * 65535, T = rows of the token-wise arrays below 2^31 / heads, max_pages * page_tokens up to 2^30. T = 0 or
  * B = 0 returns WQ_OK without a launch.
  */
 

@@ -92,6 +92,10 @@ __device__ __forceinline__ int64_t decode_slot(const KvCache& a, const AttnArgs&
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// a * b with the fp16 factor read as it is (one mixed-precision instruction; the sum with
+// 0 keeps the compiler from splitting it into a conversion and a product)
+__device__ __forceinline__ float mul_mix(float a, f16 b) { return __builtin_fmaf(a, (float)b, 0.0f); }
+
 // largest of eight positive fp16 values, as bits (positive fp16 order like integers)
 __device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
   const uint4 d = __builtin_bit_cast(uint4, v);
@@ -110,14 +114,17 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
   constexpr int ROWS = kDecodeRows * NT;
   __shared__ __align__(16) float merged[4][kDecodeRows][D + 4];
   __shared__ float ref_s[4][kDecodeRows], sum_s[4][kDecodeRows];
-  const int b = blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;
-  const int h = blockIdx.y / row_tiles;
+  // heads next to each other, so that the XCDs, which take blocks in turn, share every
+  // sequence and every chunk of it alike
+  const int h = blockIdx.x % a.hkv, split = blockIdx.x / a.hkv % p.nsplit;
+  const int rest = blockIdx.x / a.hkv / p.nsplit;
+  const int b = rest / row_tiles;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const KvSeq s = kv_sequence(a, b);
   const int rows = s.rows * p.group;
   if (rows > p.row_limit) return;
-  for (int rt = blockIdx.y % row_tiles; rt * ROWS < rows; rt += row_tiles) {
+  for (int rt = rest % row_tiles; rt * ROWS < rows; rt += row_tiles) {
     const int row0 = rt * ROWS, row1 = min(rows, row0 + ROWS) - 1;
     const TileRange range = tile_range(s, p, row0, row1, p.nsplit, p.chunk_tiles);
     if (split > 0 && split >= range.splits) continue;
@@ -162,7 +169,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
       uint4 k[RUNS], v[RUNS], ks, vs, vz;
       uint32_t kz;
     };
-    Data cur, next;
+    Data even, odd;
     const auto load = [&](Data& d) {
       const uint8_t* base = p.cache + kv_page_offset(a, b, h, page) + (int64_t)in_page * kv_tile_bytes<D>();
 #pragma unroll
@@ -182,8 +189,8 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
         ++page;
       }
     };
-    if (tile < end) load(cur);
-    for (; tile < end; tile += 4) {
+    // one tile: the next one's loads, issued first, are in flight while it is worked on
+    const auto step = [&](Data& cur, Data& next) {
       advance();
       if (tile + 4 < end) load(next);
 
@@ -209,7 +216,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[n][i + 4 * half] = sc[n][i] * (float)ks[i + 4 * half];
+          for (int i = 0; i < 4; ++i) x[n][i + 4 * half] = mul_mix(sc[n][i], ks[i + 4 * half]);
       }
 
       const int first = tile * kKvTile;
@@ -282,7 +289,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
         for (int e = 0; e < 8; ++e) {
           const float w = exp2_hw(__builtin_fmaf(x[n][e], p.c, -ref[n]));
           sum[n] += w;
-          wf[n][2 * (e & 3) + (e >> 2)] = (f16)(w * (float)vs[e]);
+          wf[n][2 * (e & 3) + (e >> 2)] = (f16)mul_mix(w, vs[e]);
         }
       }
 #pragma unroll
@@ -291,7 +298,12 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][t] = mfma_16x16x32(v, wf[n], acc[n][t]);
       }
-      cur = next;
+      tile += 4;
+    };
+    if (tile < end) load(even);
+    while (tile < end) {
+      step(even, odd);
+      if (tile < end) step(odd, even);
     }
 
     // join the four waves
@@ -365,9 +377,9 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
   __shared__ __align__(16) uint4 ksl[2][4], vsl[2][4];
   const int lane = threadIdx.x & 63, c = lane & 31, hl = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.y;
-  const int split = blockIdx.x % p.tnsplit;
-  const int rest = blockIdx.x / p.tnsplit;
+  // heads next to each other: with eight of them, each XCD's L2 serves one
+  const int h = blockIdx.x % a.hkv, split = blockIdx.x / a.hkv % p.tnsplit;
+  const int rest = blockIdx.x / a.hkv / p.tnsplit;
   const int b = rest / row_tiles;
   const KvSeq s = kv_sequence(a, b);
   const int rows = s.rows * p.group;
@@ -471,7 +483,10 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
           const f16x8 ks = as_f16x8(ksl[u][2 * q + hl]);
           vs[u][q] = as_f16x8(vsl[u][2 * q + hl]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)] *= (float)ks[e];
+          for (int e = 0; e < 8; ++e) {
+            const int r = 4 * (q + 2 * (e >> 2)) + (e & 3);
+            sc[u][r] = mul_mix(sc[u][r], ks[e]);
+          }
         }
       const int first = tile * kKvTile;
       const bool edge = first + 2 * kKvTile - 1 > p0 || (p.window > 0 && first <= p1 - p.window) || tile + 1 >= end;
@@ -529,7 +544,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
           for (int e = 0; e < 8; ++e) {
             const float w = exp2_hw(__builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], p.c, -ref));
             sum += w;
-            wf[2 * (e & 3) + (e >> 2)] = (f16)(w * (float)vs[u][q][e]);
+            wf[2 * (e & 3) + (e >> 2)] = (f16)mul_mix(w, vs[u][q][e]);
           }
 #pragma unroll
           for (int t = 0; t < CT; ++t)
@@ -566,51 +581,90 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
   }
 }
 
-// One wave per row of the output; the rows of unsplit sequences are already written.
-template <int D>
-__global__ void __launch_bounds__(256)
-kv4_combine_kernel(KvCache a, AttnArgs p) {
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= (int64_t)a.T * p.hq) return;
-  const int lane = threadIdx.x & 63;
-  const int token = (int)(at / p.hq), head = (int)(at % p.hq);
-  // the token's sequence: the last one that starts at or before it
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.seq_start[mid] <= token)
-      lo = mid;
-    else
-      hi = mid;
+// W waves per row of the output (1, 4 or 16, so that a wave takes about eight chunks);
+// the rows of unsplit sequences are already written.
+template <int D, int W>
+__global__ void __launch_bounds__(W < 4 ? 256 : 64 * W)
+kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
+  constexpr int ROWS = W < 4 ? 4 / W : 1;  // rows of a block
+  constexpr int N = D / 64;                // channels of a lane
+  __shared__ float part[W][D + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t item = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0);
+  int b, h, row;
+  KvSeq s;
+  if (by_sequence) {  // (sequence, head, row): the decode kernel's rows next to the tile kernel's
+    row = (int)(item % p.row_limit);
+    item /= p.row_limit;
+    h = (int)(item % a.hkv);
+    b = (int)(item / a.hkv);
+    if (b >= a.B) return;
+    s = kv_sequence(a, b);
+    if (row >= s.rows * p.group || s.rows * p.group > p.row_limit) return;
+  } else {  // every row of the output
+    if (item >= (int64_t)a.T * p.hq) return;
+    const int token = (int)(item / p.hq), head = (int)(item % p.hq);
+    // the token's sequence: the last one that starts at or before it
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.seq_start[mid] <= token)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+    s = kv_sequence(a, b);
+    const int tok = token - s.first_row;
+    if (tok < 0 || tok >= s.rows) return;
+    h = head / p.group;
+    row = tok * p.group + head % p.group;
   }
-  const KvSeq s = kv_sequence(a, lo);
-  const int tok = token - s.first_row;
-  if (tok < 0 || tok >= s.rows) return;
-  const int h = head / p.group, row = tok * p.group + head % p.group, rows = s.rows * p.group;
+  const int rows = s.rows * p.group;
   const bool tiled = rows > p.row_limit;
+  if (tiled ? p.tnsplit == 1 : p.nsplit == 1 || (p.compact && !by_sequence)) return;
   const int block = tiled ? kTileRows : p.decode_rows;
   const int row0 = row / block * block, row1 = min(rows, row0 + block) - 1;
   const int nsplit = tiled ? p.tnsplit : p.nsplit;
   const TileRange range = tile_range(s, p, row0, row1, nsplit, tiled ? p.tchunk_tiles : p.chunk_tiles);
   if (range.splits <= 1) return;
-  const int64_t slot = (tiled ? at : decode_slot(a, p, s, lo, h, row)) * nsplit;
+  const int64_t at = (int64_t)(s.first_row + row / p.group) * p.hq + h * p.group + row % p.group;
+  const int64_t slot = (tiled ? at : decode_slot(a, p, s, b, h, row)) * nsplit;
   const float2* st = (tiled ? p.tpart_s : p.part_s) + slot;
-  const float* po = (tiled ? p.tpart_o : p.part_o) + slot * D;
-  float best = kNoRef;
-  for (int i = 0; i < range.splits; ++i) best = fmaxf(best, st[i].x);
-  constexpr int N = D / 64;  // channels of a lane
-  float total = 0.0f, o[N];
+  const float* po = (tiled ? p.tpart_o : p.part_o) + slot * D + N * lane;
+  // every wave finds the row's reference and sum, a chunk a lane
+  float best = kNoRef, total = 0.0f;
+  for (int i = lane; i < range.splits; i += 64) best = fmaxf(best, st[i].x);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) best = fmaxf(best, __shfl_xor(best, off));
+  for (int i = lane; i < range.splits; i += 64) total = __builtin_fmaf(st[i].y, exp2_hw(st[i].x - best), total);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
+  float o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.0f;
-  for (int i = 0; i < range.splits; ++i) {
+#pragma unroll 8
+  for (int i = W == 1 ? 0 : wave; i < range.splits; i += W) {
     const float f = exp2_hw(st[i].x - best);
-    total = __builtin_fmaf(st[i].y, f, total);
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(po[(int64_t)i * D + N * lane + e], f, o[e]);
+    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(po[(int64_t)i * D + e], f, o[e]);
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) part[wave][N * lane + e] = o[e];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      o[e] = part[0][N * lane + e];
+#pragma unroll
+      for (int w = 1; w < W; ++w) o[e] += part[w][N * lane + e];
+    }
   }
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  f16* dst = p.out + at * D + N * lane;
 #pragma unroll
-  for (int e = 0; e < N; ++e) p.out[at * D + N * lane + e] = (f16)(o[e] * inv);
+  for (int e = 0; e < N; ++e) dst[e] = (f16)(o[e] * inv);
   if (lane == 0 && p.lse != nullptr) p.lse[at] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
 }
 
@@ -656,7 +710,8 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
   const int64_t drows = p.tile ? kLimit : rows;
   p.nt = drows <= kDecodeRows ? 1 : 2;
   p.row_tiles = (int)ceil_div(drows, kDecodeRows * p.nt);
-  if (p.row_tiles * hkv > 65535) p.row_tiles = (int)(65535 / hkv);
+  const int64_t most_blocks = 0x7FFFFFFF / (B * hkv);  // B hkv < 2^31, and so is the grid
+  if (p.row_tiles > most_blocks) p.row_tiles = (int)most_blocks;
   int64_t tiles = ceil_div(max_ctx < 1 ? 1 : max_ctx, kKvTile);
   if (window > 0) {  // q rows see up to window + q - 1 tokens, which may begin inside a tile
     const int64_t in_window = ceil_div(window + q - 1, kKvTile) + 1;
@@ -672,8 +727,9 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
     const int64_t blocks = B * hkv * ceil_div(rows, kTileRows);
     p.tmost = split_plan(tiles, blocks, 2 * kCus, 16, &p.tnsplit, &p.tchunk);
     if (p.tmost > 1) p.tslots = T * hq;
-    const int64_t grid = 0x7FFFFFFF / (B * p.tnsplit);
-    p.trow_tiles = (int)(ceil_div(rows, kTileRows) < grid ? ceil_div(rows, kTileRows) : grid);
+    p.trow_tiles = (int)ceil_div(rows, kTileRows);
+    // (split only where the blocks are few)
+    if (p.trow_tiles > most_blocks) p.trow_tiles = (int)most_blocks;
   }
   return p;
 }
@@ -681,27 +737,40 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
 size_t part_bytes(int64_t slots, int64_t nsplit, int64_t D) { return (size_t)slots * nsplit * (D * 4 + 8); }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
+// items: rows to look at
+template <int D>
+hipError_t combine(const KvCache& a, const AttnArgs& p, int nsplit, int64_t items, int by_sequence,
+                   hipStream_t stream) {
+  if (nsplit <= 8)
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 1>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, p,
+                       by_sequence);
+  else if (nsplit <= 32)
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 4>), dim3((unsigned)items), dim3(256), 0, stream, a, p, by_sequence);
+  else
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 16>), dim3((unsigned)items), dim3(1024), 0, stream, a, p, by_sequence);
+  return hipGetLastError();
+}
+
 template <int D>
 hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, int64_t hkv, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (pl.tile) {
-    const dim3 grid((unsigned)(B * pl.trow_tiles * pl.tnsplit), (unsigned)hkv);
+    const dim3 grid((unsigned)(B * hkv * pl.trow_tiles * pl.tnsplit));
     hipLaunchKernelGGL((kv4_tile_kernel<D>), grid, dim3(256), 0, stream, a, p, pl.trow_tiles);
     e = hipGetLastError();
   }
   if (e == hipSuccess && pl.decode) {
-    const dim3 grid((unsigned)(B * pl.nsplit), (unsigned)(hkv * pl.row_tiles));
+    const dim3 grid((unsigned)(B * hkv * pl.row_tiles * pl.nsplit));
     if (pl.nt == 1)
       hipLaunchKernelGGL((kv4_decode_kernel<D, 1>), grid, dim3(256), 0, stream, a, p, pl.row_tiles);
     else
       hipLaunchKernelGGL((kv4_decode_kernel<D, 2>), grid, dim3(256), 0, stream, a, p, pl.row_tiles);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && (pl.nsplit > 1 || pl.tnsplit > 1)) {
-    const dim3 grid((unsigned)(((int64_t)a.T * p.hq + 3) / 4));
-    hipLaunchKernelGGL((kv4_combine_kernel<D>), grid, dim3(256), 0, stream, a, p);
-    e = hipGetLastError();
-  }
+  if (e == hipSuccess && pl.decode && pl.tile && pl.nsplit > 1)
+    e = combine<D>(a, p, pl.nsplit, B * hkv * p.row_limit, 1, stream);
+  if (e == hipSuccess && (pl.tile ? pl.tnsplit : pl.nsplit) > 1)
+    e = combine<D>(a, p, pl.tile ? pl.tnsplit : pl.nsplit, (int64_t)a.T * p.hq, 0, stream);
   return e;
 }
 

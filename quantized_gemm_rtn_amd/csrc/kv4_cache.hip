@@ -34,14 +34,15 @@ kv4_append_kernel(const f16* __restrict__ k, int64_t k_stride, const f16* __rest
   constexpr int TPT = D / 8;            // threads of a token
   constexpr int TOK = 256 / TPT;        // tokens of a pass
   __shared__ __align__(16) uint8_t codes[kKvTile][D + 4];
-  const int b = blockIdx.x / tiles, h = blockIdx.y, t = threadIdx.x;
+  const int h = blockIdx.x % a.hkv, first_tile = blockIdx.x / a.hkv % tiles;
+  const int b = blockIdx.x / a.hkv / tiles, t = threadIdx.x;
   const KvSeq s = kv_sequence(a, b);
   const int begin = max(s.ctx - s.rows, 0);
   const int last = (s.ctx - 1) / kKvTile;  // rows > 0 and ctx > 0 where the loop runs
   if (s.rows == 0 || s.ctx == 0) return;
   // `tiles` comes from the caller's bound on the new tokens; a sequence with more is
   // still covered, in further rounds
-  for (int tile = begin / kKvTile + blockIdx.x % tiles; tile <= last; tile += tiles) {
+  for (int tile = begin / kKvTile + first_tile; tile <= last; tile += tiles) {
     int lo, hi;
     tile_tokens(s, tile, &lo, &hi);
     const int page = tile / a.page_tiles;
@@ -126,20 +127,21 @@ __global__ void __launch_bounds__(256)
 kv4_read_kernel(const uint8_t* __restrict__ cache, KvCache a, int tiles, f16* __restrict__ k, f16* __restrict__ v) {
   constexpr int TPT = D / 8, TOK = 256 / TPT;
   __shared__ __align__(16) uint8_t codes[kKvTile][D + 4];
-  const int b = blockIdx.x / tiles, h = blockIdx.y, t = threadIdx.x;
+  const int h = blockIdx.x % a.hkv, first_tile = blockIdx.x / a.hkv % tiles;
+  const int b = blockIdx.x / a.hkv / tiles, t = threadIdx.x;
   const KvSeq s = kv_sequence(a, b);
   const int part = t % TPT;
   // a sequence with more new tokens than its cache holds: the first of them are in no
   // page, and read as 0
   const int absent = max(s.rows - s.ctx, 0);
-  for (int i = (blockIdx.x % tiles) * TOK + t / TPT; i < absent; i += tiles * TOK) {
+  for (int i = first_tile * TOK + t / TPT; i < absent; i += tiles * TOK) {
     const int64_t at = ((int64_t)(s.first_row + i) * a.hkv + h) * D + 8 * part;
     *reinterpret_cast<uint4*>(k + at) = uint4{0, 0, 0, 0};
     *reinterpret_cast<uint4*>(v + at) = uint4{0, 0, 0, 0};
   }
   if (s.rows == 0 || s.ctx == 0) return;
   const int begin = max(s.ctx - s.rows, 0), last = (s.ctx - 1) / kKvTile;
-  for (int tile = begin / kKvTile + blockIdx.x % tiles; tile <= last; tile += tiles) {
+  for (int tile = begin / kKvTile + first_tile; tile <= last; tile += tiles) {
     int lo, hi;
     tile_tokens(s, tile, &lo, &hi);
     const int page = tile / a.page_tiles;
@@ -198,7 +200,7 @@ KvCache kv4_cache_args(const Kv4View& c, int64_t T, int64_t head_dim) {
 
 // tiles a sequence with up to max_new new tokens may touch, at most what the grid takes
 static int append_tiles(const Kv4View& c, int64_t max_new) {
-  const int64_t most = (((int64_t)1 << 31) - 1) / c.B;
+  const int64_t most = (((int64_t)1 << 31) - 1) / (c.B * c.kv_heads);  // B kv_heads < 2^31
   const int64_t want = (max_new + kKvTile - 2) / kKvTile + 1;
   return (int)(want < most ? want : most);
 }
@@ -207,7 +209,7 @@ hipError_t launch_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t
                              int64_t head_dim, int64_t max_new, const Kv4View& c, void* cache, hipStream_t stream) {
   const KvCache a = kv4_cache_args(c, T, head_dim);
   const int tiles = append_tiles(c, max_new);
-  const dim3 grid((unsigned)(c.B * tiles), (unsigned)c.kv_heads);
+  const dim3 grid((unsigned)(c.B * tiles * c.kv_heads));
   const f16* kp = reinterpret_cast<const f16*>(k);
   const f16* vp = reinterpret_cast<const f16*>(v);
   if (head_dim == 128)
@@ -223,7 +225,7 @@ hipError_t launch_kv4_read(const void* cache, int64_t T, int64_t head_dim, int64
                            uint16_t* k, uint16_t* v, hipStream_t stream) {
   const KvCache a = kv4_cache_args(c, T, head_dim);
   const int tiles = append_tiles(c, max_new);
-  const dim3 grid((unsigned)(c.B * tiles), (unsigned)c.kv_heads);
+  const dim3 grid((unsigned)(c.B * tiles * c.kv_heads));
   if (head_dim == 128)
     hipLaunchKernelGGL((kv4_read_kernel<128>), grid, dim3(256), 0, stream, static_cast<const uint8_t*>(cache), a,
                        tiles, reinterpret_cast<f16*>(k), reinterpret_cast<f16*>(v));
