@@ -33,9 +33,8 @@ struct KvCache {
   const int32_t* page_table;  // [B, max_pages]
   const int32_t* seq_start;   // [B + 1]
   const int32_t* ctx_len;     // [B]
-  int64_t num_pages;
   int64_t page_bytes;         // of one head
-  int B, hkv, max_pages;
+  int B, hkv, max_pages, num_pages;
   int page_tiles;             // tiles of a page
   int T;                      // rows of the token-wise arrays
 };
@@ -125,12 +124,14 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvCache& a, int b) {
   s.ctx = (int)min((int64_t)max(a.ctx_len[b], 0), most);
   return s;
 }
-// offset in the cache of page `page` of sequence b, head h (64 bits: a cache may be
-// larger than 4 GiB)
+// offset in the cache of head h of the page numbered id (64 bits: a cache may be larger
+// than 4 GiB), and of page `page` of sequence b
+__device__ __forceinline__ int64_t kv_page_offset(const KvCache& a, int h, int id) {
+  const int in = min(max(id, 0), a.num_pages - 1);
+  return ((int64_t)in * a.hkv + h) * a.page_bytes;
+}
 __device__ __forceinline__ int64_t kv_page_offset(const KvCache& a, int b, int h, int page) {
-  const int64_t id = a.page_table[(int64_t)b * a.max_pages + page];
-  const int64_t in = id < 0 ? 0 : (id >= a.num_pages ? a.num_pages - 1 : id);
-  return (in * a.hkv + h) * a.page_bytes;
+  return kv_page_offset(a, h, a.page_table[(int64_t)b * a.max_pages + page]);
 }
 
 }  // namespace wq

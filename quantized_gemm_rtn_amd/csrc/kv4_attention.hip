@@ -105,6 +105,47 @@ __device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
   return max((uint32_t)m.x, (uint32_t)m.y);
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kDepth = 2;  // tiles of a wave's ring: one in use, one on its way
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A lane's share of a tile in LDS. Read in assembly, with the wait inside: the compiler
+// would hold any read of its own back until every load into LDS has landed, the later
+// tiles' too.
+template <int D>
+struct TileData {
+  u32x4 k[D / 64], v[D / 64], ks, vs, vz;
+  uint32_t kz;
+};
+template <int D>
+__device__ __forceinline__ void lds_tile(TileData<D>& t, uint32_t at, int lane) {
+  const uint32_t code = at + 16 * lane, group = at + 16 * (lane >> 4), one = at + 4 * (lane & 15);
+  if constexpr (D == 128) {
+    asm volatile(
+        "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\t"
+        "ds_read_b32 %7, %10 offset:4160\n\tds_read_b128 %4, %9 offset:4096\n\t"
+        "ds_read_b128 %5, %9 offset:4224\n\tds_read_b128 %6, %9 offset:4288\n\t"
+        "ds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3072\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(t.k[0]), "=&v"(t.k[1]), "=&v"(t.v[0]), "=&v"(t.v[1]), "=&v"(t.ks), "=&v"(t.vs), "=&v"(t.vz),
+          "=&v"(t.kz)
+        : "v"(code), "v"(group), "v"(one)
+        : "memory");
+  } else {
+    asm volatile(
+        "ds_read_b128 %0, %6\n\tds_read_b32 %5, %8 offset:2112\n\tds_read_b128 %2, %7 offset:2048\n\t"
+        "ds_read_b128 %3, %7 offset:2176\n\tds_read_b128 %4, %7 offset:2240\n\t"
+        "ds_read_b128 %1, %6 offset:1024\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(t.k[0]), "=&v"(t.v[0]), "=&v"(t.ks), "=&v"(t.vs), "=&v"(t.vz), "=&v"(t.kz)
+        : "v"(code), "v"(group), "v"(one)
+        : "memory");
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(256)
 kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
@@ -112,8 +153,12 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
   constexpr int CT = D / 16;   // channel tiles of the second
   constexpr int RUNS = D / 64; // 16-byte runs a lane loads of keys, and of values
   constexpr int ROWS = kDecodeRows * NT;
-  __shared__ __align__(16) float merged[4][kDecodeRows][D + 4];
+  constexpr int TILE = kv_tile_bytes<D>();
+  // each wave's ring of tiles, and at the end the waves' results
+  constexpr int kMerge = 4 * kDecodeRows * (D + 4) * 4;
+  __shared__ __align__(16) uint8_t lds[kDepth * 4 * TILE > kMerge ? kDepth * 4 * TILE : kMerge];
   __shared__ float ref_s[4][kDecodeRows], sum_s[4][kDecodeRows];
+  float(*merged)[kDecodeRows][D + 4] = reinterpret_cast<float(*)[kDecodeRows][D + 4]>(lds);
   // heads next to each other, so that the XCDs, which take blocks in turn, share every
   // sequence and every chunk of it alike
   const int h = blockIdx.x % a.hkv, split = blockIdx.x / a.hkv % p.nsplit;
@@ -142,11 +187,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
       pos[n] = valid ? s.ctx - s.rows + tok : -1;
       const f16* qp = p.q + (int64_t)(s.first_row + tok) * p.q_stride + head * D + (D / 4) * g;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        uint4 d = *reinterpret_cast<const uint4*>(qp + 8 * w);
-        if (!valid) d = uint4{0, 0, 0, 0};
-        qf[n][w] = as_f16x8(perm_x8(d));
-      }
+      for (int w = 0; w < KW; ++w) qf[n][w] = as_f16x8(*reinterpret_cast<const uint4*>(qp + 8 * w));
     }
     const uint32_t magic = magic_1024x2();
 
@@ -165,42 +206,75 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
     const int begin = range.t0 + split * range.chunk, end = min(range.t1, begin + range.chunk);
     int tile = begin + wave;
     int page = tile / a.page_tiles, in_page = tile - page * a.page_tiles;
-    struct Data {
-      uint4 k[RUNS], v[RUNS], ks, vs, vz;
-      uint32_t kz;
+    uint8_t* ring = lds + wave * kDepth * TILE;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)ring;
+    // one tile's bytes, contiguous in memory, straight into a stage of the ring: D / 32
+    // runs of 16 bytes a lane and one of 4
+    constexpr int LOADS = D / 32 + 1;
+    // numbers of 64 pages, one a lane: a load each tile would have to wait for the tiles
+    // on their way
+    int ids = 0, ids_page = page;
+    const auto load_ids = [&]() {
+      ids = a.page_table[(int64_t)b * a.max_pages + min(ids_page + lane, a.max_pages - 1)];
+      asm volatile("" : "+v"(ids));  // waited for here
     };
-    Data even, odd;
-    const auto load = [&](Data& d) {
-      const uint8_t* base = p.cache + kv_page_offset(a, b, h, page) + (int64_t)in_page * kv_tile_bytes<D>();
-#pragma unroll
-      for (int i = 0; i < RUNS; ++i) {
-        d.k[i] = *reinterpret_cast<const uint4*>(base + kv_key_offset<D>() + 1024 * i + 16 * lane);
-        d.v[i] = *reinterpret_cast<const uint4*>(base + kv_value_offset<D>() + 1024 * i + 16 * lane);
+    if (tile < end) load_ids();
+    const auto fetch = [&](int stage) {
+      if (page - ids_page >= 64) {
+        ids_page = page;
+        load_ids();
       }
-      d.ks = *reinterpret_cast<const uint4*>(base + kv_meta_offset<D>(0) + 16 * g);
-      d.kz = *reinterpret_cast<const uint32_t*>(base + kv_meta_offset<D>(1) + 4 * c);
-      d.vs = *reinterpret_cast<const uint4*>(base + kv_meta_offset<D>(2) + 16 * g);
-      d.vz = *reinterpret_cast<const uint4*>(base + kv_meta_offset<D>(3) + 16 * g);
-    };
-    const auto advance = [&]() {
+      const int id = __builtin_amdgcn_readlane(ids, page - ids_page);
+      const auto rsrc = buffer_rsrc(p.cache + kv_page_offset(a, h, id) + (int64_t)in_page * TILE, (uint32_t)TILE);
+      auto* dst = (__attribute__((address_space(3))) uint8_t*)(ring + stage * TILE);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst + 1024 * i, 16, 16 * lane, 1024 * i, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, dst + 32 * D, 4, 4 * lane, 32 * D, 0, 0);
       in_page += 4;
       while (in_page >= a.page_tiles) {
         in_page -= a.page_tiles;
         ++page;
       }
     };
-    // one tile: the next one's loads, issued first, are in flight while it is worked on
-    const auto step = [&](Data& cur, Data& next) {
-      advance();
-      if (tile + 4 < end) load(next);
+    int fetched = tile, stage_in = 0, stage = 0;
+    const auto fetch_next = [&]() {
+      if (fetched < end) fetch(stage_in);
+      fetched += 4;
+      stage_in = stage_in + 1 == kDepth ? 0 : stage_in + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch_next();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const uint4 d = perm_x8(__builtin_bit_cast(uint4, qf[n][w]));
+        const uint32_t m = pos[n] < 0 ? 0u : 0xFFFFFFFFu;  // (a row that sees nothing may be no row at all)
+        qf[n][w] = as_f16x8(uint4{d.x & m, d.y & m, d.z & m, d.w & m});
+      }
+    for (; tile < end; tile += 4) {
+      fetch_next();
+      // this tile's loads are done when only the later tiles' are left
+      const int later = (end - 1 - tile) >> 2;
+      if (later >= kDepth - 1)
+        wait_vm<(kDepth - 1) * LOADS>();
+      else if (kDepth > 2 && later == 1)
+        wait_vm<LOADS>();
+      else if (kDepth > 3 && later == 2)
+        wait_vm<2 * LOADS>();
+      else
+        wait_vm<0>();
+      const uint32_t at = ring_at + stage * TILE;
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+      TileData<D> cur;
+      lds_tile<D>(cur, at, lane);
 
       // scores: lane's tokens 4 g + i + 16 half of the tile at index i + 4 half
-      const f16x8 ks = as_f16x8(cur.ks);
+      const f16x8 ks = __builtin_bit_cast(f16x8, cur.ks);
       const KeyZeros kz = kv_key_zeros(cur.kz);
-      f16x8 vs = as_f16x8(cur.vs);
-      uint4 vz = cur.vz;
-      const uint32_t* kw = reinterpret_cast<const uint32_t*>(&cur.k[0]);
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(&cur.v[0]);
+      f16x8 vs = __builtin_bit_cast(f16x8, cur.vs);
+      uint4 vz = __builtin_bit_cast(uint4, cur.vz);
       float x[NT][8];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -209,7 +283,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
         for (int n = 0; n < NT; ++n) sc[n] = f32x4{};
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const f16x8 k = as_f16x8(codes_minus_zero_x16(kw[KW * half + w], magic, kz.bias[half], kz.nbias16[half]));
+          const f16x8 k = as_f16x8(codes_minus_zero_x16(cur.k[(KW * half + w) >> 2][(KW * half + w) & 3], magic, kz.bias[half], kz.nbias16[half]));
 #pragma unroll
           for (int n = 0; n < NT; ++n) sc[n] = mfma_16x16x32(k, qf[n][w], sc[n]);
         }
@@ -294,16 +368,10 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
       }
 #pragma unroll
       for (int t = 0; t < CT; ++t) {
-        const f16x8 v = kv_value_operand(vw[t], magic, vz);
+        const f16x8 v = kv_value_operand(cur.v[t >> 2][t & 3], magic, vz);
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][t] = mfma_16x16x32(v, wf[n], acc[n][t]);
       }
-      tile += 4;
-    };
-    if (tile < end) load(even);
-    while (tile < end) {
-      step(even, odd);
-      if (tile < end) step(odd, even);
     }
 
     // join the four waves
@@ -312,7 +380,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
       float su = sum[n];
       su += __shfl_xor(su, 16);
       su += __shfl_xor(su, 32);
-      __syncthreads();  // the previous column tile has been read
+      __syncthreads();  // every wave is done with its ring, and with the previous column tile
       if (g == 0) {
         ref_s[wave][c] = ref[n];
         sum_s[wave][c] = su;

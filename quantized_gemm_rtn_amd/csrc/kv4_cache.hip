@@ -188,7 +188,7 @@ KvCache kv4_cache_args(const Kv4View& c, int64_t T, int64_t head_dim) {
   a.page_table = c.page_table;
   a.seq_start = c.seq_start;
   a.ctx_len = c.ctx_len;
-  a.num_pages = c.num_pages;
+  a.num_pages = (int)c.num_pages;
   a.page_bytes = c.page_tokens * (head_dim + 8);
   a.B = (int)c.B;
   a.hkv = (int)c.kv_heads;
