@@ -23,12 +23,12 @@
 // moves (and everything summed so far is only rescaled) when a tile's scores or value
 // scales would pass that bound, which any lane can see without asking the others.
 //
-//  kv4_decode_kernel   few query rows (16 or 32 a block): one block per sequence, head and
-//    chunk of the cache, whose four waves take its tiles of 32 tokens in turn, straight
-//    from memory into registers, and join through LDS at the end.
+//  kv4_decode_kernel   few query rows (16 or 32 a block): all tiles of all sequences are
+//    dealt out in equal shares, one a block, whose four waves take tiles of 32 tokens in
+//    turn and join through LDS at each row tile's end.
 //  kv4_tile_kernel     many query rows: 128 a block; a tile of codes is turned into exact
 //    fp16 integers once, in LDS, for all of them.
-//  kv4_combine_kernel  joins the chunks of a row where a sequence was split.
+//  kv4_combine_kernel  joins the parts of rows that more than one block worked on.
 #include "kv4.h"
 #include "wq_launch.h"
 
@@ -49,45 +49,87 @@ struct AttnArgs {
   int64_t q_stride;
   const uint8_t* cache;
   f16* out;
-  float* lse;        // may be null
-  float* part_o;     // [slots][nsplit][D]
-  float2* part_s;    // [slots][nsplit]: r, sum
-  float* tpart_o;    // the same for the tile kernel
-  float2* tpart_s;
-  int hq, group;     // query heads, and those of one key/value head
-  int window;        // 0: none
-  float c;           // scale * log2(e)
-  int nsplit, chunk_tiles;    // of the decode kernel
-  int tnsplit, tchunk_tiles;  // of the tile kernel
-  int decode_rows;            // rows a block of the decode kernel takes (16 or 32)
-  int row_limit;     // sequences with more rows of a head belong to the tile kernel
-  int compact;       // partials of the decode kernel by (sequence, head, row): see decode_slot
+  float* lse;         // may be null
+  float* part_o;      // partials of the decode kernel, two a block: [block][2][rows][D]
+  float2* part_s;     // [block][2][rows]: r, sum
+  float* tpart_o;     // partials of the tile kernel: [T * hq][tnsplit][D]
+  float2* tpart_s;    // [T * hq][tnsplit]
+  int hq, group;      // query heads, and those of one key/value head
+  int window;         // 0: none
+  float c;            // scale * log2(e)
+  int shares, least;  // decode kernel: blocks a head, and the fewest tiles of one
+  int decode_rows;    // rows of an item of the decode kernel (16 or 32)
+  int tnsplit, tchunk_tiles;  // tile kernel: most chunks of a row, and their tiles
+  int row_limit;      // sequences with more rows of a head belong to the tile kernel
 };
 
-// Tiles [t0, t1) of a sequence that rows row0 .. row1 (of one head group) can see, and
-// how they are split.
+// Tiles [t0, t1) of a sequence that rows row0 .. row1 (of one head group) can see.
 struct TileRange {
-  int t0, t1, chunk, splits;
+  int t0, t1;
 };
-__device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& p, int row0, int row1, int nsplit,
-                                                int chunk_tiles) {
+__device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& p, int row0, int row1) {
   const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
   const int lo = p.window > 0 ? max(p0 - p.window + 1, 0) : 0;
   TileRange r;
   r.t0 = lo / kKvTile;
   r.t1 = p1 < lo ? r.t0 : p1 / kKvTile + 1;
-  const int n = r.t1 - r.t0;
-  r.chunk = max(chunk_tiles, (n + nsplit - 1) / nsplit);
-  r.splits = (n + r.chunk - 1) / r.chunk;
   return r;
 }
+// ... and the tile kernel's chunks of them
+struct TileSplit {
+  int chunk, splits;
+};
+__device__ __forceinline__ TileSplit tile_split(const TileRange& r, const AttnArgs& p) {
+  const int n = r.t1 - r.t0;
+  TileSplit t;
+  t.chunk = max(p.tchunk_tiles, (n + p.tnsplit - 1) / p.tnsplit);
+  t.splits = (n + t.chunk - 1) / t.chunk;
+  return t;
+}
 
-// Row of the decode kernel's partials. Where the tile kernel runs too, only sequences with
-// few rows come here, and the partials are laid out by sequence; else by token.
-__device__ __forceinline__ int64_t decode_slot(const KvCache& a, const AttnArgs& p, const KvSeq& s, int b, int h,
-                                               int row) {
-  if (p.compact) return ((int64_t)b * a.hkv + h) * p.row_limit + row;
-  return (int64_t)(s.first_row + row / p.group) * p.hq + h * p.group + row % p.group;
+// The decode kernel's work: its items are a sequence's row tiles, in order, each as many
+// steps as the sequence has visible tiles (one where it has none: its rows are still to
+// be written). All steps of a head are dealt out in equal shares, one a block, so that
+// blocks end together however the sequences' lengths differ; an item that lies in one
+// share is finished there, others leave a partial in each. A wave looks at 64 sequences
+// at a time, one a lane.
+struct Sequences {
+  KvSeq s;
+  int t0, n;      // first visible tile, steps of an item (0: nothing to do here)
+  int64_t steps, upto;  // of the sequence, and of those up to it, from `first` on
+};
+__device__ __forceinline__ Sequences load_sequences(const KvCache& a, const AttnArgs& p, int first, int lane) {
+  Sequences q;
+  const int b = first + lane;
+  q.s = kv_sequence(a, min(b, a.B - 1));
+  const int rows = q.s.rows * p.group;
+  const bool mine = b < a.B && rows > 0 && rows <= p.row_limit;
+  const TileRange r = tile_range(q.s, p, 0, rows - 1);
+  q.t0 = r.t0;
+  q.n = mine ? max(r.t1 - r.t0, 1) : 0;
+  q.steps = (int64_t)q.n * ((rows + p.decode_rows - 1) / p.decode_rows);
+  q.upto = q.steps;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t v = __shfl_up(q.upto, off);
+    q.upto += lane >= off ? v : 0;
+  }
+  return q;
+}
+__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+// steps of a head in all; `q` holds the first 64 sequences
+__device__ __forceinline__ int64_t total_steps(const KvCache& a, const AttnArgs& p, const Sequences& q, int lane) {
+  int64_t n = lane_value(q.upto, 63);
+  for (int first = 64; first < a.B; first += 64) n += lane_value(load_sequences(a, p, first, lane).upto, 63);
+  return n;
+}
+__device__ __forceinline__ int64_t share_steps(const AttnArgs& p, int64_t total) {
+  const int64_t n = total < (int64_t)1 << 31 ? (int64_t)((uint32_t)(total + p.shares - 1) / (uint32_t)p.shares)
+                                             : (total + p.shares - 1) / p.shares;
+  return n < p.least ? p.least : n;
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -148,10 +190,9 @@ __device__ __forceinline__ void lds_tile(TileData<D>& t, uint32_t at, int lane) 
 
 template <int D, int NT>
 __global__ void __launch_bounds__(256)
-kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
+kv4_decode_kernel(KvCache a, AttnArgs p) {
   constexpr int KW = D / 32;   // steps of the first product
   constexpr int CT = D / 16;   // channel tiles of the second
-  constexpr int RUNS = D / 64; // 16-byte runs a lane loads of keys, and of values
   constexpr int ROWS = kDecodeRows * NT;
   constexpr int TILE = kv_tile_bytes<D>();
   // each wave's ring of tiles, and at the end the waves' results
@@ -160,19 +201,41 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
   __shared__ float ref_s[4][kDecodeRows], sum_s[4][kDecodeRows];
   float(*merged)[kDecodeRows][D + 4] = reinterpret_cast<float(*)[kDecodeRows][D + 4]>(lds);
   // heads next to each other, so that the XCDs, which take blocks in turn, share every
-  // sequence and every chunk of it alike
-  const int h = blockIdx.x % a.hkv, split = blockIdx.x / a.hkv % p.nsplit;
-  const int rest = blockIdx.x / a.hkv / p.nsplit;
-  const int b = rest / row_tiles;
+  // sequence alike
+  const int h = blockIdx.x % a.hkv, share = blockIdx.x / a.hkv;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const KvSeq s = kv_sequence(a, b);
-  const int rows = s.rows * p.group;
-  if (rows > p.row_limit) return;
-  for (int rt = rest % row_tiles; rt * ROWS < rows; rt += row_tiles) {
+  const uint32_t magic = magic_1024x2();
+
+  int first = 0;        // of the 64 sequences at hand
+  int64_t before = 0;   // steps of the sequences before them
+  Sequences seqs = load_sequences(a, p, 0, lane);
+  const int64_t total = total_steps(a, p, seqs, lane), per = share_steps(p, total);
+  int64_t at = share * per;
+  const int64_t until = at + per < total ? at + per : total;
+  bool opening = true;  // the share's first item: its partial goes to slot 0, another's to slot 1
+  while (at < until) {
+    while (before + lane_value(seqs.upto, 63) <= at) {
+      if (first + 64 >= a.B) return;  // (only if the lengths changed meanwhile)
+      before += lane_value(seqs.upto, 63);
+      first += 64;
+      seqs = load_sequences(a, p, first, lane);
+    }
+    const int j = __popcll(__ballot(before + seqs.upto <= at));  // the sequence that step `at` is of
+    const int b = first + j;
+    KvSeq s;
+    s.first_row = __builtin_amdgcn_readlane(seqs.s.first_row, j);
+    s.rows = __builtin_amdgcn_readlane(seqs.s.rows, j);
+    s.ctx = __builtin_amdgcn_readlane(seqs.s.ctx, j);
+    const int t0 = __builtin_amdgcn_readlane(seqs.t0, j), steps = __builtin_amdgcn_readlane(seqs.n, j);
+    const int rows = s.rows * p.group;
+    const int64_t into = at - (before + lane_value(seqs.upto - seqs.steps, j));
+    const int rt = rows > ROWS ? (int)(into / steps) : 0;
+    const int from = (int)(into - (int64_t)rt * steps);
+    const int count = (int)(until - at < steps - from ? until - at : steps - from);
+    const bool whole = count == steps;
+    at += count;
     const int row0 = rt * ROWS, row1 = min(rows, row0 + ROWS) - 1;
-    const TileRange range = tile_range(s, p, row0, row1, p.nsplit, p.chunk_tiles);
-    if (split > 0 && split >= range.splits) continue;
     const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
 
     // the lane's query rows: operands of the first product, and position
@@ -189,7 +252,6 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
 #pragma unroll
       for (int w = 0; w < KW; ++w) qf[n][w] = as_f16x8(*reinterpret_cast<const uint4*>(qp + 8 * w));
     }
-    const uint32_t magic = magic_1024x2();
 
     f32x4 acc[NT][CT];
     float ref[NT], sum[NT];
@@ -203,7 +265,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
     float vexp = 0.0f;          // value scales seen are at most 2^vexp, the fp16 with bits vbits
     uint32_t vbits = 0;
 
-    const int begin = range.t0 + split * range.chunk, end = min(range.t1, begin + range.chunk);
+    const int begin = t0 + from, end = s.ctx > 0 ? begin + count : begin;
     int tile = begin + wave;
     int page = tile / a.page_tiles, in_page = tile - page * a.page_tiles;
     uint8_t* ring = lds + wave * kDepth * TILE;
@@ -400,36 +462,37 @@ kv4_decode_kernel(KvCache a, AttnArgs p, int row_tiles) {
         float best = ref_s[0][r];
 #pragma unroll
         for (int w = 1; w < 4; ++w) best = fmaxf(best, ref_s[w][r]);
-        float total = 0.0f;
+        float total_sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) total = __builtin_fmaf(sum_s[w][r], exp2_hw(ref_s[w][r] - best), total);
+        for (int w = 0; w < 4; ++w) total_sum = __builtin_fmaf(sum_s[w][r], exp2_hw(ref_s[w][r] - best), total_sum);
         float o[CT];
 #pragma unroll
         for (int i = 0; i < CT; ++i)
           o[i] = (merged[0][r][CT * part + i] + merged[1][r][CT * part + i]) +
                  (merged[2][r][CT * part + i] + merged[3][r][CT * part + i]);
-        if (range.splits > 1) {
-          const int64_t at = decode_slot(a, p, s, b, h, row) * p.nsplit + split;
-          float* dst = p.part_o + at * D + CT * part;
+        if (!whole) {
+          const int64_t slot = ((int64_t)blockIdx.x * 2 + (opening ? 0 : 1)) * ROWS + kDecodeRows * n + r;
+          float* dst = p.part_o + slot * D + CT * part;
 #pragma unroll
           for (int i = 0; i < CT; i += 4) *reinterpret_cast<f32x4*>(dst + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-          if (part == 0) p.part_s[at] = make_float2(best, total);
+          if (part == 0) p.part_s[slot] = make_float2(best, total_sum);
         } else {
           const int tok = row / p.group;
-          const int64_t at = (int64_t)(s.first_row + tok) * p.hq + h * p.group + (row - tok * p.group);
-          const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-          f16* dst = p.out + at * D + CT * part;
+          const int64_t at_row = (int64_t)(s.first_row + tok) * p.hq + h * p.group + (row - tok * p.group);
+          const float inv = total_sum > 0.0f ? 1.0f / total_sum : 0.0f;
+          f16* dst = p.out + at_row * D + CT * part;
 #pragma unroll
           for (int i = 0; i < CT; i += 4) {
             typedef f16 f16x4 __attribute__((ext_vector_type(4)));
             *reinterpret_cast<f16x4*>(dst + i) =
                 f16x4{(f16)(o[i] * inv), (f16)(o[i + 1] * inv), (f16)(o[i + 2] * inv), (f16)(o[i + 3] * inv)};
           }
-          if (part == 0 && p.lse != nullptr) p.lse[at] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
+          if (part == 0 && p.lse != nullptr) p.lse[at_row] = total_sum > 0.0f ? (best + log2f(total_sum)) * kLn2 : -INFINITY;
         }
       }
     }
     __syncthreads();
+    opening = false;
   }
 }
 
@@ -457,8 +520,9 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
   for (int back = rest % row_tiles; back < have; back += row_tiles) {
     const int rt = have - 1 - back;
     const int row0 = rt * kTileRows, row1 = min(rows, row0 + kTileRows) - 1;
-    const TileRange range = tile_range(s, p, row0, row1, p.tnsplit, p.tchunk_tiles);
-    if (split > 0 && split >= range.splits) continue;
+    const TileRange range = tile_range(s, p, row0, row1);
+    const TileSplit parts = tile_split(range, p);
+    if (split > 0 && split >= parts.splits) continue;
     const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
     const int row = row0 + 32 * wave + c;
     const bool valid = row < rows;
@@ -479,7 +543,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
     float ref = kNoRef, sum = 0.0f, vexp = 0.0f;
     uint32_t vbits = 0;
 
-    const int begin = range.t0 + split * range.chunk, end = min(range.t1, begin + range.chunk);
+    const int begin = range.t0 + split * parts.chunk, end = min(range.t1, begin + parts.chunk);
     // each wave turns one tile's keys or values into LDS operands: waves 0, 1 the first
     // tile's, waves 2, 3 the second's
     const int sub = wave >> 1;
@@ -622,7 +686,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
     sum += __shfl_xor(sum, 32);
     if (valid) {
       const int64_t slot = (int64_t)(s.first_row + tok) * p.hq + head;
-      if (range.splits > 1) {
+      if (parts.splits > 1) {
         const int64_t at = slot * p.tnsplit + split;
         float* dst = p.tpart_o + at * D + 4 * hl;
 #pragma unroll
@@ -649,27 +713,29 @@ kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
   }
 }
 
-// W waves per row of the output (1, 4 or 16, so that a wave takes about eight chunks);
-// the rows of unsplit sequences are already written.
-template <int D, int W>
+// Joins the partials of rows that were split: those of the decode kernel (kTiled false)
+// or of the tile kernel. W waves per row (1, 4 or 16, so that a wave takes about eight);
+// rows that are already written are left alone. by_sequence: the rows looked at are the
+// first row_limit of each sequence and head, not all of the output.
+template <int D, int W, bool kTiled>
 __global__ void __launch_bounds__(W < 4 ? 256 : 64 * W)
 kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
   constexpr int ROWS = W < 4 ? 4 / W : 1;  // rows of a block
   constexpr int N = D / 64;                // channels of a lane
-  __shared__ float part[W][D + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float joined[W][D + 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t item = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0);
   int b, h, row;
   KvSeq s;
-  if (by_sequence) {  // (sequence, head, row): the decode kernel's rows next to the tile kernel's
+  if (by_sequence) {
     row = (int)(item % p.row_limit);
     item /= p.row_limit;
     h = (int)(item % a.hkv);
     b = (int)(item / a.hkv);
     if (b >= a.B) return;
     s = kv_sequence(a, b);
-    if (row >= s.rows * p.group || s.rows * p.group > p.row_limit) return;
-  } else {  // every row of the output
+    if (row >= s.rows * p.group) return;
+  } else {
     if (item >= (int64_t)a.T * p.hq) return;
     const int token = (int)(item / p.hq), head = (int)(item % p.hq);
     // the token's sequence: the last one that starts at or before it
@@ -689,80 +755,102 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
     row = tok * p.group + head % p.group;
   }
   const int rows = s.rows * p.group;
-  const bool tiled = rows > p.row_limit;
-  if (tiled ? p.tnsplit == 1 : p.nsplit == 1 || (p.compact && !by_sequence)) return;
-  const int block = tiled ? kTileRows : p.decode_rows;
-  const int row0 = row / block * block, row1 = min(rows, row0 + block) - 1;
-  const int nsplit = tiled ? p.tnsplit : p.nsplit;
-  const TileRange range = tile_range(s, p, row0, row1, nsplit, tiled ? p.tchunk_tiles : p.chunk_tiles);
-  if (range.splits <= 1) return;
-  const int64_t at = (int64_t)(s.first_row + row / p.group) * p.hq + h * p.group + row % p.group;
-  const int64_t slot = (tiled ? at : decode_slot(a, p, s, b, h, row)) * nsplit;
-  const float2* st = (tiled ? p.tpart_s : p.part_s) + slot;
-  const float* po = (tiled ? p.tpart_o : p.part_o) + slot * D + N * lane;
-  // every wave finds the row's reference and sum, a chunk a lane
+  if ((rows > p.row_limit) != kTiled) return;
+  const int64_t out_row = (int64_t)(s.first_row + row / p.group) * p.hq + h * p.group + row % p.group;
+
+  // the row's partials: number i is at base + i * stride, but the first at `start`
+  int parts;
+  int64_t start, base, stride;
+  const float* po;
+  const float2* ps;
+  if constexpr (kTiled) {
+    const int row0 = row / kTileRows * kTileRows, row1 = min(rows, row0 + kTileRows) - 1;
+    parts = tile_split(tile_range(s, p, row0, row1), p).splits;
+    start = base = out_row * p.tnsplit;
+    stride = 1;
+    po = p.tpart_o;
+    ps = p.tpart_s;
+  } else {
+    Sequences q = load_sequences(a, p, 0, lane);
+    const int64_t per = share_steps(p, total_steps(a, p, q, lane));
+    int64_t before = 0;
+    for (int first = 64; first <= b; first += 64) {
+      before += lane_value(q.upto, 63);
+      q = load_sequences(a, p, first, lane);
+    }
+    const int n = __builtin_amdgcn_readlane(q.n, b & 63);
+    const int64_t from = before + lane_value(q.upto - q.steps, b & 63) + (int64_t)(row / p.decode_rows) * n;
+    const int64_t i0 = from / per, i1 = (from + n - 1) / per;
+    parts = (int)(i1 - i0) + 1;
+    // share i of head h is block i * hkv + h, two partials each: the share that the item
+    // begins inside has it second
+    const auto slot = [&](int64_t i, int second) {
+      return ((i * a.hkv + h) * 2 + second) * p.decode_rows + row % p.decode_rows;
+    };
+    base = slot(i0, 0);
+    stride = (int64_t)a.hkv * 2 * p.decode_rows;
+    start = slot(i0, from > i0 * per);
+    po = p.part_o;
+    ps = p.part_s;
+  }
+  if (parts <= 1) return;
+  const auto place = [&](int i) { return i == 0 ? start : base + i * stride; };
+  // every wave finds the row's reference and sum, a partial a lane
   float best = kNoRef, total = 0.0f;
-  for (int i = lane; i < range.splits; i += 64) best = fmaxf(best, st[i].x);
+  for (int i = lane; i < parts; i += 64) best = fmaxf(best, ps[place(i)].x);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) best = fmaxf(best, __shfl_xor(best, off));
-  for (int i = lane; i < range.splits; i += 64) total = __builtin_fmaf(st[i].y, exp2_hw(st[i].x - best), total);
+  for (int i = lane; i < parts; i += 64) {
+    const float2 v = ps[place(i)];
+    total = __builtin_fmaf(v.y, exp2_hw(v.x - best), total);
+  }
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
   float o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.0f;
 #pragma unroll 8
-  for (int i = W == 1 ? 0 : wave; i < range.splits; i += W) {
-    const float f = exp2_hw(st[i].x - best);
+  for (int i = W == 1 ? 0 : wave; i < parts; i += W) {
+    const int64_t at = place(i);
+    const float f = exp2_hw(ps[at].x - best);
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(po[(int64_t)i * D + e], f, o[e]);
+    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(po[at * D + N * lane + e], f, o[e]);
   }
   if constexpr (W > 1) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) part[wave][N * lane + e] = o[e];
+    for (int e = 0; e < N; ++e) joined[wave][N * lane + e] = o[e];
     __syncthreads();
     if (wave != 0) return;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      o[e] = part[0][N * lane + e];
+      o[e] = joined[0][N * lane + e];
 #pragma unroll
-      for (int w = 1; w < W; ++w) o[e] += part[w][N * lane + e];
+      for (int w = 1; w < W; ++w) o[e] += joined[w][N * lane + e];
     }
   }
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-  f16* dst = p.out + at * D + N * lane;
+  f16* dst = p.out + out_row * D + N * lane;
 #pragma unroll
   for (int e = 0; e < N; ++e) dst[e] = (f16)(o[e] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[at] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) p.lse[out_row] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
 }
 
 namespace {
 
 constexpr int64_t kCus = 256;
+constexpr int64_t kDecodeBlocks = 2;  // blocks a CU (three fit; measured slower by 2 %: more, shorter shares)
+constexpr int64_t kLeastTiles = 8;    // of a share: two a wave
 
 struct Plan {
-  bool decode, tile;    // which kernels run
-  int nt;               // column tiles of the decode kernel
-  int row_limit, row_tiles, trow_tiles;
-  int nsplit, chunk, tnsplit, tchunk;
-  int64_t slots, tslots;      // rows of the partials, each nsplit times; 0: not split
-  int64_t most, tmost;        // bounds of nsplit and tnsplit
+  bool decode, tile;  // which kernels run
+  int decode_rows, row_limit;
+  int64_t shares;     // decode kernel: blocks a head
+  int trow_tiles;     // tile kernel: row tiles of a sequence that get blocks of their own
+  int tnsplit, tchunk;
+  int64_t tslots, tmost;  // rows of its partials (0: not split), and a bound of tnsplit
 };
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
-
-// Splits of `tiles` tiles so that `blocks` blocks become about `want`, each of at least
-// `least` tiles.
-// Returns the splits' bound, which never falls as `tiles` grows (a workspace sized for
-// longer sequences holds the partials of shorter ones).
-int64_t split_plan(int64_t tiles, int64_t blocks, int64_t want, int64_t least, int* nsplit, int* chunk) {
-  int64_t n = ceil_div(want, blocks);
-  const int64_t most = ceil_div(tiles, least);
-  n = n > most ? most : n;
-  *chunk = (int)ceil_div(tiles, n);
-  *nsplit = (int)ceil_div(tiles, *chunk);
-  return n;
-}
 
 Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int64_t max_ctx, int64_t window) {
   Plan p = {};
@@ -775,70 +863,78 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
   p.tile = rows > kLimit;
   p.decode = !p.tile || (B > 1 && B * q > T);
   p.row_limit = p.tile ? (p.decode ? (int)kLimit : 0) : 0x7FFFFFFF;
-  const int64_t drows = p.tile ? kLimit : rows;
-  p.nt = drows <= kDecodeRows ? 1 : 2;
-  p.row_tiles = (int)ceil_div(drows, kDecodeRows * p.nt);
-  const int64_t most_blocks = 0x7FFFFFFF / (B * hkv);  // B hkv < 2^31, and so is the grid
-  if (p.row_tiles > most_blocks) p.row_tiles = (int)most_blocks;
+  p.decode_rows = p.tile || rows > kDecodeRows ? 2 * kDecodeRows : kDecodeRows;
   int64_t tiles = ceil_div(max_ctx < 1 ? 1 : max_ctx, kKvTile);
   if (window > 0) {  // q rows see up to window + q - 1 tokens, which may begin inside a tile
     const int64_t in_window = ceil_div(window + q - 1, kKvTile) + 1;
     tiles = in_window < tiles ? in_window : tiles;
   }
-  p.nsplit = p.tnsplit = 1;
-  p.chunk = p.tchunk = (int)tiles;
+  p.shares = 1;
   if (p.decode) {
-    p.most = split_plan(tiles, B * hkv * p.row_tiles, 4 * kCus, 8, &p.nsplit, &p.chunk);
-    if (p.most > 1) p.slots = p.tile ? B * hkv * kLimit : T * hq;
+    // as many blocks as run well at once, each with an equal share; one a head where the
+    // heads alone are as many
+    constexpr int64_t resident = kCus * kDecodeBlocks;
+    const int64_t most = ceil_div(B * ceil_div(p.tile ? kLimit : rows, p.decode_rows) * tiles, kLeastTiles);
+    p.shares = resident / hkv < most ? resident / hkv : most;
+    if (p.shares < 1) p.shares = 1;
   }
+  p.tnsplit = 1;
+  p.tchunk = (int)tiles;
   if (p.tile) {
     const int64_t blocks = B * hkv * ceil_div(rows, kTileRows);
-    p.tmost = split_plan(tiles, blocks, 2 * kCus, 16, &p.tnsplit, &p.tchunk);
+    int64_t n = ceil_div(2 * kCus, blocks);
+    const int64_t most = ceil_div(tiles, 16);
+    p.tmost = n > most ? most : n;  // (never falls as max_ctx grows: see the workspace)
+    p.tchunk = (int)ceil_div(tiles, p.tmost);
+    p.tnsplit = (int)ceil_div(tiles, p.tchunk);
     if (p.tmost > 1) p.tslots = T * hq;
-    p.trow_tiles = (int)ceil_div(rows, kTileRows);
-    // (split only where the blocks are few)
-    if (p.trow_tiles > most_blocks) p.trow_tiles = (int)most_blocks;
+    const int64_t most_blocks = 0x7FFFFFFF / (B * hkv);  // split only where blocks are few
+    p.trow_tiles = (int)(ceil_div(rows, kTileRows) < most_blocks ? ceil_div(rows, kTileRows) : most_blocks);
   }
   return p;
 }
 
-size_t part_bytes(int64_t slots, int64_t nsplit, int64_t D) { return (size_t)slots * nsplit * (D * 4 + 8); }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+// rows of partials, each with D sums, its reference and its sum
+int64_t decode_slots(const Plan& pl, int64_t hkv) { return pl.shares > 1 ? hkv * pl.shares * 2 * pl.decode_rows : 0; }
+size_t part_bytes(int64_t slots, int64_t D) { return round256((size_t)slots * (D * 4 + 8)); }
 
-// items: rows to look at
-template <int D>
-hipError_t combine(const KvCache& a, const AttnArgs& p, int nsplit, int64_t items, int by_sequence,
+// items: rows to look at; parts: those of a row, about
+template <int D, bool kTiled>
+hipError_t combine(const KvCache& a, const AttnArgs& p, int64_t parts, int64_t items, int by_sequence,
                    hipStream_t stream) {
-  if (nsplit <= 8)
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 1>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, p,
+  if (parts <= 8)
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 1, kTiled>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a,
+                       p, by_sequence);
+  else if (parts <= 32)
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 4, kTiled>), dim3((unsigned)items), dim3(256), 0, stream, a, p,
                        by_sequence);
-  else if (nsplit <= 32)
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 4>), dim3((unsigned)items), dim3(256), 0, stream, a, p, by_sequence);
   else
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 16>), dim3((unsigned)items), dim3(1024), 0, stream, a, p, by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 16, kTiled>), dim3((unsigned)items), dim3(1024), 0, stream, a, p,
+                       by_sequence);
   return hipGetLastError();
 }
 
 template <int D>
 hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, int64_t hkv, hipStream_t stream) {
   hipError_t e = hipSuccess;
+  const int64_t out_rows = (int64_t)a.T * p.hq;
   if (pl.tile) {
     const dim3 grid((unsigned)(B * hkv * pl.trow_tiles * pl.tnsplit));
     hipLaunchKernelGGL((kv4_tile_kernel<D>), grid, dim3(256), 0, stream, a, p, pl.trow_tiles);
     e = hipGetLastError();
   }
   if (e == hipSuccess && pl.decode) {
-    const dim3 grid((unsigned)(B * hkv * pl.row_tiles * pl.nsplit));
-    if (pl.nt == 1)
-      hipLaunchKernelGGL((kv4_decode_kernel<D, 1>), grid, dim3(256), 0, stream, a, p, pl.row_tiles);
+    const dim3 grid((unsigned)(hkv * pl.shares));
+    if (pl.decode_rows == kDecodeRows)
+      hipLaunchKernelGGL((kv4_decode_kernel<D, 1>), grid, dim3(256), 0, stream, a, p);
     else
-      hipLaunchKernelGGL((kv4_decode_kernel<D, 2>), grid, dim3(256), 0, stream, a, p, pl.row_tiles);
+      hipLaunchKernelGGL((kv4_decode_kernel<D, 2>), grid, dim3(256), 0, stream, a, p);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && pl.decode && pl.tile && pl.nsplit > 1)
-    e = combine<D>(a, p, pl.nsplit, B * hkv * p.row_limit, 1, stream);
-  if (e == hipSuccess && (pl.tile ? pl.tnsplit : pl.nsplit) > 1)
-    e = combine<D>(a, p, pl.tile ? pl.tnsplit : pl.nsplit, (int64_t)a.T * p.hq, 0, stream);
+  if (e == hipSuccess && pl.decode && pl.shares > 1)
+    e = combine<D, false>(a, p, pl.shares / B + 1, pl.tile ? B * hkv * p.row_limit : out_rows, pl.tile, stream);
+  if (e == hipSuccess && pl.tile && pl.tnsplit > 1) e = combine<D, true>(a, p, pl.tnsplit, out_rows, 0, stream);
   return e;
 }
 
@@ -847,7 +943,7 @@ hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, i
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q,
                                      int64_t max_ctx) {
   const Plan pl = make_plan(T, B, hq, hkv, max_q, max_ctx, 0);
-  return round256(part_bytes(pl.slots, pl.most, head_dim)) + round256(part_bytes(pl.tslots, pl.tmost, head_dim));
+  return part_bytes(decode_slots(pl, hkv), head_dim) + part_bytes(pl.tslots * pl.tmost, head_dim);
 }
 
 hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
@@ -862,22 +958,22 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.out = reinterpret_cast<f16*>(out);
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
+  const int64_t slots = decode_slots(pl, c.kv_heads), tslots = pl.tslots * pl.tnsplit;
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_s = reinterpret_cast<float2*>(ws + (size_t)pl.slots * pl.nsplit * head_dim * 4);
-  ws += round256(part_bytes(pl.slots, pl.most, head_dim));
+  p.part_s = reinterpret_cast<float2*>(ws + (size_t)slots * head_dim * 4);
+  ws += part_bytes(slots, head_dim);
   p.tpart_o = reinterpret_cast<float*>(ws);
-  p.tpart_s = reinterpret_cast<float2*>(ws + (size_t)pl.tslots * pl.tnsplit * head_dim * 4);
+  p.tpart_s = reinterpret_cast<float2*>(ws + (size_t)tslots * head_dim * 4);
   p.hq = (int)hq;
   p.group = (int)(hq / c.kv_heads);
   p.window = (int)window;
   p.c = scale * 1.44269504088896341f;
-  p.nsplit = pl.nsplit;
-  p.chunk_tiles = pl.chunk;
+  p.shares = (int)pl.shares;
+  p.least = (int)kLeastTiles;
+  p.decode_rows = pl.decode_rows;
   p.tnsplit = pl.tnsplit;
   p.tchunk_tiles = pl.tchunk;
-  p.decode_rows = kDecodeRows * pl.nt;
   p.row_limit = pl.row_limit;
-  p.compact = pl.tile;
   return head_dim == 128 ? run<128>(a, p, pl, c.B, c.kv_heads, stream) : run<64>(a, p, pl, c.B, c.kv_heads, stream);
 }
 
