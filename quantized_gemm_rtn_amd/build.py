@@ -26,7 +26,8 @@ PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
 
 SOURCES = ["wq_api.hip", "split.hip", "quant.hip", "gemv.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip",
-           "lowrank.hip", "actorder.hip", "w4a8.hip", "norm.hip", "kv4_cache.hip", "kv4_attention.hip"]
+           "lowrank.hip", "actorder.hip", "w4a8.hip", "norm.hip", "kv4_cache.hip", "kv4_attention.hip",
+           "kv4_tile.hip"]
 
 COMMON = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -43,11 +44,12 @@ COMMON = [
 # The attention's accumulators stay in vector registers, where the rescaling reads them.
 PER_FILE = {"quant.hip": ["-ffp-contract=off"], "split.hip": ["-ffp-contract=off"],
             "kv4_cache.hip": ["-ffp-contract=off"], "kv4_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+            "kv4_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
             "w4a8.hip": ["-ffp-contract=off", "-mllvm", "-amdgpu-mfma-vgpr-form"]}
 # The product kernels must keep everything in registers and LDS: the compiler
 # reports each kernel's per-lane scratch, and any use of it fails the build.
 NO_SCRATCH = {"gemv.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip", "lowrank.hip", "w4a8.hip", "norm.hip",
-              "kv4_cache.hip", "kv4_attention.hip"}
+              "kv4_cache.hip", "kv4_attention.hip", "kv4_tile.hip"}
 RESOURCE_REMARK = "-Rpass-analysis=kernel-resource-usage"
 
 

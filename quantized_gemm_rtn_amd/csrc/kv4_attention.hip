@@ -26,66 +26,13 @@
 //  kv4_decode_kernel   few query rows (16 or 32 a block): all tiles of all sequences are
 //    dealt out in equal shares, one a block, whose four waves take tiles of 32 tokens in
 //    turn and join through LDS at each row tile's end.
-//  kv4_tile_kernel     many query rows: 128 a block; a tile of codes is turned into exact
-//    fp16 integers once, in LDS, for all of them.
+//  kv4_tile_kernel     many query rows: 128 a block; a tile of codes is turned into
+//    exact fp16 integers once, in LDS, for all of them.
 //  kv4_combine_kernel  joins the parts of rows that more than one block worked on.
-#include "kv4.h"
+#include "kv4_attention.h"
 #include "wq_launch.h"
 
 namespace wq {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-
-constexpr float kNoRef = -1e30f;      // reference of a row that has seen nothing
-constexpr float kTop = 10.0f;         // log2 of the largest weight times value scale after a move of r,
-constexpr float kSlack = 4.0f;        // and how far it may grow before the next
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kDecodeRows = 16;       // query rows of one column tile
-constexpr int kTileRows = 128;        // query rows of a block of kv4_tile_kernel
-
-struct AttnArgs {
-  const f16* q;
-  int64_t q_stride;
-  const uint8_t* cache;
-  f16* out;
-  float* lse;         // may be null
-  float* part_o;      // partials of the decode kernel, two a block: [block][2][rows][D]
-  float2* part_s;     // [block][2][rows]: r, sum
-  float* tpart_o;     // partials of the tile kernel: [T * hq][tnsplit][D]
-  float2* tpart_s;    // [T * hq][tnsplit]
-  int hq, group;      // query heads, and those of one key/value head
-  int window;         // 0: none
-  float c;            // scale * log2(e)
-  int shares, least;  // decode kernel: blocks a head, and the fewest tiles of one
-  int decode_rows;    // rows of an item of the decode kernel (16 or 32)
-  int tnsplit, tchunk_tiles;  // tile kernel: most chunks of a row, and their tiles
-  int row_limit;      // sequences with more rows of a head belong to the tile kernel
-};
-
-// Tiles [t0, t1) of a sequence that rows row0 .. row1 (of one head group) can see.
-struct TileRange {
-  int t0, t1;
-};
-__device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& p, int row0, int row1) {
-  const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
-  const int lo = p.window > 0 ? max(p0 - p.window + 1, 0) : 0;
-  TileRange r;
-  r.t0 = lo / kKvTile;
-  r.t1 = p1 < lo ? r.t0 : p1 / kKvTile + 1;
-  return r;
-}
-// ... and the tile kernel's chunks of them
-struct TileSplit {
-  int chunk, splits;
-};
-__device__ __forceinline__ TileSplit tile_split(const TileRange& r, const AttnArgs& p) {
-  const int n = r.t1 - r.t0;
-  TileSplit t;
-  t.chunk = max(p.tchunk_tiles, (n + p.tnsplit - 1) / p.tnsplit);
-  t.splits = (n + t.chunk - 1) / t.chunk;
-  return t;
-}
 
 // The decode kernel's work: its items are a sequence's row tiles, in order, each as many
 // steps as the sequence has visible tiles (one where it has none: its rows are still to
@@ -108,17 +55,8 @@ __device__ __forceinline__ Sequences load_sequences(const KvCache& a, const Attn
   q.t0 = r.t0;
   q.n = mine ? max(r.t1 - r.t0, 1) : 0;
   q.steps = (int64_t)q.n * ((rows + p.decode_rows - 1) / p.decode_rows);
-  q.upto = q.steps;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t v = __shfl_up(q.upto, off);
-    q.upto += lane >= off ? v : 0;
-  }
+  q.upto = wave_sums_upto(q.steps, lane);
   return q;
-}
-__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
-  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
-                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
 }
 // steps of a head in all; `q` holds the first 64 sequences
 __device__ __forceinline__ int64_t total_steps(const KvCache& a, const AttnArgs& p, const Sequences& q, int lane) {
@@ -130,21 +68,6 @@ __device__ __forceinline__ int64_t share_steps(const AttnArgs& p, int64_t total)
   const int64_t n = total < (int64_t)1 << 31 ? (int64_t)((uint32_t)(total + p.shares - 1) / (uint32_t)p.shares)
                                              : (total + p.shares - 1) / p.shares;
   return n < p.least ? p.least : n;
-}
-
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// a * b with the fp16 factor read as it is (one mixed-precision instruction; the sum with
-// 0 keeps the compiler from splitting it into a conversion and a product)
-__device__ __forceinline__ float mul_mix(float a, f16 b) { return __builtin_fmaf(a, (float)b, 0.0f); }
-
-// largest of eight positive fp16 values, as bits (positive fp16 order like integers)
-__device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
-  const uint4 d = __builtin_bit_cast(uint4, v);
-  const u16x2 a = __builtin_elementwise_max(__builtin_bit_cast(u16x2, d.x), __builtin_bit_cast(u16x2, d.y));
-  const u16x2 b = __builtin_elementwise_max(__builtin_bit_cast(u16x2, d.z), __builtin_bit_cast(u16x2, d.w));
-  const u16x2 m = __builtin_elementwise_max(a, b);
-  return max((uint32_t)m.x, (uint32_t)m.y);
 }
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -496,228 +419,10 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(256)
-kv4_tile_kernel(KvCache a, AttnArgs p, int row_tiles) {
-  constexpr int KS = D / 16;   // steps of the first product
-  constexpr int CT = D / 32;   // channel tiles of the second
-  constexpr int RUNS = D / 64;
-  // two tiles of 32 tokens: keys [step][lane], values [step][channel tile][lane], 16
-  // bytes each, and the tiles' scales
-  __shared__ __align__(16) uint4 kl[2][KS][64], vl[2][2][CT][64];
-  __shared__ __align__(16) uint4 ksl[2][4], vsl[2][4];
-  const int lane = threadIdx.x & 63, c = lane & 31, hl = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // heads next to each other: with eight of them, each XCD's L2 serves one
-  const int h = blockIdx.x % a.hkv, split = blockIdx.x / a.hkv % p.tnsplit;
-  const int rest = blockIdx.x / a.hkv / p.tnsplit;
-  const int b = rest / row_tiles;
-  const KvSeq s = kv_sequence(a, b);
-  const int rows = s.rows * p.group;
-  if (rows <= p.row_limit) return;
-  const int have = (rows + kTileRows - 1) / kTileRows;
-  // the last rows see the most tokens: they start first
-  for (int back = rest % row_tiles; back < have; back += row_tiles) {
-    const int rt = have - 1 - back;
-    const int row0 = rt * kTileRows, row1 = min(rows, row0 + kTileRows) - 1;
-    const TileRange range = tile_range(s, p, row0, row1);
-    const TileSplit parts = tile_split(range, p);
-    if (split > 0 && split >= parts.splits) continue;
-    const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
-    const int row = row0 + 32 * wave + c;
-    const bool valid = row < rows;
-    const int tok = valid ? row / p.group : 0;
-    const int head = h * p.group + (valid ? row - tok * p.group : 0);
-    const int pos = valid ? s.ctx - s.rows + tok : -1;
-    f16x8 qf[KS];
-    const f16* qp = p.q + (int64_t)(s.first_row + tok) * p.q_stride + head * D + 8 * hl;
-#pragma unroll
-    for (int w = 0; w < KS; ++w) {
-      uint4 d = *reinterpret_cast<const uint4*>(qp + 16 * w);
-      if (!valid) d = uint4{0, 0, 0, 0};
-      qf[w] = as_f16x8(perm_x8(d));
-    }
-    f32x16 acc[CT];
-#pragma unroll
-    for (int t = 0; t < CT; ++t) acc[t] = f32x16{};
-    float ref = kNoRef, sum = 0.0f, vexp = 0.0f;
-    uint32_t vbits = 0;
-
-    const int begin = range.t0 + split * parts.chunk, end = min(range.t1, begin + parts.chunk);
-    // each wave turns one tile's keys or values into LDS operands: waves 0, 1 the first
-    // tile's, waves 2, 3 the second's
-    const int sub = wave >> 1;
-    const bool is_v = wave & 1;
-    const int g = lane >> 4, c16 = lane & 15;
-    uint4 data[RUNS], scales, zeros;
-    const auto load = [&](int tile) {
-      tile = min(tile, end - 1);  // past the range: loaded again, and masked by position
-      const int page = tile / a.page_tiles;
-      const uint8_t* base = p.cache + kv_page_offset(a, b, h, page) +
-                            (int64_t)(tile - page * a.page_tiles) * kv_tile_bytes<D>();
-      const int off = is_v ? kv_value_offset<D>() : kv_key_offset<D>();
-#pragma unroll
-      for (int i = 0; i < RUNS; ++i) data[i] = *reinterpret_cast<const uint4*>(base + off + 1024 * i + 16 * lane);
-      const uint8_t* meta = base + kv_meta_offset<D>(is_v ? 2 : 0);
-      scales = *reinterpret_cast<const uint4*>(meta + 16 * (lane & 3));
-      if (is_v)
-        zeros = *reinterpret_cast<const uint4*>(meta + 64 + 16 * g);
-      else
-        zeros.x = *reinterpret_cast<const uint32_t*>(meta + 64 + 4 * c16);
-    };
-    const uint32_t magic = magic_1024x2();
-    const auto stash = [&]() {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&data[0]);
-      if (!is_v) {
-        const KeyZeros kz = kv_key_zeros(zeros.x);
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const int block = (D / 32) * g + i;  // eight channels
-            kl[sub][block >> 1][32 * (block & 1) + 16 * half + c16] =
-                codes_minus_zero_x16(w[(D / 32) * half + i], magic, kz.bias[half], kz.nbias16[half]);
-          }
-        if (lane < 4) ksl[sub][lane] = scales;
-      } else {
-        // what stands past the cache's end may be anything; its weight is 0
-        zeros = kv_value_zeros_finite(zeros);
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t)
-          vl[sub][g >> 1][t >> 1][32 * (g & 1) + 16 * (t & 1) + c16] =
-              __builtin_bit_cast(uint4, kv_value_operand(w[t], magic, zeros));
-        if (lane < 4) vsl[sub][lane] = scales;
-      }
-    };
-
-    if (begin < end) load(begin + sub);
-    for (int tile = begin; tile < end; tile += 2) {
-      __syncthreads();  // the previous tiles have been read
-      stash();
-      __syncthreads();
-      if (tile + 2 < end) load(tile + 2 + sub);
-
-      f32x16 sc[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        sc[u] = f32x16{};
-#pragma unroll
-        for (int w = 0; w < KS; ++w)
-          sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16x8(kl[u][w][lane]), qf[w], sc[u], 0, 0, 0);
-      }
-      // the lane's tokens: 8 q + 4 hl + i of a tile in register 4 q + i; quads q and
-      // q + 2 (q = 0, 1) are one run of scales
-      f16x8 vs[2][2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const f16x8 ks = as_f16x8(ksl[u][2 * q + hl]);
-          vs[u][q] = as_f16x8(vsl[u][2 * q + hl]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = 4 * (q + 2 * (e >> 2)) + (e & 3);
-            sc[u][r] = mul_mix(sc[u][r], ks[e]);
-          }
-        }
-      const int first = tile * kKvTile;
-      const bool edge = first + 2 * kKvTile - 1 > p0 || (p.window > 0 && first <= p1 - p.window) || tile + 1 >= end;
-      if (edge) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int t = first + 32 * u + 8 * (e >> 2) + 4 * hl + (e & 3);
-            const bool see = t <= pos && (p.window == 0 || t > pos - p.window) && tile + u < end;
-            sc[u][e] = see ? sc[u][e] : -INFINITY;
-          }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              vs[u][q][e] = sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)] == -INFINITY ? (f16)0.0f : vs[u][q][e];
-      }
-      float mx = -INFINITY;
-      uint32_t vmax = 0;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[u][e]);
-        vmax = max(vmax, max(max_bits8(vs[u][0]), max_bits8(vs[u][1])));
-      }
-      mx *= p.c;
-      if (__any(vmax > vbits || mx + vexp - kTop > ref + kSlack)) {
-        uint32_t top = vmax;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-        float grown = 0.0f;
-        if (top > vbits) {
-          const float ve = (float)((int)(top >> 10) + 1 - 15);
-          grown = vbits == 0 ? 0.0f : ve - vexp;
-          vexp = ve;
-          vbits = ((top >> 10) << 10) | 0x3FFu;
-        }
-        const float m = fmaxf(mx, __shfl_xor(mx, 32));
-        const float to = fmaxf(ref + grown, m + vexp - kTop);
-        const float f = exp2_hw(ref - to);
-        ref = to;
-        sum *= f;
-#pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] *= f;
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          f16x8 wf;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float w = exp2_hw(__builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], p.c, -ref));
-            sum += w;
-            wf[2 * (e & 3) + (e >> 2)] = (f16)mul_mix(w, vs[u][q][e]);
-          }
-#pragma unroll
-          for (int t = 0; t < CT; ++t)
-            acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16x8(vl[u][q][t][lane]), wf, acc[t], 0, 0, 0);
-        }
-    }
-    sum += __shfl_xor(sum, 32);
-    if (valid) {
-      const int64_t slot = (int64_t)(s.first_row + tok) * p.hq + head;
-      if (parts.splits > 1) {
-        const int64_t at = slot * p.tnsplit + split;
-        float* dst = p.tpart_o + at * D + 4 * hl;
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4*>(dst + 32 * t + 8 * q) =
-                f32x4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]};
-        if (hl == 0) p.tpart_s[at] = make_float2(ref, sum);
-      } else {
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        f16* dst = p.out + slot * D + 4 * hl;
-        typedef f16 f16x4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f16x4*>(dst + 32 * t + 8 * q) =
-                f16x4{(f16)(acc[t][4 * q] * inv), (f16)(acc[t][4 * q + 1] * inv), (f16)(acc[t][4 * q + 2] * inv),
-                      (f16)(acc[t][4 * q + 3] * inv)};
-        if (hl == 0 && p.lse != nullptr) p.lse[slot] = sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
-      }
-    }
-  }
-}
-
-// Joins the partials of rows that were split: those of the decode kernel (kTiled false)
-// or of the tile kernel. W waves per row (1, 4 or 16, so that a wave takes about eight);
+// Joins the decode kernel's partials of rows that were split. W waves per row (1, 4 or 16, so that a wave takes about eight);
 // rows that are already written are left alone. by_sequence: the rows looked at are the
 // first row_limit of each sequence and head, not all of the output.
-template <int D, int W, bool kTiled>
+template <int D, int W>
 __global__ void __launch_bounds__(W < 4 ? 256 : 64 * W)
 kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
   constexpr int ROWS = W < 4 ? 4 / W : 1;  // rows of a block
@@ -755,53 +460,33 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
     row = tok * p.group + head % p.group;
   }
   const int rows = s.rows * p.group;
-  if ((rows > p.row_limit) != kTiled) return;
+  if (rows > p.row_limit) return;
   const int64_t out_row = (int64_t)(s.first_row + row / p.group) * p.hq + h * p.group + row % p.group;
 
-  // the row's partials: number i is at base + i * stride, but the first at `start`
-  int parts;
-  int64_t start, base, stride;
-  const float* po;
-  const float2* ps;
-  if constexpr (kTiled) {
-    const int row0 = row / kTileRows * kTileRows, row1 = min(rows, row0 + kTileRows) - 1;
-    parts = tile_split(tile_range(s, p, row0, row1), p).splits;
-    start = base = out_row * p.tnsplit;
-    stride = 1;
-    po = p.tpart_o;
-    ps = p.tpart_s;
-  } else {
-    Sequences q = load_sequences(a, p, 0, lane);
-    const int64_t per = share_steps(p, total_steps(a, p, q, lane));
-    int64_t before = 0;
-    for (int first = 64; first <= b; first += 64) {
-      before += lane_value(q.upto, 63);
-      q = load_sequences(a, p, first, lane);
-    }
-    const int n = __builtin_amdgcn_readlane(q.n, b & 63);
-    const int64_t from = before + lane_value(q.upto - q.steps, b & 63) + (int64_t)(row / p.decode_rows) * n;
-    const int64_t i0 = from / per, i1 = (from + n - 1) / per;
-    parts = (int)(i1 - i0) + 1;
-    // share i of head h is block i * hkv + h, two partials each: the share that the item
-    // begins inside has it second
-    const auto slot = [&](int64_t i, int second) {
-      return ((i * a.hkv + h) * 2 + second) * p.decode_rows + row % p.decode_rows;
-    };
-    base = slot(i0, 0);
-    stride = (int64_t)a.hkv * 2 * p.decode_rows;
-    start = slot(i0, from > i0 * per);
-    po = p.part_o;
-    ps = p.part_s;
+  // the row's partials: those of shares i0 .. i1 of its head. Share i is block i * hkv + h,
+  // with two partials: an item that begins inside the share comes second.
+  Sequences q = load_sequences(a, p, 0, lane);
+  const int64_t per = share_steps(p, total_steps(a, p, q, lane));
+  int64_t before = 0;
+  for (int first = 64; first <= b; first += 64) {
+    before += lane_value(q.upto, 63);
+    q = load_sequences(a, p, first, lane);
   }
+  const int n = __builtin_amdgcn_readlane(q.n, b & 63);
+  const int64_t X = before + lane_value(q.upto - q.steps, b & 63) + (int64_t)(row / p.decode_rows) * n;
+  const int64_t i0 = X / per;
+  const int parts = (int)((X + n - 1) / per - i0) + 1;
   if (parts <= 1) return;
-  const auto place = [&](int i) { return i == 0 ? start : base + i * stride; };
+  const auto place = [&](int i) {
+    return (((i0 + i) * a.hkv + h) * 2 + (i == 0 && X > i0 * per ? 1 : 0)) * p.decode_rows + row % p.decode_rows;
+  };
   // every wave finds the row's reference and sum, a partial a lane
   float best = kNoRef, total = 0.0f;
-  for (int i = lane; i < parts; i += 64) best = fmaxf(best, ps[place(i)].x);
+  for (int i = lane; i < parts; i += 64) best = fmaxf(best, p.part_s[place(i)].x);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) best = fmaxf(best, __shfl_xor(best, off));
   for (int i = lane; i < parts; i += 64) {
-    const float2 v = ps[place(i)];
+    const float2 v = p.part_s[place(i)];
     total = __builtin_fmaf(v.y, exp2_hw(v.x - best), total);
   }
 #pragma unroll
@@ -812,9 +497,9 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
 #pragma unroll 8
   for (int i = W == 1 ? 0 : wave; i < parts; i += W) {
     const int64_t at = place(i);
-    const float f = exp2_hw(ps[at].x - best);
+    const float f = exp2_hw(p.part_s[at].x - best);
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(po[at * D + N * lane + e], f, o[e]);
+    for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(p.part_o[at * D + N * lane + e], f, o[e]);
   }
   if constexpr (W > 1) {
 #pragma unroll
@@ -845,9 +530,8 @@ struct Plan {
   bool decode, tile;  // which kernels run
   int decode_rows, row_limit;
   int64_t shares;     // decode kernel: blocks a head
-  int trow_tiles;     // tile kernel: row tiles of a sequence that get blocks of their own
-  int tnsplit, tchunk;
-  int64_t tslots, tmost;  // rows of its partials (0: not split), and a bound of tnsplit
+  int64_t tshares, most_tshares;  // tile kernel: the same (0: whole row tiles), and its bound
+  int row_tiles, snake;
 };
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
@@ -857,7 +541,12 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
   const int64_t group = hq / hkv;
   const int64_t q = max_q < 1 ? 1 : (max_q > T ? T : max_q);
   const int64_t rows = q * group;
-  constexpr int64_t kLimit = 2 * kDecodeRows;
+  // Rows of a sequence and head up to which the decode kernel (32 rows an item, the cache
+  // read once for each) beats the tile kernel (128 rows, whether there or not): with 64
+  // rows 32 against 47 us (8 sequences of 4000 tokens, 4 heads), 25 against 51 us (one of
+  // 20000); with 96 38 and 41, 34 and 69 us; with 128 rows it is 43 and 53 there, but 129
+  // and 111 us for 32 sequences of 4000 tokens and 8 heads.
+  constexpr int64_t kLimit = 96;
   // a sequence's rows decide its kernel; from the host only the largest is known, and
   // that all are alike where there is one sequence or B max_q new tokens
   p.tile = rows > kLimit;
@@ -878,18 +567,29 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
     p.shares = resident / hkv < most ? resident / hkv : most;
     if (p.shares < 1) p.shares = 1;
   }
-  p.tnsplit = 1;
-  p.tchunk = (int)tiles;
   if (p.tile) {
-    const int64_t blocks = B * hkv * ceil_div(rows, kTileRows);
-    int64_t n = ceil_div(2 * kCus, blocks);
-    const int64_t most = ceil_div(tiles, 16);
-    p.tmost = n > most ? most : n;  // (never falls as max_ctx grows: see the workspace)
-    p.tchunk = (int)ceil_div(tiles, p.tmost);
-    p.tnsplit = (int)ceil_div(tiles, p.tchunk);
-    if (p.tmost > 1) p.tslots = T * hq;
-    const int64_t most_blocks = 0x7FFFFFFF / (B * hkv);  // split only where blocks are few
-    p.trow_tiles = (int)(ceil_div(rows, kTileRows) < most_blocks ? ceil_div(rows, kTileRows) : most_blocks);
+    // Whole row tiles, or equal shares of them: shares keep every CU busy to the end, but
+    // cost partials (written, read and joined, some 50 000 cycles in all). In cycles, with
+    // 5400 measured for two blocks' steps of 64 tokens on a CU and 4200 for one alone, from
+    // bounds: all rows at most, each sequence as long as the longest.
+    const int64_t per_seq = ceil_div(rows, kTileRows), by_rows = ceil_div(T * group, kTileRows) + B;
+    const int64_t blocks = hkv * (B * per_seq < by_rows ? B * per_seq : by_rows);
+    const double longest = (double)ceil_div(tiles, 2);
+    const double mean = window > 0 ? longest : (longest > (double)q / 128 ? longest - (double)q / 128 : longest / 2);
+    const double shared = blocks * mean / (2 * kCus) * 5400 + 50000;
+    double whole = blocks * mean / (2 * kCus) * 5400 + longest * 2100;
+    if (blocks <= 2 * kCus) whole = longest * 4200 > mean * 5400 ? longest * 4200 : mean * 5400;
+    if (blocks <= kCus) whole = longest * 4200;
+    const int64_t most = ceil_div(T * group * tiles, (int64_t)kLeastItemTiles * kTileRows) + 1;
+    const int64_t most_blocks = 0x7FFFFFFF / (B * hkv);  // B hkv < 2^31, and so is the grid
+    const int64_t fit = 2 * kCus / hkv < 1 ? 1 : 2 * kCus / hkv;
+    p.tshares = fit < most ? fit : most;
+    p.most_tshares = p.tshares;
+    if (whole <= shared) {
+      p.tshares = 0;
+      p.row_tiles = (int)(per_seq < most_blocks ? per_seq : most_blocks);
+      p.snake = B * hkv * per_seq <= 2 * kCus;
+    }
   }
   return p;
 }
@@ -897,33 +597,27 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // rows of partials, each with D sums, its reference and its sum
 int64_t decode_slots(const Plan& pl, int64_t hkv) { return pl.shares > 1 ? hkv * pl.shares * 2 * pl.decode_rows : 0; }
+int64_t tile_slots(const Plan& pl, int64_t hkv) { return hkv * pl.most_tshares * 2 * kTileRows; }
 size_t part_bytes(int64_t slots, int64_t D) { return round256((size_t)slots * (D * 4 + 8)); }
 
 // items: rows to look at; parts: those of a row, about
-template <int D, bool kTiled>
+template <int D>
 hipError_t combine(const KvCache& a, const AttnArgs& p, int64_t parts, int64_t items, int by_sequence,
                    hipStream_t stream) {
   if (parts <= 8)
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 1, kTiled>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a,
-                       p, by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 1>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, p,
+                       by_sequence);
   else if (parts <= 32)
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 4, kTiled>), dim3((unsigned)items), dim3(256), 0, stream, a, p,
-                       by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 4>), dim3((unsigned)items), dim3(256), 0, stream, a, p, by_sequence);
   else
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 16, kTiled>), dim3((unsigned)items), dim3(1024), 0, stream, a, p,
-                       by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 16>), dim3((unsigned)items), dim3(1024), 0, stream, a, p, by_sequence);
   return hipGetLastError();
 }
 
 template <int D>
 hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, int64_t hkv, hipStream_t stream) {
   hipError_t e = hipSuccess;
-  const int64_t out_rows = (int64_t)a.T * p.hq;
-  if (pl.tile) {
-    const dim3 grid((unsigned)(B * hkv * pl.trow_tiles * pl.tnsplit));
-    hipLaunchKernelGGL((kv4_tile_kernel<D>), grid, dim3(256), 0, stream, a, p, pl.trow_tiles);
-    e = hipGetLastError();
-  }
+  if (pl.tile) e = launch_kv4_tile(a, p, D, stream);
   if (e == hipSuccess && pl.decode) {
     const dim3 grid((unsigned)(hkv * pl.shares));
     if (pl.decode_rows == kDecodeRows)
@@ -933,8 +627,7 @@ hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, i
     e = hipGetLastError();
   }
   if (e == hipSuccess && pl.decode && pl.shares > 1)
-    e = combine<D, false>(a, p, pl.shares / B + 1, pl.tile ? B * hkv * p.row_limit : out_rows, pl.tile, stream);
-  if (e == hipSuccess && pl.tile && pl.tnsplit > 1) e = combine<D, true>(a, p, pl.tnsplit, out_rows, 0, stream);
+    e = combine<D>(a, p, pl.shares / B + 1, pl.tile ? B * hkv * p.row_limit : (int64_t)a.T * p.hq, pl.tile, stream);
   return e;
 }
 
@@ -943,7 +636,7 @@ hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, i
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q,
                                      int64_t max_ctx) {
   const Plan pl = make_plan(T, B, hq, hkv, max_q, max_ctx, 0);
-  return part_bytes(decode_slots(pl, hkv), head_dim) + part_bytes(pl.tslots * pl.tmost, head_dim);
+  return part_bytes(decode_slots(pl, hkv), head_dim) + part_bytes(tile_slots(pl, hkv), head_dim);
 }
 
 hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
@@ -958,7 +651,7 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.out = reinterpret_cast<f16*>(out);
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  const int64_t slots = decode_slots(pl, c.kv_heads), tslots = pl.tslots * pl.tnsplit;
+  const int64_t slots = decode_slots(pl, c.kv_heads), tslots = pl.tshares > 1 ? tile_slots(pl, c.kv_heads) : 0;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_s = reinterpret_cast<float2*>(ws + (size_t)slots * head_dim * 4);
   ws += part_bytes(slots, head_dim);
@@ -971,8 +664,9 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.shares = (int)pl.shares;
   p.least = (int)kLeastTiles;
   p.decode_rows = pl.decode_rows;
-  p.tnsplit = pl.tnsplit;
-  p.tchunk_tiles = pl.tchunk;
+  p.tshares = (int)pl.tshares;
+  p.row_tiles = pl.row_tiles;
+  p.snake = pl.snake;
   p.row_limit = pl.row_limit;
   return head_dim == 128 ? run<128>(a, p, pl, c.B, c.kv_heads, stream) : run<64>(a, p, pl, c.B, c.kv_heads, stream);
 }

@@ -566,6 +566,9 @@ int wq_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t q_h
   if (q_heads % kv_heads != 0 || q_stride < q_heads * head_dim || max_q < 0 || max_ctx < 0 || max_ctx > kMaxContext ||
       window < 0 || window >= kMax32)
     return WQ_ERR_SHAPE;
+  // sums over rows of the tokens they see, in units of 1 / (2 group), stay below 2^62
+  const int64_t group = q_heads / kv_heads;
+  if ((double)(T * group) * (double)(max_pages * page_tokens) * (double)(2 * group) > 4.0e18) return WQ_ERR_SHAPE;
   if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 8) || !aligned(lse, 4)) return WQ_ERR_ALIGN;
   if (T == 0 || B == 0) return WQ_OK;
   const size_t need = wq::kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx);
