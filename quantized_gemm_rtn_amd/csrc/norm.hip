@@ -10,14 +10,13 @@
 // One block per row. A thread holds its channels of the row in registers between the
 // three steps (sum of squares, amax, output), so x and residual are read once and each
 // output is written once: 2 + 2 bytes in and 2 + 1 (INT8) or 2 + 2 (fp16) out per
-// channel. Rows longer than kNormThreads * 16 * kNormUnits channels re-read them.
+// channel. Rows longer than a block's threads hold (32768 channels) are read again.
 #include "wq_device.h"
 #include "wq_launch.h"
 
 namespace wq {
 
 constexpr int kNormThreads = 1024;  // at most; a multiple of 64 that covers K / 16 units
-constexpr int kNormUnits = 2;       // units of 16 channels a thread may hold
 constexpr int kNormOutliers = 16;
 
 // 16 consecutive channels in float32: two 16-byte loads a tensor
@@ -70,11 +69,20 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
   return r;
 }
 
-// bit e set: channel 16 unit + e is an outlier
-__device__ __forceinline__ uint32_t unit_outliers(int unit, const int* o, int n_out) {
+// bit e set: channel 16 unit + e is an outlier. o: the list, one a lane (lane j the j-th),
+// -1 past its end; it stays in registers and every lane sees it through scalar reads.
+__device__ __forceinline__ uint32_t unit_outliers(int unit, int o, int n_out) {
   uint32_t m = 0;
-  for (int j = 0; j < n_out; ++j) m |= (o[j] >> 4) == unit ? 1u << (o[j] & 15) : 0u;
+  for (int j = 0; j < n_out; ++j) {
+    const int ch = __builtin_amdgcn_readlane(o, j);
+    m |= (ch >> 4) == unit ? 1u << (ch & 15) : 0u;
+  }
   return m;
+}
+// the lane's entry of the list; an index outside [0, K) is clamped
+__device__ __forceinline__ int load_outlier(const int32_t* outliers, int n_out, int K) {
+  const int j = threadIdx.x & 63;
+  return j < n_out ? min(max(outliers[j], 0), K - 1) : -1;
 }
 
 // Eight INT8 values of channels e0, e1, .. as bytes: y * inv + 1.5 * 2^23 rounds half to
@@ -90,99 +98,111 @@ __device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d
   return ab | cd;
 }
 
-template <bool kInt8>
+// kUnits: units of 16 channels a thread holds; kLong: the row has more than those.
+template <bool kInt8, int kUnits, bool kLong>
 __global__ void __launch_bounds__(kNormThreads)
-add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ weight,
-                   int64_t M, int K, float eps, const int32_t* __restrict__ outliers, int n_out, f16* hout,
-                   f16* __restrict__ y, int8_t* __restrict__ xq, float* __restrict__ sx, f16* __restrict__ xo) {
+add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ weight, int64_t M, int K, float eps,
+                   const int32_t* __restrict__ outliers, int n_out, f16* hout, f16* __restrict__ y,
+                   int8_t* __restrict__ xq, float* __restrict__ sx, f16* __restrict__ xo) {
   __shared__ float red_sum[kNormThreads / 64], red_max[kNormThreads / 64];
-  __shared__ int o[kNormOutliers];
   const int units = K >> 4, nt = (int)blockDim.x, t = (int)threadIdx.x;
-  // an index outside [0, K) is clamped here, once, for the mask and for xo alike
-  if (kInt8 && t < n_out) o[t] = min(max(outliers[t], 0), K - 1);
+  const int o = kInt8 ? load_outlier(outliers, n_out, K) : -1;
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const size_t row = (size_t)m * K;
-    float h[kNormUnits][16];
+    float h[kUnits][16];
+    f16x8 w[kUnits][2];
     float sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kNormUnits; ++u) {
+    for (int u = 0; u < kUnits; ++u) {
       const int unit = t + u * nt;
       if (unit < units) {
         load_h(x, residual, row + 16 * unit, h[u]);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum = __builtin_fmaf(h[u][e], h[u][e], sum);
+        w[u][0] = as_f16x8(*reinterpret_cast<const uint4*>(weight + 16 * unit));
+        w[u][1] = as_f16x8(*reinterpret_cast<const uint4*>(weight + 16 * unit + 8));
       }
     }
-    for (int unit = t + kNormUnits * nt; unit < units; unit += nt) {
-      float g[16];
-      load_h(x, residual, row + 16 * unit, g);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sum = __builtin_fmaf(g[e], g[e], sum);
+    // an outlier channel's y is found again from its own h by the j-th thread
+    float oh = 0.0f, ow = 0.0f;
+    if (kInt8 && t < n_out) {
+      oh = (float)x[row + o];
+      if (residual != nullptr) oh += (float)residual[row + o];
+      ow = (float)weight[o];
     }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+      if (t + u * nt < units)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum = __builtin_fmaf(h[u][e], h[u][e], sum);
+    if constexpr (kLong)
+      for (int unit = t + kUnits * nt; unit < units; unit += nt) {
+        float g[16];
+        load_h(x, residual, row + 16 * unit, g);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum = __builtin_fmaf(g[e], g[e], sum);
+      }
     sum = block_reduce<false>(sum, red_sum);
     const float r = 1.0f / sqrtf(sum / (float)K + eps);
 
-    // channel unit -> h out, and y in place of h
-    const auto normalize = [&](float* v, int unit) {
-      if (hout != nullptr) store16(hout + row + 16 * unit, v);
-      float w[16];
-      load16(weight + 16 * unit, w);
+    const auto scale = [&](float* v, const f16x8* f) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
+      for (int e = 0; e < 16; ++e) v[e] = v[e] * r * (float)f[e >> 3][e & 7];
     };
+    // a unit past the ones held: h and its weights again
+    const auto reload = [&](float* g, int unit, bool write_h) {
+      load_h(x, residual, row + 16 * unit, g);
+      const f16x8 f[2] = {as_f16x8(*reinterpret_cast<const uint4*>(weight + 16 * unit)),
+                          as_f16x8(*reinterpret_cast<const uint4*>(weight + 16 * unit + 8))};
+      if (write_h && hout != nullptr) store16(hout + row + 16 * unit, g);
+      scale(g, f);
+    };
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int unit = t + u * nt;
+      if (unit < units) {
+        if (hout != nullptr) store16(hout + row + 16 * unit, h[u]);
+        scale(h[u], w[u]);
+      }
+    }
     if constexpr (!kInt8) {
 #pragma unroll
-      for (int u = 0; u < kNormUnits; ++u) {
-        const int unit = t + u * nt;
-        if (unit < units) {
-          normalize(h[u], unit);
-          store16(y + row + 16 * unit, h[u]);
+      for (int u = 0; u < kUnits; ++u)
+        if (t + u * nt < units) store16(y + row + 16 * (t + u * nt), h[u]);
+      if constexpr (kLong)
+        for (int unit = t + kUnits * nt; unit < units; unit += nt) {
+          float g[16];
+          reload(g, unit, true);
+          store16(y + row + 16 * unit, g);
         }
-      }
-      for (int unit = t + kNormUnits * nt; unit < units; unit += nt) {
-        float g[16];
-        load_h(x, residual, row + 16 * unit, g);
-        normalize(g, unit);
-        store16(y + row + 16 * unit, g);
-      }
     } else {
       float amax = 0.0f;
-      // y of the unit; its outlier channels are handed to xo and then count as 0
-      const auto split = [&](float* v, int unit) {
+      // outlier channels count as 0
+      const auto clear = [&](float* v, int unit) {
         const uint32_t om = unit_outliers(unit, o, n_out);
-        if (om != 0) {
-          for (int j = 0; j < n_out; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (o[j] == 16 * unit + e) xo[m * kNormOutliers + j] = (f16)v[e];
+        if (om != 0)
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = (om >> e) & 1u ? 0.0f : v[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
       };
 #pragma unroll
-      for (int u = 0; u < kNormUnits; ++u) {
-        const int unit = t + u * nt;
-        if (unit < units) {
-          normalize(h[u], unit);
-          split(h[u], unit);
-        }
-      }
-      // (a long row's further units: h stays unwritten until the last pass reads them again)
-      for (int unit = t + kNormUnits * nt; unit < units; unit += nt) {
-        float g[16], w[16];
-        load_h(x, residual, row + 16 * unit, g);
-        load16(weight + 16 * unit, w);
+      for (int u = 0; u < kUnits; ++u)
+        if (t + u * nt < units) {
+          clear(h[u], t + u * nt);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = g[e] * r * w[e];
-        split(g, unit);
-      }
+          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(h[u][e]));
+        }
+      // (a long row's further units: h stays unwritten until the last pass reads them again)
+      if constexpr (kLong)
+        for (int unit = t + kUnits * nt; unit < units; unit += nt) {
+          float g[16];
+          reload(g, unit, false);
+          clear(g, unit);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(g[e]));
+        }
       amax = block_reduce<true>(amax, red_max);
       const float s = amax > 0.0f ? amax / 127.0f : 1.0f;
       const float inv = amax > 0.0f ? 127.0f / amax : 1.0f;
       if (t == 0) sx[m] = s;
-      if (t >= n_out && t < kNormOutliers) xo[m * kNormOutliers + t] = (f16)0.0f;
+      if (t < kNormOutliers) xo[m * kNormOutliers + t] = t < n_out ? (f16)(oh * r * ow) : (f16)0.0f;
       // byte order of the 16 channels: 0,2,4,6, 1,3,5,7, 8,10,12,14, 9,11,13,15
       const auto write = [&](const float* v, int unit) {
         *reinterpret_cast<uint4*>(xq + row + 16 * unit) =
@@ -190,19 +210,15 @@ add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ we
                        pack_int8(v[8], v[10], v[12], v[14], inv), pack_int8(v[9], v[11], v[13], v[15], inv));
       };
 #pragma unroll
-      for (int u = 0; u < kNormUnits; ++u) {
-        const int unit = t + u * nt;
-        if (unit < units) write(h[u], unit);
-      }
-      for (int unit = t + kNormUnits * nt; unit < units; unit += nt) {
-        float g[16];
-        load_h(x, residual, row + 16 * unit, g);
-        normalize(g, unit);
-        const uint32_t om = unit_outliers(unit, o, n_out);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = (om >> e) & 1u ? 0.0f : g[e];
-        write(g, unit);
-      }
+      for (int u = 0; u < kUnits; ++u)
+        if (t + u * nt < units) write(h[u], t + u * nt);
+      if constexpr (kLong)
+        for (int unit = t + kUnits * nt; unit < units; unit += nt) {
+          float g[16];
+          reload(g, unit, true);
+          clear(g, unit);
+          write(g, unit);
+        }
     }
     __syncthreads();  // the reduction arrays are reused by the block's next row
   }
@@ -212,14 +228,13 @@ add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ we
 __global__ void __launch_bounds__(256)
 dequantize_act_int8_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx, const f16* __restrict__ xo,
                            const int32_t* __restrict__ outliers, int n_out, int64_t M, int K, f16* __restrict__ out) {
-  __shared__ int o[kNormOutliers];
-  if ((int)threadIdx.x < n_out) o[threadIdx.x] = min(max(outliers[threadIdx.x], 0), K - 1);
-  __syncthreads();
   const int units = K >> 4;
-  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-    const int unit = (int)(blockIdx.x * 256 + threadIdx.x);
-    if (unit >= units) continue;
-    const uint4 p = *reinterpret_cast<const uint4*>(xq + (size_t)m * K + 16 * unit);
+  const int o = load_outlier(outliers, n_out, K);
+  const int64_t total = M * units, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+    const int64_t m = i / units;
+    const int unit = (int)(i - m * units);
+    const uint4 p = *reinterpret_cast<const uint4*>(xq + 16 * i);
     const uint32_t d[4] = {p.x, p.y, p.z, p.w};
     const float s = sx[m];
     float v[16];
@@ -228,11 +243,15 @@ dequantize_act_int8_kernel(const int8_t* __restrict__ xq, const float* __restric
     for (int j = 0; j < 16; ++j) v[ord[j]] = (float)(int8_t)(d[j >> 2] >> (8 * (j & 3))) * s;
     const uint32_t om = unit_outliers(unit, o, n_out);
     if (om != 0)
-      for (int j = 0; j < n_out; ++j)
+      for (int j = 0; j < n_out; ++j) {
+        const int ch = __builtin_amdgcn_readlane(o, j);
+        if ((ch >> 4) == unit) {
+          const float f = (float)xo[m * kNormOutliers + j];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (o[j] == 16 * unit + e) v[e] = (float)xo[m * kNormOutliers + j];
-    store16(out + (size_t)m * K + 16 * unit, v);
+          for (int e = 0; e < 16; ++e) v[e] = (ch & 15) == e ? f : v[e];
+        }
+      }
+    store16(out + 16 * i, v);
   }
 }
 
@@ -241,23 +260,28 @@ hipError_t launch_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const
                               int8_t* xq, float* sx, uint16_t* xo, hipStream_t stream) {
   const int64_t units = K / 16;
   const int64_t threads = units >= kNormThreads ? kNormThreads : (units + 63) / 64 * 64;
-  const dim3 grid((unsigned)(M < 65536 ? M : 65536));
+  const dim3 grid((unsigned)(M < 65536 ? M : 65536)), block((unsigned)threads);
   const auto f = [](const uint16_t* p) { return reinterpret_cast<const f16*>(p); };
   const auto g = [](uint16_t* p) { return reinterpret_cast<f16*>(p); };
-  if (xq != nullptr)
-    hipLaunchKernelGGL((add_rmsnorm_kernel<true>), grid, dim3((unsigned)threads), 0, stream, f(x), f(residual),
-                       f(weight), M, (int)K, eps, outliers, (int)n_out, g(h), g(y), xq, sx, g(xo));
+  const auto run = [&](auto kern) {
+    hipLaunchKernelGGL(kern, grid, block, 0, stream, f(x), f(residual), f(weight), M, (int)K, eps, outliers,
+                       (int)n_out, g(h), g(y), xq, sx, g(xo));
+  };
+  if (units <= threads)
+    xq != nullptr ? run(add_rmsnorm_kernel<true, 1, false>) : run(add_rmsnorm_kernel<false, 1, false>);
+  else if (units <= 2 * threads)
+    xq != nullptr ? run(add_rmsnorm_kernel<true, 2, false>) : run(add_rmsnorm_kernel<false, 2, false>);
   else
-    hipLaunchKernelGGL((add_rmsnorm_kernel<false>), grid, dim3((unsigned)threads), 0, stream, f(x), f(residual),
-                       f(weight), M, (int)K, eps, outliers, (int)n_out, g(h), g(y), xq, sx, g(xo));
+    xq != nullptr ? run(add_rmsnorm_kernel<true, 1, true>) : run(add_rmsnorm_kernel<false, 1, true>);
   return hipGetLastError();
 }
 
 hipError_t launch_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo, const int32_t* outliers,
                                       int64_t n_out, int64_t M, int64_t K, uint16_t* out, hipStream_t stream) {
-  const dim3 grid((unsigned)((K / 16 + 255) / 256), (unsigned)(M < 65535 ? M : 65535));
-  hipLaunchKernelGGL(dequantize_act_int8_kernel, grid, dim3(256), 0, stream, xq, sx,
-                     reinterpret_cast<const f16*>(xo), outliers, (int)n_out, M, (int)K, reinterpret_cast<f16*>(out));
+  const int64_t blocks = (M * (K / 16) + 255) / 256;
+  hipLaunchKernelGGL(dequantize_act_int8_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
+                     stream, xq, sx, reinterpret_cast<const f16*>(xo), outliers, (int)n_out, M, (int)K,
+                     reinterpret_cast<f16*>(out));
   return hipGetLastError();
 }
 
