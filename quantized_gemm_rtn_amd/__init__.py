@@ -584,9 +584,9 @@ def add_rmsnorm_int8(x, weight, residual=None, eps: float = 1e-5, outliers=None,
     if outliers is not None:
         _need(outliers, torch.int32, "outliers")
         n_out = outliers.numel()
-    xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    sx = torch.empty(M, dtype=torch.float32, device=x.device)
-    xo = torch.empty((M, 16), dtype=torch.float16, device=x.device)
+    xq = torch.empty_like(x, dtype=torch.int8)
+    sx = x.new_empty(M, dtype=torch.float32)
+    xo = x.new_empty((M, 16))
     rc = lib.wq_add_rmsnorm_int8(_p(x), _p(residual), _p(weight), M, K, eps, _p(outliers) if n_out else None, n_out,
                                  _p(h), _p(xq), _p(sx), _p(xo), _stream(x))
     _check("wq_add_rmsnorm_int8", rc)
@@ -606,7 +606,7 @@ def dequantize_act_int8(xq, sx, xo=None, outliers=None):
         _need(xo, torch.float16, "xo")
     if sx.numel() != M or (n_out and tuple(xo.shape) != (M, 16)):
         raise ValueError("sx must be [M] and xo [M, 16]")
-    out = torch.empty((M, K), dtype=torch.float16, device=xq.device)
+    out = torch.empty_like(xq, dtype=torch.float16)
     rc = lib.wq_dequantize_act_int8(_p(xq), _p(sx), _p(xo) if n_out else None, _p(outliers) if n_out else None, n_out,
                                     M, K, _p(out), _stream(xq))
     _check("wq_dequantize_act_int8", rc)
@@ -689,7 +689,7 @@ def kv4_read(cache, page_table, seq_start, ctx_len, tokens: int, head_dim: int, 
     import torch
     lib = load()
     B, max_pages, num_pages, page_tokens, kv_heads = _kv4_view(cache, page_table, seq_start, ctx_len, head_dim)
-    k = torch.empty((tokens, kv_heads, head_dim), dtype=torch.float16, device=cache.device)
+    k = cache.new_empty((tokens, kv_heads, head_dim), dtype=torch.float16)
     v = torch.empty_like(k)
     rc = lib.wq_kv4_read(_p(cache), num_pages, page_tokens, tokens, kv_heads, head_dim, _p(seq_start), _p(ctx_len), B,
                          tokens if max_new is None else max_new, _p(page_table), max_pages, _p(k), _p(v),
@@ -723,12 +723,12 @@ def kv4_attention(q, cache, page_table, seq_start, ctx_len, max_q=None, max_ctx=
     max_q = T if max_q is None else max_q
     max_ctx = max_pages * page_tokens if max_ctx is None else max_ctx
     if out is None:
-        out = torch.empty((T, q_heads, head_dim), dtype=torch.float16, device=q.device)
+        out = q.new_empty((T, q_heads, head_dim))
     else:
         _need(out, torch.float16, "out")
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-    lse = torch.empty((T, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty((T, q_heads), dtype=torch.float32) if return_lse else None
     if workspace is None:
         nbytes = int(lib.wq_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx))
         if nbytes:

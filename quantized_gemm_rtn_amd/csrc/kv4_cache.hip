@@ -16,6 +16,8 @@
 //   collects the eight tokens of its words. Words that also hold tokens that were in
 //   the cache before are read first.
 // kv4_read_kernel: the way back, the same split: fp16 values of the new tokens.
+#include <type_traits>
+
 #include "kv4.h"
 #include "wq_launch.h"
 
@@ -27,12 +29,36 @@ __device__ __forceinline__ void tile_tokens(const KvSeq& s, int tile, int* lo, i
   *hi = min(s.ctx, (tile + 1) * kKvTile);
 }
 
+// largest value over the 8 or 16 lanes of a token, by exchanges inside rows of 16 lanes
+template <int N>
+__device__ __forceinline__ float token_max(float v) {
+  const auto step = [&](auto ctrl) {
+    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF, 0xF, false);
+    v = fmaxf(v, __builtin_bit_cast(float, o));
+  };
+  step(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  step(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  step(std::integral_constant<int, 0x141>{});  // lane 7 - i of each eight
+  if constexpr (N == 16) step(std::integral_constant<int, 0x140>{});  // lane 15 - i
+  return v;
+}
+
+// rint(x / s), half to even, for fp16 x and s with |x| <= 15 s, from the reciprocal of s.
+// x / s is a half-integer k + 1/2 exactly, or at least 2^-13 away from it: x and
+// (k + 1/2) s are multiples of 2^-12 of the power of two below s. So x times the rounded
+// reciprocal, rounded to a multiple of 2^-13 (1536 added and taken off again), is the
+// half-integer itself in the first case and on the right side of it in the second.
+__device__ __forceinline__ float round_quotient(float x, float reciprocal) {
+  return rintf((x * reciprocal + 1536.0f) - 1536.0f);
+}
+
 template <int D>
 __global__ void __launch_bounds__(256)
 kv4_append_kernel(const f16* __restrict__ k, int64_t k_stride, const f16* __restrict__ v, int64_t v_stride, KvCache a,
                   int tiles, uint8_t* __restrict__ cache) {
   constexpr int TPT = D / 8;            // threads of a token
   constexpr int TOK = 256 / TPT;        // tokens of a pass
+  constexpr int PASSES = kKvTile / TOK;
   __shared__ __align__(16) uint8_t codes[kKvTile][D + 4];
   const int h = blockIdx.x % a.hkv, first_tile = blockIdx.x / a.hkv % tiles;
   const int b = blockIdx.x / a.hkv / tiles, t = threadIdx.x;
@@ -49,15 +75,22 @@ kv4_append_kernel(const f16* __restrict__ k, int64_t k_stride, const f16* __rest
     uint8_t* base = cache + kv_page_offset(a, b, h, page) +
                     (int64_t)(tile - page * a.page_tiles) * kv_tile_bytes<D>();
     const int part = t % TPT;
-    for (int which = 0; which < 2; ++which) {
-      const f16* src = which ? v : k;
-      const int64_t stride = which ? v_stride : k_stride;
+    // both tensors' loads first, so that their latencies pass together
+    uint4 raw[2][PASSES];
 #pragma unroll
-      for (int pass = 0; pass < kKvTile / TOK; ++pass) {
+    for (int pass = 0; pass < PASSES; ++pass) {
+      const int pos = tile * kKvTile + pass * TOK + t / TPT;
+      const int64_t row = s.first_row + min(max(pos - (s.ctx - s.rows), 0), s.rows - 1);
+      raw[0][pass] = *reinterpret_cast<const uint4*>(k + row * k_stride + h * D + 8 * part);
+      raw[1][pass] = *reinterpret_cast<const uint4*>(v + row * v_stride + h * D + 8 * part);
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+      for (int pass = 0; pass < PASSES; ++pass) {
         const int in = pass * TOK + t / TPT, pos = tile * kKvTile + in;
         if (pos >= lo && pos < hi) {  // the same for all threads of a token
-          const int64_t row = s.first_row + (pos - (s.ctx - s.rows));
-          const f16x8 x = as_f16x8(*reinterpret_cast<const uint4*>(src + row * stride + h * D + 8 * part));
+          const f16x8 x = as_f16x8(raw[which][pass]);
           float f[8], top = 0.0f, bottom = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -65,18 +98,15 @@ kv4_append_kernel(const f16* __restrict__ k, int64_t k_stride, const f16* __rest
             top = fmaxf(top, f[e]);
             bottom = fminf(bottom, f[e]);
           }
-#pragma unroll
-          for (int off = TPT / 2; off >= 1; off >>= 1) {
-            top = fmaxf(top, __shfl_xor(top, off));
-            bottom = fminf(bottom, __shfl_xor(bottom, off));
-          }
+          top = token_max<TPT>(top);
+          bottom = -token_max<TPT>(-bottom);
           const f16 s16 = (f16)fmaxf(__fdiv_rn(top - bottom, 15.0f), 6.103515625e-05f);
-          const float sc = (float)s16;
-          const float z = fminf(fmaxf(rintf(__fdiv_rn(-bottom, sc)), 0.0f), 15.0f);
+          const float reciprocal = __fdiv_rn(1.0f, (float)s16);
+          const float z = fminf(round_quotient(-bottom, reciprocal), 15.0f);
           uint32_t q[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            q[e] = (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(f[e], sc)) + z, 0.0f), 15.0f);
+            q[e] = (uint32_t)(int)fminf(fmaxf(round_quotient(f[e], reciprocal) + z, 0.0f), 15.0f);
           if (which == 0) {
             uint32_t w = 0;
 #pragma unroll

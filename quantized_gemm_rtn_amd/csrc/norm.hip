@@ -41,7 +41,7 @@ __device__ __forceinline__ void store16(f16* p, const float* f) {
   *reinterpret_cast<uint4*>(p + 8) = __builtin_bit_cast(uint4, b);
 }
 
-__device__ __forceinline__ void load_h(const f16* x, const f16* residual, size_t at, float* h) {
+__device__ __forceinline__ void load_h(const f16* x, const f16* residual, uint32_t at, float* h) {
   load16(x + at, h);
   if (residual != nullptr) {
     float r[16];
@@ -98,7 +98,9 @@ __device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d
   return ab | cd;
 }
 
-// kUnits: units of 16 channels a thread holds; kLong: the row has more than those.
+// kUnits: units of 16 channels a thread holds; kLong: the row has more than those. (One
+// unit takes 64 registers: eight blocks of 256 threads a CU, so 2048 rows of 4096 channels
+// run at once.)
 template <bool kInt8, int kUnits, bool kLong>
 __global__ void __launch_bounds__(kNormThreads)
 add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ weight, int64_t M, int K, float eps,
@@ -107,8 +109,8 @@ add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ we
   __shared__ float red_sum[kNormThreads / 64], red_max[kNormThreads / 64];
   const int units = K >> 4, nt = (int)blockDim.x, t = (int)threadIdx.x;
   const int o = kInt8 ? load_outlier(outliers, n_out, K) : -1;
-  for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-    const size_t row = (size_t)m * K;
+  for (int m = blockIdx.x; m < (int)M; m += gridDim.x) {
+    const uint32_t row = (uint32_t)m * K;  // M K < 2^31
     float h[kUnits][16];
     f16x8 w[kUnits][2];
     float sum = 0.0f;
@@ -230,11 +232,11 @@ dequantize_act_int8_kernel(const int8_t* __restrict__ xq, const float* __restric
                            const int32_t* __restrict__ outliers, int n_out, int64_t M, int K, f16* __restrict__ out) {
   const int units = K >> 4;
   const int o = load_outlier(outliers, n_out, K);
-  const int64_t total = M * units, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
-    const int64_t m = i / units;
+  const uint32_t total = (uint32_t)M * units, step = gridDim.x * 256u;  // M K < 2^31
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += step) {
+    const uint32_t m = i / (uint32_t)units;
     const int unit = (int)(i - m * units);
-    const uint4 p = *reinterpret_cast<const uint4*>(xq + 16 * i);
+    const uint4 p = *reinterpret_cast<const uint4*>(xq + (size_t)16 * i);
     const uint32_t d[4] = {p.x, p.y, p.z, p.w};
     const float s = sx[m];
     float v[16];
@@ -246,12 +248,12 @@ dequantize_act_int8_kernel(const int8_t* __restrict__ xq, const float* __restric
       for (int j = 0; j < n_out; ++j) {
         const int ch = __builtin_amdgcn_readlane(o, j);
         if ((ch >> 4) == unit) {
-          const float f = (float)xo[m * kNormOutliers + j];
+          const float f = (float)xo[(size_t)m * kNormOutliers + j];
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = (ch & 15) == e ? f : v[e];
         }
       }
-    store16(out + 16 * i, v);
+    store16(out + (size_t)16 * i, v);
   }
 }
 
