@@ -635,11 +635,13 @@ def _rows(t, name, heads, head_dim):
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype != torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+    tokens, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
+    if h != heads or d != head_dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}]")
-    if (t.stride(2) != 1 and head_dim > 1) or (t.stride(1) != head_dim and heads > 1):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != head_dim and heads > 1):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return s0 if tokens > 1 else heads * head_dim
 
 
 def _kv4_view(cache, page_table, seq_start, ctx_len, head_dim):
