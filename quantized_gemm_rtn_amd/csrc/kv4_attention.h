@@ -29,6 +29,7 @@ struct AttnArgs {
   int window;         // 0: none
   float c;            // scale * log2(e)
   int shares, least;  // decode kernel: blocks a head, and the fewest tiles of one
+  int pad;            // items count as multiples of `least` steps: one item a block
   int decode_rows;    // rows of an item of the decode kernel (16 or 32)
   int tshares;        // tile kernel: blocks a head, each an equal share of the work; or 0,
   int row_tiles;      // and a block takes every row_tiles-th row tile of a sequence,

@@ -38,11 +38,15 @@ namespace wq {
 // steps as the sequence has visible tiles (one where it has none: its rows are still to
 // be written). All steps of a head are dealt out in equal shares, one a block, so that
 // blocks end together however the sequences' lengths differ; an item that lies in one
-// share is finished there, others leave a partial in each. A wave looks at 64 sequences
-// at a time, one a lane.
+// share is finished there, others leave a partial in each. Where there is less work than
+// blocks for it (p.pad), items count as a multiple of the fewest steps of a share, the
+// last of them empty, so that a share has one item: two are done one after the other, and
+// the latency of a block is what such a call takes (8 sequences of 3 to 5 drafted tokens,
+// window 1000, in 4 heads: 13.1 us without, 8.8 us with). A wave looks at 64 sequences at a time, one a lane.
 struct Sequences {
   KvSeq s;
-  int t0, n;      // first visible tile, steps of an item (0: nothing to do here)
+  int t0, tiles;  // first visible tile, tiles of an item
+  int n;          // steps of an item (0: nothing to do here)
   int64_t steps, upto;  // of the sequence, and of those up to it, from `first` on
 };
 __device__ __forceinline__ Sequences load_sequences(const KvCache& a, const AttnArgs& p, int first, int lane) {
@@ -53,7 +57,8 @@ __device__ __forceinline__ Sequences load_sequences(const KvCache& a, const Attn
   const bool mine = b < a.B && rows > 0 && rows <= p.row_limit;
   const TileRange r = tile_range(q.s, p, 0, rows - 1);
   q.t0 = r.t0;
-  q.n = mine ? max(r.t1 - r.t0, 1) : 0;
+  q.tiles = max(r.t1 - r.t0, 1);
+  q.n = mine ? (p.pad ? (q.tiles + p.least - 1) & -p.least : q.tiles) : 0;
   q.steps = (int64_t)q.n * ((rows + p.decode_rows - 1) / p.decode_rows);
   q.upto = wave_sums_upto(q.steps, lane);
   return q;
@@ -151,6 +156,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
     s.rows = __builtin_amdgcn_readlane(seqs.s.rows, j);
     s.ctx = __builtin_amdgcn_readlane(seqs.s.ctx, j);
     const int t0 = __builtin_amdgcn_readlane(seqs.t0, j), steps = __builtin_amdgcn_readlane(seqs.n, j);
+    const int last = t0 + __builtin_amdgcn_readlane(seqs.tiles, j);
     const int rows = s.rows * p.group;
     const int64_t into = at - (before + lane_value(seqs.upto - seqs.steps, j));
     const int rt = rows > ROWS ? (int)(into / steps) : 0;
@@ -188,7 +194,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
     float vexp = 0.0f;          // value scales seen are at most 2^vexp, the fp16 with bits vbits
     uint32_t vbits = 0;
 
-    const int begin = t0 + from, end = s.ctx > 0 ? begin + count : begin;
+    const int begin = t0 + from, end = s.ctx > 0 ? min(begin + count, last) : begin;
     int tile = begin + wave;
     int page = tile / a.page_tiles, in_page = tile - page * a.page_tiles;
     uint8_t* ring = lds + wave * kDepth * TILE;
@@ -524,12 +530,13 @@ namespace {
 
 constexpr int64_t kCus = 256;
 constexpr int64_t kDecodeBlocks = 2;  // blocks a CU (three fit; measured slower by 2 %: more, shorter shares)
-constexpr int64_t kLeastTiles = 8;    // of a share: two a wave
+constexpr int64_t kLeastTiles = 8;    // of a share: two a wave (a power of two)
 
 struct Plan {
   bool decode, tile;  // which kernels run
   int decode_rows, row_limit;
   int64_t shares;     // decode kernel: blocks a head
+  int pad;            // and whether each has one item
   int64_t tshares, most_tshares;  // tile kernel: the same (0: whole row tiles), and its bound
   int row_tiles, snake;
 };
@@ -563,8 +570,10 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
     // as many blocks as run well at once, each with an equal share; one a head where the
     // heads alone are as many
     constexpr int64_t resident = kCus * kDecodeBlocks;
-    const int64_t most = ceil_div(B * ceil_div(p.tile ? kLimit : rows, p.decode_rows) * tiles, kLeastTiles);
-    p.shares = resident / hkv < most ? resident / hkv : most;
+    const int64_t items = B * ceil_div(p.tile ? kLimit : rows, p.decode_rows);
+    const int64_t most = ceil_div(items * tiles, kLeastTiles), padded = items * ceil_div(tiles, kLeastTiles);
+    p.pad = padded <= resident / hkv;
+    p.shares = p.pad ? padded : (resident / hkv < most ? resident / hkv : most);
     if (p.shares < 1) p.shares = 1;
   }
   if (p.tile) {
@@ -663,6 +672,7 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.c = scale * 1.44269504088896341f;
   p.shares = (int)pl.shares;
   p.least = (int)kLeastTiles;
+  p.pad = pl.pad;
   p.decode_rows = pl.decode_rows;
   p.tshares = (int)pl.tshares;
   p.row_tiles = pl.row_tiles;
