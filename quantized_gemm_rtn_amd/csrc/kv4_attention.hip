@@ -486,7 +486,20 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
   const auto place = [&](int i) {
     return (((i0 + i) * a.hkv + h) * 2 + (i == 0 && X > i0 * per ? 1 : 0)) * p.decode_rows + row % p.decode_rows;
   };
-  // every wave finds the row's reference and sum, a partial a lane
+  // The wave's first partials are on their way while every wave finds the row's reference
+  // and sum, a partial a lane.
+  constexpr int AHEAD = 8;
+  float ahead[AHEAD][N], ahead_r[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    const int i = (W == 1 ? 0 : wave) + W * k;
+    if (i < parts) {
+      const int64_t at = place(i);
+      ahead_r[k] = p.part_s[at].x;
+#pragma unroll
+      for (int e = 0; e < N; ++e) ahead[k][e] = p.part_o[at * D + N * lane + e];
+    }
+  }
   float best = kNoRef, total = 0.0f;
   for (int i = lane; i < parts; i += 64) best = fmaxf(best, p.part_s[place(i)].x);
 #pragma unroll
@@ -500,8 +513,15 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
   float o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if ((W == 1 ? 0 : wave) + W * k < parts) {
+      const float f = exp2_hw(ahead_r[k] - best);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(ahead[k][e], f, o[e]);
+    }
 #pragma unroll 8
-  for (int i = W == 1 ? 0 : wave; i < parts; i += W) {
+  for (int i = (W == 1 ? 0 : wave) + W * AHEAD; i < parts; i += W) {
     const int64_t at = place(i);
     const float f = exp2_hw(p.part_s[at].x - best);
 #pragma unroll
