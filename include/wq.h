@@ -442,7 +442,7 @@ int wq_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo
  *              sequence. They only shape the launch: every sequence is handled in full
  *              whatever they are, only slower when they are far off.
  * Lengths, starts and page numbers outside their arrays are clamped on the device (wrong
- * values, never an invalid access). B up to 2^20 and below 2^26 / heads, heads up to
+ * values, never an invalid access). B up to 2^20 and below 2^24 / heads, heads up to
  * 65535, T = rows of the token-wise arrays below 2^31 / heads, max_pages * page_tokens up to 2^30. T = 0 or
  * B = 0 returns WQ_OK without a launch.
  */
@@ -490,7 +490,9 @@ size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, i
  *          sizes (may be NULL when that is 0); contents on entry do not matter.
  * Scores, maxima and sums are fp32; a weight is rounded once to fp16, times its value
  * scale, as an MFMA operand. Deterministic: a fixed order for the same sizes. Rows of q
- * that belong to no sequence leave their rows of out and lse unwritten.
+ * that belong to no sequence leave their rows of out and lse unwritten. T *
+ * (q_heads / kv_heads)^2 * max_pages * page_tokens is at most 2e18 (WQ_ERR_SHAPE
+ * otherwise): the work is counted in 64-bit integers.
  */
 int wq_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
                      int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B, int64_t max_q,

@@ -435,7 +435,7 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
   constexpr int N = D / 64;                // channels of a lane
   __shared__ float joined[W][D + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t item = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0);
+  int64_t item = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + (W == 1 ? wave : 0);
   int b, h, row;
   KvSeq s;
   if (by_sequence) {
@@ -610,7 +610,7 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
     if (blocks <= 2 * kCus) whole = longest * 4200 > mean * 5400 ? longest * 4200 : mean * 5400;
     if (blocks <= kCus) whole = longest * 4200;
     const int64_t most = ceil_div(T * group * tiles, (int64_t)kLeastItemTiles * kTileRows) + 1;
-    const int64_t most_blocks = 0x7FFFFFFF / (B * hkv);  // B hkv < 2^31, and so is the grid
+    const int64_t most_blocks = 0xFFFFFF / (B * hkv);  // B hkv < 2^24, and so is the grid
     const int64_t fit = 2 * kCus / hkv < 1 ? 1 : 2 * kCus / hkv;
     p.tshares = fit < most ? fit : most;
     p.most_tshares = p.tshares;
@@ -633,13 +633,17 @@ size_t part_bytes(int64_t slots, int64_t D) { return round256((size_t)slots * (D
 template <int D>
 hipError_t combine(const KvCache& a, const AttnArgs& p, int64_t parts, int64_t items, int by_sequence,
                    hipStream_t stream) {
+  // blocks in two dimensions: one holds 2^32 threads
+  const auto grid = [](int64_t blocks) {
+    constexpr int64_t x = 1 << 20;
+    return dim3((unsigned)(blocks < x ? blocks : x), (unsigned)ceil_div(blocks, x));
+  };
   if (parts <= 8)
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 1>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, p,
-                       by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 1>), grid(ceil_div(items, 4)), dim3(256), 0, stream, a, p, by_sequence);
   else if (parts <= 32)
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 4>), dim3((unsigned)items), dim3(256), 0, stream, a, p, by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 4>), grid(items), dim3(256), 0, stream, a, p, by_sequence);
   else
-    hipLaunchKernelGGL((kv4_combine_kernel<D, 16>), dim3((unsigned)items), dim3(1024), 0, stream, a, p, by_sequence);
+    hipLaunchKernelGGL((kv4_combine_kernel<D, 16>), grid(items), dim3(1024), 0, stream, a, p, by_sequence);
   return hipGetLastError();
 }
 

@@ -230,7 +230,7 @@ KvCache kv4_cache_args(const Kv4View& c, int64_t T, int64_t head_dim) {
 
 // tiles a sequence with up to max_new new tokens may touch, at most what the grid takes
 static int append_tiles(const Kv4View& c, int64_t max_new) {
-  const int64_t most = (((int64_t)1 << 31) - 1) / (c.B * c.kv_heads);  // B kv_heads < 2^31
+  const int64_t most = (((int64_t)1 << 24) - 1) / (c.B * c.kv_heads);  // B kv_heads < 2^24, blocks too
   const int64_t want = (max_new + kKvTile - 2) / kKvTile + 1;
   return (int)(want < most ? want : most);
 }

@@ -118,8 +118,9 @@ size_t act_order_copy_bytes(int64_t rows, int64_t K, size_t elem) { return ((siz
 
 constexpr int64_t kKvTile = 32;                // tokens of a cache tile: pages hold whole tiles
 constexpr int64_t kMaxBatch = (int64_t)1 << 20;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 24;
 constexpr int64_t kMaxContext = (int64_t)1 << 30;
-constexpr int64_t kMaxHeads = 65535;           // and 32 * batch * heads < 2^31: grids are (batch, head, ..)
+constexpr int64_t kMaxHeads = 65535;           // and batch * heads < 2^24: grids are (batch, head, ..), of 2^32 threads at most
 
 int check_norm_args(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
                     float eps, const uint16_t* h) {
@@ -146,7 +147,7 @@ int check_kv4_args(int64_t T, int64_t heads, const wq::Kv4View& c, int64_t head_
   if (!kv4_format(c.page_tokens, head_dim)) return WQ_ERR_UNSUPPORTED;
   if (T < 0 || c.B < 0 || c.B > kMaxBatch || c.kv_heads < 1 || c.kv_heads > kMaxHeads || heads < c.kv_heads ||
       heads > kMaxHeads || c.num_pages < 1 || c.num_pages >= kMax32 || c.max_pages < 1 ||
-      c.max_pages > kMaxContext / c.page_tokens || T >= kMax32 / heads || c.B >= kMax32 / (32 * heads))
+      c.max_pages > kMaxContext / c.page_tokens || T >= kMax32 / heads || c.B >= kMaxBlocks / heads)
     return WQ_ERR_SHAPE;
   if (!aligned(cache, 16) || !aligned(c.seq_start, 4) || !aligned(c.ctx_len, 4) || !aligned(c.page_table, 4))
     return WQ_ERR_ALIGN;
@@ -547,7 +548,7 @@ size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, i
                                         int64_t max_q, int64_t max_ctx) {
   if (T < 1 || B < 1 || B > kMaxBatch || kv_heads < 1 || kv_heads > kMaxHeads || q_heads < kv_heads ||
       q_heads > kMaxHeads || q_heads % kv_heads != 0 || T >= kMax32 / q_heads ||
-      B >= kMax32 / (32 * q_heads) || (head_dim != 64 && head_dim != 128))
+      B >= kMaxBlocks / q_heads || (head_dim != 64 && head_dim != 128))
     return 0;
   if (max_q < 0 || max_ctx < 0 || max_ctx > kMaxContext) return 0;
   return wq::kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx);

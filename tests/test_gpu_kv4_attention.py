@@ -38,6 +38,21 @@ def test_several_tokens(gpu_lib, new, ctx, hq, hkv, page, d):
     check(*b.attention(), b.reference())
 
 
+@pytest.mark.parametrize("hint", [20, 600])
+@pytest.mark.parametrize("B,hkv", [(3, 4), (100, 1), (150, 2)])
+def test_less_work_than_blocks(gpu_lib, B, hkv, hint):
+    """Batches small enough for one item a block, also of more than 64 sequences, some of
+    them idle or empty, with the lengths within the bounds given and beyond them."""
+    import torch
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, 6, B).tolist()
+    ctx = [int(n + rng.integers(0, 600 - n)) if n else int(rng.integers(0, 300)) for n in new]
+    new[1], ctx[1], new[2], ctx[2] = 3, 2, 5, 599
+    say(f"[kv4 small batch] B={B} hkv={hkv} max_ctx={hint}")
+    b = Batch(gpu_lib, torch, new, ctx, 7 * hkv, hkv, 64, 32, seed=B).fill()
+    check(*b.attention(max_ctx=hint), b.reference())
+
+
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 10000])
 @pytest.mark.parametrize("new,ctx,hq,hkv", [([1, 1, 1], [1, 95, 400], 4, 2), ([5, 3], [77, 300], 6, 2),
                                             ([90, 1], [250, 120], 4, 1)])

@@ -148,6 +148,17 @@ def test_attention_validation(lib, kw, status):
     assert attention(lib, **kw) == status
 
 
+def test_grid_and_work_limits(lib):
+    """Batch times heads stays below 2^24 (a grid has 2^32 threads), and the tokens that
+    all rows may see within 64-bit sums."""
+    assert append(lib, B=1 << 19, hkv=32, ks=4096, vs=4096) == -2
+    assert read(lib, B=1 << 19, hkv=32) == -2
+    assert attention(lib, B=1 << 19) == -2
+    assert lib.wq_kv4_attention_workspace_bytes(4, 1 << 19, 32, 8, 128, 1, 100) == 0
+    assert lib.wq_kv4_attention_workspace_bytes(4, (1 << 19) - 1, 32, 8, 128, 1, 100) > 0
+    assert attention(lib, T=1 << 24, hq=64, qs=8192, hkv=1, max_pages=1 << 24) == -2
+
+
 def test_attention_workspace(lib):
     f = lib.wq_kv4_attention_workspace_bytes
     assert f(1, 1, 32, 8, 128, 1, 32) == 0                 # one tile: nothing to split
