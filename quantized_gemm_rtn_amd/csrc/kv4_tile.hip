@@ -273,64 +273,149 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
 }
 
 // Joins the partials of the items that more than one share worked on: block (head, share
-// i, quarter of the rows) those of the item that share i begins but does not end. Sixteen
-// lanes take a row, D / 16 channels each, so that a wave has four rows on their way.
-template <int D>
+// i, slice of the rows) those of the item that share i begins but does not end. 16 lanes
+// take a row, D / 16 channels each, a wave 4 PASSES rows, AHEAD partials at a time. With
+// few partials of a row (PW = 1) a wave takes all of them, with many (PW = 4) the block's
+// four waves take them in turn and join theirs through LDS. Which shares have tiles of the
+// item the lanes find out for 64 of them at once (a quotient in double each). Bound by the
+// partials' bytes where there are many rows (67 MB written and read for 1357 tokens of 32
+// heads: 16 us), else by latency: one row tile of 59 000 tokens in 85 shares takes 24 us,
+// and took 110 us with a wave for all of a row's partials.
+template <int D, int PW, int PASSES, int AHEAD>
 __global__ void __launch_bounds__(256)
 kv4_tile_combine_kernel(KvCache a, AttnArgs p) {
-  constexpr int N = D / 16;  // channels of a lane
-  const int lane = threadIdx.x & 63;
+  constexpr int N = D / 64;  // runs of four channels of a lane
+  constexpr int ROWS = 4 * PASSES * (4 / PW);  // rows of the block
+  __shared__ f32x4 o_s[PW][PW > 1 ? ROWS : 1][D / 4];
+  __shared__ float2 s_s[PW][ROWS];
+  const int lane = threadIdx.x & 63, part = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x % a.hkv, share = blockIdx.x / a.hkv;
-  AreaWalk walk;
-  const int64_t total = area_begin(walk, a, p, lane), per = share_area(p, total);
-  const int64_t from = share * per, until = from + per;
-  if (until >= total) return;  // (the last share ends its items)
-  AreaItem t;
-  if (!area_find(t, walk, a, p, until - 1, lane)) return;
-  // the share's last item: it must begin in this share and go on in the next
-  if (t.X < from || t.next <= until) return;
+  // one wave looks for the share's last item (every block does: with four it took 6 us of
+  // the kernel for each 2048 blocks); it must begin in this share and go on in the next
+  __shared__ AreaItem item_s;
+  __shared__ int64_t per_s;
+  __shared__ int split_s;
+  if (wave == 0) {
+    AreaWalk walk;
+    AreaItem t;
+    const int64_t total = area_begin(walk, a, p, lane), per = share_area(p, total);
+    const int64_t from = share * per, until = from + per;
+    const bool split = until < total && area_find(t, walk, a, p, until - 1, lane) && t.X >= from && t.next > until;
+    if (lane == 0) {
+      if (split) item_s = t;
+      per_s = per;
+      split_s = split;
+    }
+  }
+  __syncthreads();
+  if (!split_s) return;
+  const AreaItem t = item_s;
+  const int64_t per = per_s, from = share * per;
   const int rows = t.s.rows * p.group, row0 = t.rt * kTileRows, row1 = min(rows, row0 + kTileRows) - 1;
+  const int slice = ROWS * blockIdx.y, in = (PW == 1 ? 4 * PASSES * wave : 0) + (lane >> 4);
+  if (row0 + slice > row1) return;
   const TileRange range = tile_range(t.s, p, row0, row1);
   const int n = range.t1 - range.t0;
   const int64_t W = t.next - t.X;
-  // shares of the item, with the tiles that each had; one that had all wrote the rows
-  int parts = 0;
-  for (int64_t x = from; x < t.next; x += per, ++parts)
-    if (tiles_before(x + per, t.X, W, n) - tiles_before(x, t.X, W, n) == n) return;
-  const int part = threadIdx.x & 15;
+  const int parts = (int)((t.next - from + per - 1) / per);  // shares of the item
+  float best[PASSES], sum[PASSES];
+  f32x4 o[PASSES][N];
 #pragma unroll
-  for (int pass = 0; pass < kTileRows / 64; ++pass) {
-    const int in = 64 * pass + 16 * blockIdx.y + (threadIdx.x >> 4), row = row0 + in;
-    if (row > row1) continue;
-    float best = kNoRef, total_sum = 0.0f, o[N];
+  for (int k = 0; k < PASSES; ++k) {
+    best[k] = kNoRef;
+    sum[k] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-      const int64_t x = from + i * per;
-      if (tiles_before(x + per, t.X, W, n) == tiles_before(x, t.X, W, n)) continue;
-      const int64_t at = (((int64_t)(share + i) * a.hkv + h) * 2 + (i == 0 && t.X > from ? 1 : 0)) * kTileRows + in;
-      const float2 v = p.tpart_s[at];
-      const float to = fmaxf(best, v.x), keep = exp2_hw(best - to), f = exp2_hw(v.x - to);
-      best = to;
-      total_sum = total_sum * keep + v.y * f;
+    for (int j = 0; j < N; ++j) o[k][j] = f32x4{};
+  }
+  for (int i0 = 0; i0 < parts; i0 += 64) {
+    const int64_t x = from + min(i0 + lane, parts - 1) * per;
+    const int had = tiles_before(x + per, t.X, W, n) - tiles_before(x, t.X, W, n);
+    if (__any(had == n)) return;  // a share that had all wrote the rows
+    uint64_t mine = __ballot(i0 + lane < parts && had > 0) & (PW == 1 ? ~0ull : 0x1111111111111111ull << wave);
+    while (mine != 0) {
+      bool has[AHEAD];
+      float2 v[AHEAD][PASSES];
+      f32x4 d[AHEAD][PASSES][N];
 #pragma unroll
-      for (int e = 0; e < N; e += 4) {
-        const f32x4 d = *reinterpret_cast<const f32x4*>(p.tpart_o + at * D + 64 * (e >> 2) + 4 * part);
+      for (int g = 0; g < AHEAD; ++g) {
+        has[g] = mine != 0;
+        if (!has[g]) continue;
+        const int i = i0 + __builtin_ctzll(mine);
+        mine &= mine - 1;
+        const int64_t first = (((int64_t)(share + i) * a.hkv + h) * 2 + (i == 0 && t.X > from ? 1 : 0)) * kTileRows;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[e + k] = o[e + k] * keep + d[k] * f;
+        for (int k = 0; k < PASSES; ++k) {
+          const int64_t at = first + min(slice + in + 4 * k, row1 - row0);
+          v[g][k] = p.tpart_s[at];
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            d[g][k][j] = *reinterpret_cast<const f32x4*>(p.tpart_o + at * D + 64 * j + 4 * part);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < AHEAD; ++g) {
+        if (!has[g]) continue;
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+          const float to = fmaxf(best[k], v[g][k].x), keep = exp2_hw(best[k] - to), f = exp2_hw(v[g][k].x - to);
+          best[k] = to;
+          sum[k] = sum[k] * keep + v[g][k].y * f;
+#pragma unroll
+          for (int j = 0; j < N; ++j) o[k][j] = o[k][j] * keep + d[g][k][j] * f;
+        }
       }
     }
+  }
+  const auto store = [&](int row, float top, float all, const f32x4(&v)[N]) {
+    if (row > row1) return;
     const int tok = row / p.group;
     const int64_t out_row = (int64_t)(t.s.first_row + tok) * p.hq + h * p.group + (row - tok * p.group);
-    const float inv = total_sum > 0.0f ? 1.0f / total_sum : 0.0f;
+    const float inv = all > 0.0f ? 1.0f / all : 0.0f;
     typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int e = 0; e < N; e += 4)
-      *reinterpret_cast<f16x4*>(p.out + out_row * D + 64 * (e >> 2) + 4 * part) =
-          f16x4{(f16)(o[e] * inv), (f16)(o[e + 1] * inv), (f16)(o[e + 2] * inv), (f16)(o[e + 3] * inv)};
-    if (part == 0 && p.lse != nullptr)
-      p.lse[out_row] = total_sum > 0.0f ? (best + log2f(total_sum)) * kLn2 : -INFINITY;
+    for (int j = 0; j < N; ++j)
+      *reinterpret_cast<f16x4*>(p.out + out_row * D + 64 * j + 4 * part) =
+          f16x4{(f16)(v[j][0] * inv), (f16)(v[j][1] * inv), (f16)(v[j][2] * inv), (f16)(v[j][3] * inv)};
+    if (part == 0 && p.lse != nullptr) p.lse[out_row] = all > 0.0f ? (top + log2f(all)) * kLn2 : -INFINITY;
+  };
+  if constexpr (PW == 1) {
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) store(row0 + slice + in + 4 * k, best[k], sum[k], o[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      if (part == 0) s_s[wave][in + 4 * k] = make_float2(best[k], sum[k]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) o_s[wave][in + 4 * k][16 * j + part] = o[k][j];
+    }
+    __syncthreads();
+    const int r = threadIdx.x >> 4;
+    if (r >= ROWS) return;
+    float top = s_s[0][r].x, all = 0.0f;
+#pragma unroll
+    for (int w = 1; w < PW; ++w) top = fmaxf(top, s_s[w][r].x);
+    f32x4 v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = f32x4{};
+#pragma unroll
+    for (int w = 0; w < PW; ++w) {
+      const float f = exp2_hw(s_s[w][r].x - top);
+      all += s_s[w][r].y * f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] += o_s[w][r][16 * j + part] * f;
+    }
+    store(row0 + slice + r, top, all, v);
   }
+}
+
+template <int D>
+hipError_t join(const KvCache& a, const AttnArgs& p, unsigned blocks, bool many, hipStream_t stream) {
+  if (many)
+    hipLaunchKernelGGL((kv4_tile_combine_kernel<D, 4, 2, 2>), dim3(blocks, kTileRows / 8), dim3(256), 0, stream, a, p);
+  else
+    hipLaunchKernelGGL((kv4_tile_combine_kernel<D, 1, 2, 2>), dim3(blocks, kTileRows / 32), dim3(256), 0, stream, a, p);
+  return hipGetLastError();
 }
 
 hipError_t launch_kv4_tile(const KvCache& a, const AttnArgs& p, int64_t head_dim, hipStream_t stream) {
@@ -341,12 +426,9 @@ hipError_t launch_kv4_tile(const KvCache& a, const AttnArgs& p, int64_t head_dim
     hipLaunchKernelGGL((kv4_tile_kernel<64>), grid, dim3(256), 0, stream, a, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.tshares <= 1) return e;
-  const dim3 quarters(grid.x, 4);
-  if (head_dim == 128)
-    hipLaunchKernelGGL((kv4_tile_combine_kernel<128>), quarters, dim3(256), 0, stream, a, p);
-  else
-    hipLaunchKernelGGL((kv4_tile_combine_kernel<64>), quarters, dim3(256), 0, stream, a, p);
-  return hipGetLastError();
+  // shares of a row tile, about: with many, few blocks have work, and each should have little
+  const bool many = p.tshares > 6 * ((int64_t)a.T * p.group / kTileRows + 1);
+  return head_dim == 128 ? join<128>(a, p, grid.x, many, stream) : join<64>(a, p, grid.x, many, stream);
 }
 
 }  // namespace wq
