@@ -1,5 +1,22 @@
 // Causal attention over the 4-bit cache for many query rows, for gfx950: the tile kernel
 // (kv4_attention.hip has the mathematics, the kernel for few rows, and the choice).
+//
+// A block has 128 rows of one key/value head, four waves 32 each, and takes 64 tokens a
+// step: two barriers, between which the waves unpack a quarter of the step's codes each
+// into LDS as the products' operands, and after which every wave reads all of them, once
+// for each of its two products (keys . queries^T, values^T . weights^T, 32x32x16). Queries,
+// scores, weights and sums stay in registers (232 of 256: two blocks a CU). The codes of
+// the next step are on their way meanwhile.
+//
+// Measured: 1357 tokens in chunks of 700, 535 and 122 after up to 6000, 32 heads on 8: 126
+// GFLOP in 180 us (0.70 PFLOP/s); a prompt of 2048 62 us, of which its last rows' 32 steps,
+// alone on their CUs, are 56. Two blocks' steps take 5400 cycles a CU: matrix units are
+// busy for 2048 of them, vector units for 2800, and LDS for 2500 (32 rows a wave need 1 KB
+// of operands a matrix instruction, its full rate at the matrix units' own). None fills the
+// step because each block's phases follow on one another and only two blocks overlap. Tried
+// and slower: 64 rows a wave (spills); three blocks a CU with 32 tokens at a time; eight
+// waves that halve the tokens; the next step's scores made while this one's weights are;
+// one barrier a step.
 #include "kv4_attention.h"
 
 namespace wq {

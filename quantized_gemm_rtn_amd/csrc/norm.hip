@@ -11,6 +11,12 @@
 // three steps (sum of squares, amax, output), so x and residual are read once and each
 // output is written once: 2 + 2 bytes in and 2 + 1 (INT8) or 2 + 2 (fp16) out per
 // channel. Rows longer than a block's threads hold (32768 channels) are read again.
+// The INT8 values and the fp16 outliers and sums are the only roundings.
+//
+// Bound by memory for many rows, by latency for few. Measured: INT8, 2048 rows of 4096
+// channels with 8 outliers 16.0 us (58.7 MB, 3.7 TB/s; all rows at once, so that reading
+// and writing do not overlap much), one row 3.8 us; fp16, 33 rows of 8192 4.1 us. Loading
+// weights and outliers only when they are used: 21.8 and 7.0 us.
 #include "wq_device.h"
 #include "wq_launch.h"
 
@@ -227,6 +233,7 @@ add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ we
 }
 
 // xq (in the products' byte order) * sx, with the outlier channels from xo: fp16 [M, K].
+// A thread takes 16 channels. 2048 rows of 4096: 8.2 us (25 MB, 3.1 TB/s), one row 2.7 us.
 __global__ void __launch_bounds__(256)
 dequantize_act_int8_kernel(const int8_t* __restrict__ xq, const float* __restrict__ sx, const f16* __restrict__ xo,
                            const int32_t* __restrict__ outliers, int n_out, int64_t M, int K, f16* __restrict__ out) {
