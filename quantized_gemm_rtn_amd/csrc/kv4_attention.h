@@ -64,6 +64,9 @@ __device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
   return max((uint32_t)m.x, (uint32_t)m.y);
 }
 
+// log2 of the power of two above a positive normal fp16 with these bits
+__device__ __forceinline__ float bound_of(uint32_t bits) { return (float)((int)(bits >> 10) - 14); }
+
 // value of a lane of the wave (64 bits)
 __device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
   return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |

@@ -19,9 +19,12 @@
 // maxima, sums and outputs are fp32.
 //
 // The reference r keeps the fp16 operands in range and precise: weights times value
-// scales, 2^(x - r) u, are held near 2^10 at the row's largest, at most 2^14. It only
-// moves (and everything summed so far is only rescaled) when a tile's scores or value
-// scales would pass that bound, which any lane can see without asking the others.
+// scales, 2^(x - r) u, are held near 2^10 at the row's largest, at most 2^14. It is the
+// largest sum of a lane's top score of a tile and the power of two above its value scales
+// there, and only moves (and everything summed so far is only rescaled) when one passes
+// that bound by 4, which any lane can see without asking the others. (With the largest
+// score and the largest scale of the whole row instead, tokens of small scales that take
+// a row after others of scales 2^24 as large lost their operands' last bits.)
 //
 //  kv4_decode_kernel   few query rows (16 or 32 a block): all tiles of all sequences are
 //    dealt out in equal shares, one a block, whose four waves take tiles of 32 tokens in
@@ -199,8 +202,6 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
 #pragma unroll
       for (int t = 0; t < CT; ++t) acc[n][t] = f32x4{};
     }
-    float vexp = 0.0f;          // value scales seen are at most 2^vexp, the fp16 with bits vbits
-    uint32_t vbits = 0;
 
     const int begin = t0 + from, end = s.ctx > 0 ? min(begin + count, last) : begin;
     int tile = begin + wave;
@@ -319,33 +320,23 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
 
       float mx[NT];
       const uint32_t vmax = max_bits8(vs);
-      bool move = vmax > vbits;
+      const float ve = bound_of(vmax);
+      bool move = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         mx[n] = x[n][0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) mx[n] = fmaxf(mx[n], x[n][e]);
-        mx[n] *= p.c;
-        move |= mx[n] + vexp - kTop > ref[n] + kSlack;
+        mx[n] = __builtin_fmaf(mx[n], p.c, ve);
+        move |= mx[n] - kTop > ref[n] + kSlack;
       }
       if (__any(move)) {
-        uint32_t top = vmax;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-        float grown = 0.0f;
-        if (top > vbits) {
-          // the next power of two: exponent field + 1, mantissa 0 (scales are normal fp16)
-          const float ve = (float)((int)(top >> 10) + 1 - 15);
-          grown = vbits == 0 ? 0.0f : ve - vexp;
-          vexp = ve;
-          vbits = ((top >> 10) << 10) | 0x3FFu;
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float m = mx[n];
           m = fmaxf(m, __shfl_xor(m, 16));
           m = fmaxf(m, __shfl_xor(m, 32));
-          const float to = fmaxf(ref[n] + grown, m + vexp - kTop);
+          const float to = fmaxf(ref[n], m - kTop);
           const float f = exp2_hw(ref[n] - to);
           ref[n] = to;
           sum[n] *= f;
@@ -563,15 +554,16 @@ constexpr int64_t kLeastTiles = 8;    // of a share: two a wave (a power of two)
 struct Plan {
   bool decode, tile;  // which kernels run
   int decode_rows, row_limit;
-  int64_t shares;     // decode kernel: blocks a head
-  int pad;            // and whether each has one item
+  int64_t shares, most_shares;  // decode kernel: blocks a head, and their bound
+  int pad;            // whether each has one item
   int64_t tshares, most_tshares;  // tile kernel: the same (0: whole row tiles), and its bound
   int row_tiles, snake;
 };
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
-Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int64_t max_ctx, int64_t window) {
+Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q, int64_t max_ctx,
+               int64_t window) {
   Plan p = {};
   const int64_t group = hq / hkv;
   const int64_t q = max_q < 1 ? 1 : (max_q > T ? T : max_q);
@@ -584,27 +576,27 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
   constexpr int64_t kLimit = 96;
   // a sequence's rows decide its kernel; from the host only the largest is known, and
   // that all are alike where there is one sequence or B max_q new tokens
-  p.tile = rows > kLimit;
-  p.decode = !p.tile || (B > 1 && B * q > T);
-  p.row_limit = p.tile ? (p.decode ? (int)kLimit : 0) : 0x7FFFFFFF;
-  p.decode_rows = p.tile || rows > kDecodeRows ? 2 * kDecodeRows : kDecodeRows;
+  const bool many = rows > kLimit, mixed = B > 1 && B * q > T;
+  p.decode_rows = many || rows > kDecodeRows ? 2 * kDecodeRows : kDecodeRows;
   int64_t tiles = ceil_div(max_ctx < 1 ? 1 : max_ctx, kKvTile);
   if (window > 0) {  // q rows see up to window + q - 1 tokens, which may begin inside a tile
     const int64_t in_window = ceil_div(window + q - 1, kKvTile) + 1;
     tiles = in_window < tiles ? in_window : tiles;
   }
-  p.shares = 1;
-  if (p.decode) {
-    // as many blocks as run well at once, each with an equal share; one a head where the
-    // heads alone are as many
+  // The decode kernel, for sequences of up to `most_rows` rows: as many blocks as run well
+  // at once, each with an equal share; one a head where the heads alone are as many
+  const auto deal = [&](int64_t most_rows, int& pad) {
     constexpr int64_t resident = kCus * kDecodeBlocks;
-    const int64_t items = B * ceil_div(p.tile ? kLimit : rows, p.decode_rows);
+    const int64_t items = B * ceil_div(most_rows, p.decode_rows);
     const int64_t most = ceil_div(items * tiles, kLeastTiles), padded = items * ceil_div(tiles, kLeastTiles);
-    p.pad = padded <= resident / hkv;
-    p.shares = p.pad ? padded : (resident / hkv < most ? resident / hkv : most);
-    if (p.shares < 1) p.shares = 1;
-  }
-  if (p.tile) {
+    pad = padded <= resident / hkv;
+    const int64_t shares = pad ? padded : (resident / hkv < most ? resident / hkv : most);
+    return shares < 1 ? (int64_t)1 : shares;
+  };
+  int pad_few = 0, pad_all = 0;
+  const int64_t few = deal(many ? kLimit : rows, pad_few), all = deal(rows, pad_all);
+  p.most_shares = few > all ? few : all;
+  if (many) {
     // Whole row tiles, or equal shares of them: shares keep every CU busy to the end, but
     // cost partials (written, read and joined, some 50 000 cycles in all). In cycles, with
     // 5400 measured for two blocks' steps of 64 tokens on a CU and 4200 for one alone, from
@@ -627,13 +619,31 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t max_q, int
       p.row_tiles = (int)(per_seq < most_blocks ? per_seq : most_blocks);
       p.snake = B * hkv * per_seq <= 2 * kCus;
     }
+    // Where few rows see long sequences, the decode kernel is faster all the same, and it
+    // saves the pair of launches that a mixed batch takes (10 us): in us, from the same
+    // bounds, 0.35 a tile and 32 rows on a CU and 20 an item a block begins, half of it
+    // with 64 channels, against the tile kernel's cycles at 2.4 GHz. Whole calls
+    // with it and without: 17 tokens after 1200, 16 sequences, 64 heads on 8, 30 and 67 us;
+    // 119 in a window of 2300, 11 sequences, 8 heads, 32 and 63; 54 after 59 000 59 and 76;
+    // 8 after 4000, 43 sequences, 16 heads of 64 on 1, 42 and 36.
+    const int64_t dec_seq = ceil_div(rows, p.decode_rows), dec_rows = ceil_div(T * group, p.decode_rows) + B;
+    const double items = (double)hkv * (double)(B * dec_seq < dec_rows ? B * dec_seq : dec_rows);
+    const double by_decode = head_dim / 128.0 * (items * tiles * (0.35 / kCus) + 20 * items / (2 * kCus) + 10);
+    const double by_tile = (whole < shared ? whole : shared) / 2400 + (mixed ? 10 : 0);
+    p.tile = by_tile <= by_decode;
   }
+  p.decode = !p.tile || mixed;
+  p.row_limit = p.tile ? (p.decode ? (int)kLimit : 0) : 0x7FFFFFFF;
+  p.shares = !p.decode ? 1 : (p.tile ? few : all);
+  p.pad = p.tile ? pad_few : pad_all;
   return p;
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // rows of partials, each with D sums, its reference and its sum
-int64_t decode_slots(const Plan& pl, int64_t hkv) { return pl.shares > 1 ? hkv * pl.shares * 2 * pl.decode_rows : 0; }
+int64_t decode_slots(const Plan& pl, int64_t hkv, int64_t shares) {
+  return shares > 1 ? hkv * shares * 2 * pl.decode_rows : 0;
+}
 int64_t tile_slots(const Plan& pl, int64_t hkv) { return hkv * pl.most_tshares * 2 * kTileRows; }
 size_t part_bytes(int64_t slots, int64_t D) { return round256((size_t)slots * (D * 4 + 8)); }
 
@@ -676,14 +686,15 @@ hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, i
 
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q,
                                      int64_t max_ctx) {
-  const Plan pl = make_plan(T, B, hq, hkv, max_q, max_ctx, 0);
-  return part_bytes(decode_slots(pl, hkv), head_dim) + part_bytes(tile_slots(pl, hkv), head_dim);
+  const Plan pl = make_plan(T, B, hq, hkv, head_dim, max_q, max_ctx, 0);
+  // whichever kernels run: a shorter batch may take others than the longest
+  return part_bytes(decode_slots(pl, hkv, pl.most_shares), head_dim) + part_bytes(tile_slots(pl, hkv), head_dim);
 }
 
 hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
                                 int64_t max_q, int64_t max_ctx, int64_t window, float scale, const void* cache,
                                 const Kv4View& c, uint16_t* out, float* lse, void* workspace, hipStream_t stream) {
-  const Plan pl = make_plan(T, c.B, hq, c.kv_heads, max_q, max_ctx, window);
+  const Plan pl = make_plan(T, c.B, hq, c.kv_heads, head_dim, max_q, max_ctx, window);
   const KvCache a = kv4_cache_args(c, T, head_dim);
   AttnArgs p = {};
   p.q = reinterpret_cast<const f16*>(q);
@@ -692,7 +703,7 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.out = reinterpret_cast<f16*>(out);
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  const int64_t slots = decode_slots(pl, c.kv_heads), tslots = pl.tshares > 1 ? tile_slots(pl, c.kv_heads) : 0;
+  const int64_t slots = decode_slots(pl, c.kv_heads, pl.shares), tslots = pl.tile && pl.tshares > 1 ? tile_slots(pl, c.kv_heads) : 0;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_s = reinterpret_cast<float2*>(ws + (size_t)slots * head_dim * 4);
   ws += part_bytes(slots, head_dim);

@@ -110,8 +110,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
     f32x16 acc[CT];
 #pragma unroll
     for (int t = 0; t < CT; ++t) acc[t] = f32x16{};
-    float ref = kNoRef, sum = 0.0f, vexp = 0.0f;
-    uint32_t vbits = 0;
+    float ref = kNoRef, sum = 0.0f;
 
     // each wave turns one tile's keys or values into LDS operands: waves 0, 1 the first
     // tile's of a step, waves 2, 3 the second's. Page numbers come through the scalar
@@ -223,20 +222,9 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
         for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[u][e]);
         vmax = max(vmax, max(max_bits8(vs[u][0]), max_bits8(vs[u][1])));
       }
-      mx *= p.c;
-      if (__any(vmax > vbits || mx + vexp - kTop > ref + kSlack)) {
-        uint32_t top = vmax;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-        float grown = 0.0f;
-        if (top > vbits) {
-          const float ve = (float)((int)(top >> 10) + 1 - 15);
-          grown = vbits == 0 ? 0.0f : ve - vexp;
-          vexp = ve;
-          vbits = ((top >> 10) << 10) | 0x3FFu;
-        }
-        const float m = fmaxf(mx, __shfl_xor(mx, 32));
-        const float to = fmaxf(ref + grown, m + vexp - kTop);
+      mx = __builtin_fmaf(mx, p.c, bound_of(vmax));
+      if (__any(mx - kTop > ref + kSlack)) {
+        const float to = fmaxf(ref, fmaxf(mx, __shfl_xor(mx, 32)) - kTop);
         const float f = exp2_hw(ref - to);
         ref = to;
         sum *= f;

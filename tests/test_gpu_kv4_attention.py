@@ -38,6 +38,26 @@ def test_several_tokens(gpu_lib, new, ctx, hq, hkv, page, d):
     check(*b.attention(), b.reference())
 
 
+@pytest.mark.parametrize("new,ctx,hq,hkv,d,window,page", [
+    ([500], [500], 32, 4, 64, 0, 64),                        # whole row tiles
+    ([500, 333], [500, 1000], 16, 2, 128, 0, 32),
+    ([300], [3000], 16, 2, 128, 0, 64),                      # shares of them, joined
+    ([200] * 12, [2400] * 6 + [200, 1111, 2399, 201, 999, 31], 10, 2, 64, 0, 96),
+    ([65], [20000], 16, 1, 128, 0, 64),                      # many shares of one
+    ([130], [72000], 16, 1, 64, 0, 128),
+    ([500, 1, 40, 1, 0], [3000, 2500, 100, 1, 70], 16, 2, 128, 0, 64),   # single tokens beside them
+    ([600], [1500], 16, 2, 128, 500, 32),                    # windows
+    ([700, 600], [300, 2000], 16, 2, 128, 0, 64),            # leading rows that see nothing
+    ([700, 600], [300, 2000], 16, 2, 128, 70, 64),
+    ([160] * 80, list(range(160, 240)), 7, 1, 64, 0, 32),    # more than 64 sequences
+])
+def test_many_rows(gpu_lib, new, ctx, hq, hkv, d, window, page):
+    import torch
+    say(f"[kv4 many rows] new={new} ctx={ctx} hq={hq} hkv={hkv} d={d} window={window} page={page}")
+    b = Batch(gpu_lib, torch, new, ctx, hq, hkv, d, page, seed=sum(ctx) + d).fill()
+    check(*b.attention(window=window), b.reference(window=window))
+
+
 @pytest.mark.parametrize("hint", [20, 600])
 @pytest.mark.parametrize("B,hkv", [(3, 4), (100, 1), (150, 2)])
 def test_less_work_than_blocks(gpu_lib, B, hkv, hint):
@@ -86,7 +106,8 @@ def test_rows_that_see_nothing(gpu_lib, d):
 
 
 @pytest.mark.parametrize("hint_q,hint_ctx", [(0, 0), (1, 1), (1, 100000), (1000, 40), (None, None), (60, 2500)])
-@pytest.mark.parametrize("new,ctx,hq,hkv", [([1, 1, 1], [2300, 1, 77], 8, 2), ([60, 1, 9], [2500, 900, 9], 8, 2)])
+@pytest.mark.parametrize("new,ctx,hq,hkv", [([1, 1, 1], [2300, 1, 77], 8, 2), ([60, 1, 9], [2500, 900, 9], 8, 2),
+                                            ([300, 1, 9], [1500, 900, 9], 16, 2)])
 def test_hints_only_shape_the_launch(gpu_lib, hint_q, hint_ctx, new, ctx, hq, hkv):
     """max_q and max_ctx far too small and far too large: other splits, the same rows."""
     import torch
@@ -105,7 +126,7 @@ def test_long_sequences_are_split(gpu_lib, new, ctx, hq, hkv, d):
     check(*b.attention(), b.reference())
 
 
-@pytest.mark.parametrize("new,ctx", [([1, 1], [700, 2100]), ([50], [1200])])
+@pytest.mark.parametrize("new,ctx", [([1, 1], [700, 2100]), ([50], [1200]), ([1900], [1900])])
 def test_values_and_scores_of_all_sizes(gpu_lib, new, ctx):
     """Value scales that grow along the sequence from 2^-13 to 2^11, and from large to small;
     scores that rise and fall by hundreds: the running reference moves, and moves back
