@@ -283,7 +283,8 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
         for (int n = 0; n < NT; ++n) sc[n] = f32x4{};
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const f16x8 k = as_f16x8(codes_minus_zero_x16(cur.k[(KW * half + w) >> 2][(KW * half + w) & 3], magic, kz.bias[half], kz.nbias16[half]));
+          const uint32_t word = cur.k[(KW * half + w) >> 2][(KW * half + w) & 3];
+          const f16x8 k = as_f16x8(codes_minus_zero_x16(word, magic, kz.bias[half], kz.nbias16[half]));
 #pragma unroll
           for (int n = 0; n < NT; ++n) sc[n] = mfma_16x16x32(k, qf[n][w], sc[n]);
         }
@@ -415,7 +416,8 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
             *reinterpret_cast<f16x4*>(dst + i) =
                 f16x4{(f16)(o[i] * inv), (f16)(o[i + 1] * inv), (f16)(o[i + 2] * inv), (f16)(o[i + 3] * inv)};
           }
-          if (part == 0 && p.lse != nullptr) p.lse[at_row] = total_sum > 0.0f ? (best + log2f(total_sum)) * kLn2 : -INFINITY;
+          if (part == 0 && p.lse != nullptr)
+            p.lse[at_row] = total_sum > 0.0f ? (best + log2f(total_sum)) * kLn2 : -INFINITY;
         }
       }
     }
@@ -424,9 +426,10 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
   }
 }
 
-// Joins the decode kernel's partials of rows that were split. W waves per row (1, 4 or 16, so that a wave takes about eight);
-// rows that are already written are left alone. by_sequence: the rows looked at are the
-// first row_limit of each sequence and head, not all of the output.
+// Joins the decode kernel's partials of rows that were split. W waves per row (1, 4 or
+// 16, so that a wave takes about eight); rows that are already written are left alone.
+// by_sequence: the rows looked at are the first row_limit of each sequence and head, not
+// all of the output.
 template <int D, int W>
 __global__ void __launch_bounds__(W < 4 ? 256 : 64 * W)
 kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
@@ -703,7 +706,8 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.out = reinterpret_cast<f16*>(out);
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  const int64_t slots = decode_slots(pl, c.kv_heads, pl.shares), tslots = pl.tile && pl.tshares > 1 ? tile_slots(pl, c.kv_heads) : 0;
+  const int64_t slots = decode_slots(pl, c.kv_heads, pl.shares);
+  const int64_t tslots = pl.tile && pl.tshares > 1 ? tile_slots(pl, c.kv_heads) : 0;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_s = reinterpret_cast<float2*>(ws + (size_t)slots * head_dim * 4);
   ws += part_bytes(slots, head_dim);

@@ -5,7 +5,7 @@
 // step: two barriers, between which the waves unpack a quarter of the step's codes each
 // into LDS as the products' operands, and after which every wave reads all of them, once
 // for each of its two products (keys . queries^T, values^T . weights^T, 32x32x16). Queries,
-// scores, weights and sums stay in registers (232 of 256: two blocks a CU). The codes of
+// scores, weights and sums stay in registers (251 of 256: two blocks a CU). The codes of
 // the next step are on their way meanwhile.
 //
 // Measured: 1357 tokens in chunks of 700, 535 and 122 after up to 6000, 32 heads on 8: 126
