@@ -26,7 +26,7 @@ struct AttnArgs {
   float* tpart_o;     // the same of the tile kernel: [block][2][kTileRows][D]
   float2* tpart_s;    // [block][2][kTileRows]
   int hq, group;      // query heads, and those of one key/value head
-  int window;         // 0: none
+  int window;         // 0: none, also where the pages hold no more tokens than it
   float c;            // scale * log2(e)
   int shares, least;  // decode kernel: blocks a head, and the fewest tiles of one
   int pad;            // items count as multiples of `least` steps: one item a block
@@ -43,7 +43,8 @@ struct TileRange {
 };
 __device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& p, int row0, int row1) {
   const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
-  const int lo = p.window > 0 ? max(p0 - p.window + 1, 0) : 0;
+  // (compared before it is subtracted: rows before the first token have p0 < 0)
+  const int lo = p.window > 0 && p0 >= p.window ? p0 - p.window + 1 : 0;
   TileRange r;
   r.t0 = lo / kKvTile;
   r.t1 = p1 < lo ? r.t0 : p1 / kKvTile + 1;

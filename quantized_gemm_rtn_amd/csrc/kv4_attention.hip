@@ -295,7 +295,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
       }
 
       const int first = tile * kKvTile;
-      const bool edge = first + kKvTile - 1 > p0 || (p.window > 0 && first <= p1 - p.window);
+      const bool edge = first + kKvTile - 1 > p0 || (p.window > 0 && p1 - first >= p.window);
       uint32_t seen[NT];
       if (edge) {
         // tokens past a row's own, before its window or past the cache's end: whatever
@@ -306,7 +306,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int t = first + 4 * g + (e & 3) + 16 * (e >> 2);
-            const bool see = t <= pos[n] && (p.window == 0 || t > pos[n] - p.window);
+            const bool see = t <= pos[n] && (p.window == 0 || pos[n] - t < p.window);
             x[n][e] = see ? x[n][e] : -INFINITY;
             seen[n] |= see ? 1u << e : 0u;
           }
@@ -697,6 +697,8 @@ size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t h
 hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
                                 int64_t max_q, int64_t max_ctx, int64_t window, float scale, const void* cache,
                                 const Kv4View& c, uint16_t* out, float* lse, void* workspace, hipStream_t stream) {
+  // a window of all tokens that the pages hold hides none
+  if (window >= c.max_pages * c.page_tokens) window = 0;
   const Plan pl = make_plan(T, c.B, hq, c.kv_heads, head_dim, max_q, max_ctx, window);
   const KvCache a = kv4_cache_args(c, T, head_dim);
   AttnArgs p = {};

@@ -196,14 +196,14 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
           }
         }
       const int first = tile * kKvTile;
-      const bool edge = first + 2 * kKvTile - 1 > p0 || (p.window > 0 && first <= p1 - p.window) || tile + 1 >= end;
+      const bool edge = first + 2 * kKvTile - 1 > p0 || (p.window > 0 && p1 - first >= p.window) || tile + 1 >= end;
       if (edge) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int t = first + 32 * u + 8 * (e >> 2) + 4 * hl + (e & 3);
-            const bool see = t <= pos && (p.window == 0 || t > pos - p.window) && tile + u < end;
+            const bool see = t <= pos && (p.window == 0 || pos - t < p.window) && tile + u < end;
             sc[u][e] = see ? sc[u][e] : -INFINITY;
           }
 #pragma unroll
