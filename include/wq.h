@@ -386,7 +386,9 @@ int wq_linear_w4a8_quantized(const int8_t* xq, const float* sx, const uint16_t* 
  * float32 inside and one rounding at each output:
  *   h = x + residual,   y = h / sqrt(mean over the row of h^2 + eps) * weight.
  * K is a positive multiple of 16 here (products need a multiple of 128), eps >= 0 and
- * finite (WQ_ERR_UNSUPPORTED otherwise); a row of zeros with eps = 0 gives NaN.
+ * finite (WQ_ERR_UNSUPPORTED otherwise). A NaN or an infinity in a row, or a row of zeros
+ * with eps = 0, makes NaN of what the formula makes NaN of; in 8 bits, where codes have
+ * none, it is the row's scale (and so all its values, and its products) that is NaN.
  *  x         [M, K] fp16, 16-byte aligned.
  *  residual  [M, K] fp16, 16-byte aligned, or NULL (h = x).
  *  weight    [K] fp16, 16-byte aligned.
@@ -400,7 +402,8 @@ int wq_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* 
 
 /*
  * wq_add_rmsnorm_int8 - y in 8 bits, as wq_linear_w4a8_quantized reads it: with
- * s = amax / 127 over the row's channels that are not outliers (1 when amax is 0),
+ * s = amax / 127 over the row's channels that are not outliers (1 when amax is 0, NaN when
+ * one of them is NaN),
  *  xq  [M, K] int8 out, 16-byte aligned: rint(y / s) in the byte order of
  *      wq_quantize_act_int8, 0 on outlier channels (y is not rounded to fp16 first, and
  *      1 / s is applied as a factor, so a value within a few float32 roundings of a

@@ -4,7 +4,9 @@
 //   h = x + residual (float32, never rounded inside),   y = h / sqrt(mean(h^2) + eps) * weight,
 // and for the INT8 output, over the channels that are not outliers,
 //   s = amax|y| / 127 (1 when amax is 0),   xq = rint(y * (1 / s)),   0 on outlier channels,
-// the outlier channels' y going to xo in fp16. h is also written, rounded to fp16: it
+// the outlier channels' y going to xo in fp16. The maximum keeps a NaN, which so becomes the
+// row's scale: codes have none, and without it a row that an infinity or a NaN came into
+// (or one of zeros with eps = 0) would leave as a plain row of zeros. h is also written, rounded to fp16: it
 // is the residual of the next block.
 //
 // One block per row. A thread holds its channels of the row in registers between the
@@ -58,20 +60,20 @@ __device__ __forceinline__ void load_h(const f16* x, const f16* residual, uint32
 }
 
 // Sum (or maximum) over the block's threads, the same value in every thread, added in
-// a fixed order. red holds one value a wave; the two reductions of a row use two arrays,
+// a fixed order; the maximum keeps a NaN. red holds one value a wave; the two reductions of a row use two arrays,
 // so one barrier each is enough.
 template <bool kMax>
 __device__ __forceinline__ float block_reduce(float v, float* red) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     const float o = __shfl_xor(v, off);
-    v = kMax ? fmaxf(v, o) : v + o;
+    v = kMax ? __builtin_elementwise_maximum(v, o) : v + o;
   }
   const int waves = blockDim.x >> 6;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float r = red[0];
-  for (int w = 1; w < waves; ++w) r = kMax ? fmaxf(r, red[w]) : r + red[w];
+  for (int w = 1; w < waves; ++w) r = kMax ? __builtin_elementwise_maximum(r, red[w]) : r + red[w];
   return r;
 }
 
@@ -92,7 +94,8 @@ __device__ __forceinline__ int load_outlier(const int32_t* outliers, int n_out, 
 }
 
 // Eight INT8 values of channels e0, e1, .. as bytes: y * inv + 1.5 * 2^23 rounds half to
-// even and leaves the integer's two's complement in the low byte (|y * inv| <= 127).
+// even and leaves the integer's two's complement in the low byte (|y * inv| <= 127; in a row
+// whose scale is NaN the bytes stand for nothing).
 __device__ __forceinline__ uint32_t pack_int8(float a, float b, float c, float d, float inv) {
   const float magic = 12582912.0f;
   const uint32_t ia = __builtin_bit_cast(uint32_t, __builtin_fmaf(a, inv, magic));
@@ -195,7 +198,7 @@ add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ we
         if (t + u * nt < units) {
           clear(h[u], t + u * nt);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(h[u][e]));
+          for (int e = 0; e < 16; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(h[u][e]));
         }
       // (a long row's further units: h stays unwritten until the last pass reads them again)
       if constexpr (kLong)
@@ -204,11 +207,11 @@ add_rmsnorm_kernel(const f16* x, const f16* residual, const f16* __restrict__ we
           reload(g, unit, false);
           clear(g, unit);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(g[e]));
+          for (int e = 0; e < 16; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(g[e]));
         }
       amax = block_reduce<true>(amax, red_max);
-      const float s = amax > 0.0f ? amax / 127.0f : 1.0f;
-      const float inv = amax > 0.0f ? 127.0f / amax : 1.0f;
+      const float s = amax == 0.0f ? 1.0f : amax / 127.0f;
+      const float inv = amax == 0.0f ? 1.0f : 127.0f / amax;
       if (t == 0) sx[m] = s;
       if (t < kNormOutliers) xo[m * kNormOutliers + t] = t < n_out ? (f16)(oh * r * ow) : (f16)0.0f;
       // byte order of the 16 channels: 0,2,4,6, 1,3,5,7, 8,10,12,14, 9,11,13,15
