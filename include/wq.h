@@ -488,7 +488,7 @@ size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, i
  *  window  0 for none, else >= 1.
  *  out     [T, q_heads, head_dim] fp16 out, contiguous, 8-byte aligned.
  *  lse     [T, q_heads] float32 out, or NULL: log of the sum of exp(scale * q . k_t)
- *          (-infinity where no token is seen).
+ *          (-infinity where no token is seen, NaN where the row's scores hold one).
  *  workspace  256-byte aligned, wq_kv4_attention_workspace_bytes bytes for the same
  *          sizes (may be NULL when that is 0); contents on entry do not matter.
  * Scores, maxima and sums are fp32; a weight is rounded once to fp16, times its value

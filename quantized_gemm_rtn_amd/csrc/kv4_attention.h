@@ -52,6 +52,13 @@ __device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& 
 }
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// What a row's sum of weights makes of its outputs, and the row's log of the sum of
+// exponentials: 0 and -infinity where no token is seen (the sum is 0), NaN where a score was.
+__device__ __forceinline__ float inverse_sum(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+__device__ __forceinline__ float log_sum(float ref, float sum) {
+  return sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+}
+
 // a * b with the fp16 factor read as it is (one mixed-precision instruction; the sum with
 // 0 keeps the compiler from splitting it into a conversion and a product)
 __device__ __forceinline__ float mul_mix(float a, f16 b) { return __builtin_fmaf(a, (float)b, 0.0f); }

@@ -408,7 +408,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
         } else {
           const int tok = row / p.group;
           const int64_t at_row = (int64_t)(s.first_row + tok) * p.hq + h * p.group + (row - tok * p.group);
-          const float inv = total_sum > 0.0f ? 1.0f / total_sum : 0.0f;
+          const float inv = inverse_sum(total_sum);
           f16* dst = p.out + at_row * D + CT * part;
 #pragma unroll
           for (int i = 0; i < CT; i += 4) {
@@ -417,7 +417,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
                 f16x4{(f16)(o[i] * inv), (f16)(o[i + 1] * inv), (f16)(o[i + 2] * inv), (f16)(o[i + 3] * inv)};
           }
           if (part == 0 && p.lse != nullptr)
-            p.lse[at_row] = total_sum > 0.0f ? (best + log2f(total_sum)) * kLn2 : -INFINITY;
+            p.lse[at_row] = log_sum(best, total_sum);
         }
       }
     }
@@ -541,11 +541,11 @@ kv4_combine_kernel(KvCache a, AttnArgs p, int by_sequence) {
       for (int w = 1; w < W; ++w) o[e] += joined[w][N * lane + e];
     }
   }
-  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  const float inv = inverse_sum(total);
   f16* dst = p.out + out_row * D + N * lane;
 #pragma unroll
   for (int e = 0; e < N; ++e) dst[e] = (f16)(o[e] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[out_row] = total > 0.0f ? (best + log2f(total)) * kLn2 : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) p.lse[out_row] = log_sum(best, total);
 }
 
 namespace {

@@ -261,7 +261,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
                 f32x4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]};
         if (hl == 0) p.tpart_s[place] = make_float2(ref, sum);
       } else {
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float inv = inverse_sum(sum);
         f16* dst = p.out + slot * D + 4 * hl;
         typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
@@ -271,7 +271,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
             *reinterpret_cast<f16x4*>(dst + 32 * t + 8 * q) =
                 f16x4{(f16)(acc[t][4 * q] * inv), (f16)(acc[t][4 * q + 1] * inv), (f16)(acc[t][4 * q + 2] * inv),
                       (f16)(acc[t][4 * q + 3] * inv)};
-        if (hl == 0 && p.lse != nullptr) p.lse[slot] = sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+        if (hl == 0 && p.lse != nullptr) p.lse[slot] = log_sum(ref, sum);
       }
     }
   }
@@ -376,13 +376,13 @@ kv4_tile_combine_kernel(KvCache a, AttnArgs p) {
     if (row > row1) return;
     const int tok = row / p.group;
     const int64_t out_row = (int64_t)(t.s.first_row + tok) * p.hq + h * p.group + (row - tok * p.group);
-    const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+    const float inv = inverse_sum(all);
     typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int j = 0; j < N; ++j)
       *reinterpret_cast<f16x4*>(p.out + out_row * D + 64 * j + 4 * part) =
           f16x4{(f16)(v[j][0] * inv), (f16)(v[j][1] * inv), (f16)(v[j][2] * inv), (f16)(v[j][3] * inv)};
-    if (part == 0 && p.lse != nullptr) p.lse[out_row] = all > 0.0f ? (top + log2f(all)) * kLn2 : -INFINITY;
+    if (part == 0 && p.lse != nullptr) p.lse[out_row] = log_sum(top, all);
   };
   if constexpr (PW == 1) {
 #pragma unroll
