@@ -50,6 +50,9 @@ PER_FILE = {"quant.hip": ["-ffp-contract=off"], "split.hip": ["-ffp-contract=off
 # reports each kernel's per-lane scratch, and any use of it fails the build.
 NO_SCRATCH = {"gemv.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip", "lowrank.hip", "w4a8.hip", "norm.hip",
               "kv4_cache.hip", "kv4_attention.hip", "kv4_tile.hip"}
+# Kernels whose plan counts on so many waves a SIMD (two blocks a CU): a register too many
+# would halve them without another sign.
+LEAST_WAVES = {"kv4_tile.hip": {"kv4_tile_kernel": 2}}
 RESOURCE_REMARK = "-Rpass-analysis=kernel-resource-usage"
 
 
@@ -74,22 +77,38 @@ def _compile(src: str, verbose: bool) -> str:
         bad = scratch_users(r.stderr)
         if bad:
             raise RuntimeError(f"{src}: kernels using scratch memory (bytes per lane): {bad}")
+        bad = too_few_waves(r.stderr, LEAST_WAVES.get(src, {}))
+        if bad:
+            raise RuntimeError(f"{src}: kernels with fewer waves a SIMD than planned: {bad}")
     elif verbose and r.stderr.strip():
         print(r.stderr, file=sys.stderr)
     return obj
 
 
-def scratch_users(remarks: str) -> dict:
-    """Kernels with a nonzero ScratchSize in the compiler's resource-usage remarks."""
-    bad, name = {}, None
+def _resource(remarks: str, what: str):
+    """(kernel, value) of a number in the compiler's resource-usage remarks."""
+    name = None
     for line in remarks.splitlines():
         m = re.search(r"Function Name: (\S+)", line)
         if m:
             name = m.group(1)
             continue
-        m = re.search(r"ScratchSize \[bytes/lane\]: (\d+)", line)
-        if m and name is not None and int(m.group(1)) > 0:
-            bad[name] = int(m.group(1))
+        m = re.search(re.escape(what) + r": (\d+)", line)
+        if m and name is not None:
+            yield name, int(m.group(1))
+
+
+def scratch_users(remarks: str) -> dict:
+    """Kernels with a nonzero ScratchSize in the compiler's resource-usage remarks."""
+    return {name: n for name, n in _resource(remarks, "ScratchSize [bytes/lane]") if n > 0}
+
+
+def too_few_waves(remarks: str, least: dict) -> dict:
+    """Kernels below the waves a SIMD in `least` (by a part of their name); a part that no
+    kernel's name has comes back as None."""
+    waves = list(_resource(remarks, "Occupancy [waves/SIMD]"))
+    bad = {part: None for part in least if not any(part in name for name, _ in waves)}
+    bad.update({name: n for name, n in waves for part, want in least.items() if part in name and n < want})
     return bad
 
 

@@ -37,14 +37,19 @@ struct AttnArgs {
   int row_limit;      // sequences with more rows of a head belong to the tile kernel
 };
 
+// The last token that the window of a row at this position has passed, -1 for none (compared
+// before it is subtracted: rows before the first token have negative positions).
+__device__ __forceinline__ int last_passed(const AttnArgs& p, int pos) {
+  return p.window > 0 && pos >= p.window ? pos - p.window : -1;
+}
+
 // Tiles [t0, t1) of a sequence that rows row0 .. row1 (of one head group) can see.
 struct TileRange {
   int t0, t1;
 };
 __device__ __forceinline__ TileRange tile_range(const KvSeq& s, const AttnArgs& p, int row0, int row1) {
   const int p0 = s.ctx - s.rows + row0 / p.group, p1 = s.ctx - s.rows + row1 / p.group;
-  // (compared before it is subtracted: rows before the first token have p0 < 0)
-  const int lo = p.window > 0 && p0 >= p.window ? p0 - p.window + 1 : 0;
+  const int lo = last_passed(p, p0) + 1;
   TileRange r;
   r.t0 = lo / kKvTile;
   r.t1 = p1 < lo ? r.t0 : p1 / kKvTile + 1;

@@ -180,7 +180,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
 
     // the lane's query rows: operands of the first product, and position
     f16x8 qf[NT][KW];
-    int pos[NT];
+    int pos[NT], passed[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = row0 + kDecodeRows * n + c;
@@ -188,6 +188,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
       const int tok = valid ? row / p.group : 0;
       const int head = h * p.group + (valid ? row - tok * p.group : 0);
       pos[n] = valid ? s.ctx - s.rows + tok : -1;
+      passed[n] = last_passed(p, pos[n]);
       const f16* qp = p.q + (int64_t)(s.first_row + tok) * p.q_stride + head * D + (D / 4) * g;
 #pragma unroll
       for (int w = 0; w < KW; ++w) qf[n][w] = as_f16x8(*reinterpret_cast<const uint4*>(qp + 8 * w));
@@ -306,7 +307,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int t = first + 4 * g + (e & 3) + 16 * (e >> 2);
-            const bool see = t <= pos[n] && (p.window == 0 || pos[n] - t < p.window);
+            const bool see = t <= pos[n] && t > passed[n];
             x[n][e] = see ? x[n][e] : -INFINITY;
             seen[n] |= see ? 1u << e : 0u;
           }

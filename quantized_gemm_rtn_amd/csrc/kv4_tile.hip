@@ -5,8 +5,10 @@
 // step: two barriers, between which the waves unpack a quarter of the step's codes each
 // into LDS as the products' operands, and after which every wave reads all of them, once
 // for each of its two products (keys . queries^T, values^T . weights^T, 32x32x16). Queries,
-// scores, weights and sums stay in registers (251 of 256: two blocks a CU). The codes of
-// the next step are on their way meanwhile.
+// scores, weights and sums stay in registers: 251 of the 256 that two blocks a CU have, which
+// the build checks (with 258 a prompt of 2048 took 96 us instead of 63; the same bound given
+// to the compiler changes its schedule, 75 us). The codes of the next step are on their way
+// meanwhile.
 //
 // Measured: 1357 tokens in chunks of 700, 535 and 122 after up to 6000, 32 heads on 8: 126
 // GFLOP in 180 us (0.70 PFLOP/s); a prompt of 2048 62 us, of which its last rows' 32 steps,
@@ -98,7 +100,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
     const bool valid = row < rows;
     const int tok = valid ? row / p.group : 0;
     const int head = h * p.group + (valid ? row - tok * p.group : 0);
-    const int pos = valid ? s.ctx - s.rows + tok : -1;
+    const int pos = valid ? s.ctx - s.rows + tok : -1, passed = last_passed(p, pos);
     f16x8 qf[KS];
     const f16* qp = p.q + (int64_t)(s.first_row + tok) * p.q_stride + head * D + 8 * hl;
 #pragma unroll
@@ -203,7 +205,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int t = first + 32 * u + 8 * (e >> 2) + 4 * hl + (e & 3);
-            const bool see = t <= pos && (p.window == 0 || pos - t < p.window) && tile + u < end;
+            const bool see = t <= pos && t > passed && tile + u < end;
             sc[u][e] = see ? sc[u][e] : -INFINITY;
           }
 #pragma unroll
