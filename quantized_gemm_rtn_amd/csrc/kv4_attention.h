@@ -9,8 +9,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNoRef = -1e30f;      // reference of a row that has seen nothing
-constexpr float kTop = 10.0f;         // log2 of the largest weight times value scale after a move of r,
-constexpr float kSlack = 4.0f;        // and how far it may grow before the next
+constexpr float kTop = 12.8f;         // log2 of the largest weight times value scale after a move of r,
+constexpr float kSlack = 3.1f;        // how far it may grow before the next (fp16 ends at 2^16),
+constexpr float kMixed = 3.0f;        // and how far below that top it may stay
+constexpr uint32_t kAlike = 2 << 10;  // value scales whose bits differ by less are within 2^kMixed
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kTileRows = 128;        // query rows of a block of kv4_tile_kernel
 constexpr int kDecodeRows = 16;       // query rows of one column tile
@@ -68,17 +70,33 @@ __device__ __forceinline__ float log_sum(float ref, float sum) {
 // 0 keeps the compiler from splitting it into a conversion and a product)
 __device__ __forceinline__ float mul_mix(float a, f16 b) { return __builtin_fmaf(a, (float)b, 0.0f); }
 
-// largest of eight positive fp16 values, as bits (positive fp16 order like integers)
-__device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
+// largest and smallest of eight fp16 values of at least 0, as bits (these order like integers)
+template <class F>
+__device__ __forceinline__ uint32_t of_eight(const f16x8& v, F pick) {
   const uint4 d = __builtin_bit_cast(uint4, v);
-  const u16x2 a = __builtin_elementwise_max(__builtin_bit_cast(u16x2, d.x), __builtin_bit_cast(u16x2, d.y));
-  const u16x2 b = __builtin_elementwise_max(__builtin_bit_cast(u16x2, d.z), __builtin_bit_cast(u16x2, d.w));
-  const u16x2 m = __builtin_elementwise_max(a, b);
-  return max((uint32_t)m.x, (uint32_t)m.y);
+  const u16x2 a = pick(__builtin_bit_cast(u16x2, d.x), __builtin_bit_cast(u16x2, d.y));
+  const u16x2 b = pick(__builtin_bit_cast(u16x2, d.z), __builtin_bit_cast(u16x2, d.w));
+  const u16x2 m = pick(a, b);
+  return pick(u16x2{m.x, 0}, u16x2{m.y, 0}).x;
+}
+__device__ __forceinline__ uint32_t max_bits8(const f16x8& v) {
+  return of_eight(v, [](u16x2 x, u16x2 y) { return __builtin_elementwise_max(x, y); });
+}
+__device__ __forceinline__ uint32_t min_bits8(const f16x8& v) {
+  return of_eight(v, [](u16x2 x, u16x2 y) { return __builtin_elementwise_min(x, y); });
 }
 
-// log2 of the power of two above a positive normal fp16 with these bits
-__device__ __forceinline__ float bound_of(uint32_t bits) { return (float)((int)(bits >> 10) - 14); }
+// log2 of the fp16 with these bits
+__device__ __forceinline__ float log2_bits(uint32_t bits) {
+  return __builtin_amdgcn_logf((float)__builtin_bit_cast(f16, (uint16_t)bits));
+}
+
+// A row's reference after a tile, from the row's `sum` (of the lanes' top scores and bounds on
+// their value scales) and `one` (the largest that one token has of both); a row that does not
+// need to move stays, whatever the wave's other rows do.
+__device__ __forceinline__ float moved_reference(float ref, float sum, float one) {
+  return sum - kTop > ref + kSlack ? fmaxf(ref, fminf(sum, one + kMixed) - kTop) : ref;
+}
 
 // value of a lane of the wave (64 bits)
 __device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {

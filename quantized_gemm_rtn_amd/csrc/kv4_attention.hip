@@ -19,12 +19,14 @@
 // maxima, sums and outputs are fp32.
 //
 // The reference r keeps the fp16 operands in range and precise: weights times value
-// scales, 2^(x - r) u, are held near 2^10 at the row's largest, at most 2^14. It is the
-// largest sum of a lane's top score of a tile and the power of two above its value scales
-// there, and only moves (and everything summed so far is only rescaled) when one passes
-// that bound by 4, which any lane can see without asking the others. (With the largest
-// score and the largest scale of the whole row instead, tokens of small scales that take
-// a row after others of scales 2^24 as large lost their operands' last bits.)
+// scales, 2^(x - r) u, are near 2^12.8 at the row's largest and at most 2^15.9, so that a
+// token of the smallest scale keeps its bits beside one of the largest (2^27 apart). It
+// only moves (and everything summed so far is only rescaled) when a lane's top score and
+// log2 of its largest value scale pass that bound together, which any lane can see without
+// asking the others. These may be two tokens', and their sum up to 27 more than any one
+// has; so where r moves to is found token by token, score plus log2 of its own scale, of
+// which the lane's sum may take it no further than kMixed. (With the sums alone operands
+// were subnormal where tokens of unlike scales stood side by side, and lost their last bits.)
 //
 //  kv4_decode_kernel   few query rows (16 or 32 a block): all tiles of all sequences are
 //    dealt out in equal shares, one a block, whose four waves take tiles of 32 tokens in
@@ -322,7 +324,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
 
       float mx[NT];
       const uint32_t vmax = max_bits8(vs);
-      const float ve = bound_of(vmax);
+      const float ve = log2_bits(vmax);
       bool move = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -333,12 +335,18 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
         move |= mx[n] - kTop > ref[n] + kSlack;
       }
       if (__any(move)) {
+        const f16x8 lv = __builtin_elementwise_log2(vs);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float m = mx[n];
           m = fmaxf(m, __shfl_xor(m, 16));
           m = fmaxf(m, __shfl_xor(m, 32));
-          const float to = fmaxf(ref[n], m - kTop);
+          float one = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) one = fmaxf(one, __builtin_fmaf(x[n][e], p.c, (float)lv[e]));
+          one = fmaxf(one, __shfl_xor(one, 16));
+          one = fmaxf(one, __shfl_xor(one, 32));
+          const float to = moved_reference(ref[n], m, one);
           const float f = exp2_hw(ref[n] - to);
           ref[n] = to;
           sum[n] *= f;
