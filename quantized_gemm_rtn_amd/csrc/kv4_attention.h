@@ -12,6 +12,8 @@ constexpr float kNoRef = -1e30f;      // reference of a row that has seen nothin
 constexpr float kTop = 12.8f;         // log2 of the largest weight times value scale after a move of r,
 constexpr float kSlack = 3.1f;        // how far it may grow before the next (fp16 ends at 2^16),
 constexpr float kMixed = 3.0f;        // and how far below that top it may stay
+constexpr float kFar = 262144.0f;     // references from which float32 no longer holds these fractions,
+constexpr float kNone = 1e29f;        // up to those that no score reaches
 constexpr uint32_t kAlike = 2 << 10;  // value scales whose bits differ by less are within 2^kMixed
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kTileRows = 128;        // query rows of a block of kv4_tile_kernel
@@ -96,6 +98,13 @@ __device__ __forceinline__ float log2_bits(uint32_t bits) {
 // need to move stays, whatever the wave's other rows do.
 __device__ __forceinline__ float moved_reference(float ref, float sum, float one) {
   return sum - kTop > ref + kSlack ? fmaxf(ref, fminf(sum, one + kMixed) - kTop) : ref;
+}
+// Scores (times log2 e) so large that differences from a rounded reference are off by whole
+// powers of two, if the product by p.c is fused with the subtraction: then the products are
+// rounded first, and the largest of them is the reference.
+__device__ __forceinline__ bool is_far(float ref) { return fabsf(ref) >= kFar && fabsf(ref) < kNone; }
+__device__ __forceinline__ float far_reference(float ref, float to, float top) {
+  return fabsf(top) >= kFar ? fmaxf(ref, top) : to;
 }
 
 // value of a lane of the wave (64 bits)

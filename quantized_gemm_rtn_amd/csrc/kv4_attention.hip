@@ -27,6 +27,8 @@
 // has; so where r moves to is found token by token, score plus log2 of its own scale, of
 // which the lane's sum may take it no further than kMixed. (With the sums alone operands
 // were subnormal where tokens of unlike scales stood side by side, and lost their last bits.)
+// Where r itself is so large that float32 does not hold such fractions of it, it is the
+// largest score (see far_reference; scores of 1e8 gave infinite weights).
 //
 //  kv4_decode_kernel   few query rows (16 or 32 a block): all tiles of all sequences are
 //    dealt out in equal shares, one a block, whose four waves take tiles of 32 tokens in
@@ -240,6 +242,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
         ++page;
       }
     };
+    bool far = false;  // a row's scores are (see far_reference), the same for the wave
     int fetched = tile, stage_in = 0, stage = 0;
     const auto fetch_next = [&]() {
       if (fetched < end) fetch(stage_in);
@@ -334,8 +337,10 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
         mx[n] = __builtin_fmaf(mx[n], p.c, ve);
         move |= mx[n] - kTop > ref[n] + kSlack;
       }
-      if (__any(move)) {
+      float factor = p.c;
+      if (__any(move) || far) {
         const f16x8 lv = __builtin_elementwise_log2(vs);
+        float to[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float m = mx[n];
@@ -346,9 +351,28 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
           for (int e = 0; e < 8; ++e) one = fmaxf(one, __builtin_fmaf(x[n][e], p.c, (float)lv[e]));
           one = fmaxf(one, __shfl_xor(one, 16));
           one = fmaxf(one, __shfl_xor(one, 32));
-          const float to = moved_reference(ref[n], m, one);
-          const float f = exp2_hw(ref[n] - to);
-          ref[n] = to;
+          to[n] = moved_reference(ref[n], m, one);
+          far |= is_far(to[n]);
+        }
+        if (__any(far)) {
+          factor = 1.0f;
+          far = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, x[n][e] *= p.c);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            to[n] = far_reference(ref[n], to[n], top);
+            far |= is_far(to[n]);
+          }
+          far = __any(far);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float f = exp2_hw(ref[n] - to[n]);
+          ref[n] = to[n];
           sum[n] *= f;
 #pragma unroll
           for (int t = 0; t < CT; ++t) acc[n][t] *= f;
@@ -361,7 +385,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float w = exp2_hw(__builtin_fmaf(x[n][e], p.c, -ref[n]));
+          const float w = exp2_hw(__builtin_fmaf(x[n][e], factor, -ref[n]));
           sum[n] += w;
           wf[n][2 * (e & 3) + (e >> 2)] = (f16)mul_mix(w, vs[e]);
         }

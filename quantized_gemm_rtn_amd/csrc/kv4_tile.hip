@@ -113,6 +113,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
 #pragma unroll
     for (int t = 0; t < CT; ++t) acc[t] = f32x16{};
     float ref = kNoRef, sum = 0.0f;
+    bool far = false;  // a row's scores are (see far_reference), the same for the wave
 
     // each wave turns one tile's keys or values into LDS operands: waves 0, 1 the first
     // tile's of a step, waves 2, 3 the second's. Page numbers come through the scalar
@@ -228,7 +229,8 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
         vmax = max(vmax, max(max_bits8(vs[u][0]), max_bits8(vs[u][1])));
       }
       mx = __builtin_fmaf(mx, p.c, log2_bits(vmax));
-      if (__any(mx - kTop > ref + kSlack)) {
+      float factor = p.c;
+      if (__any(mx - kTop > ref + kSlack) || far) {
         float one = mx;
         const uint32_t vmin = min(min(min_bits8(vs[0][0]), min_bits8(vs[0][1])),
                                   min(min_bits8(vs[1][0]), min_bits8(vs[1][1])));
@@ -245,7 +247,17 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
             }
         }
         one = fmaxf(one, __shfl_xor(one, 32));
-        const float to = moved_reference(ref, fmaxf(mx, __shfl_xor(mx, 32)), one);
+        float to = moved_reference(ref, fmaxf(mx, __shfl_xor(mx, 32)), one);
+        if (__any(is_far(to)) || far) {
+          factor = 1.0f;
+          float top = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[u][e] *= p.c);
+          to = far_reference(ref, to, fmaxf(top, __shfl_xor(top, 32)));
+          far = __any(is_far(to));
+        }
         const float f = exp2_hw(ref - to);
         ref = to;
         sum *= f;
@@ -259,7 +271,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
           f16x8 wf;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float w = exp2_hw(__builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], p.c, -ref));
+            const float w = exp2_hw(__builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], factor, -ref));
             sum += w;
             wf[2 * (e & 3) + (e >> 2)] = (f16)mul_mix(w, vs[u][q][e]);
           }
