@@ -484,7 +484,7 @@ size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, i
  *  q       [T, q_heads, head_dim] fp16, 16-byte aligned, q_stride elements from one token
  *          to the next (a multiple of 8, at least q_heads * head_dim). q_heads is a
  *          multiple of kv_heads: query head j reads key/value head j / (q_heads / kv_heads).
- *  scale   positive and finite (WQ_ERR_UNSUPPORTED otherwise), 1 / sqrt(head_dim) usually.
+ *  scale   positive, at most 1e16 (WQ_ERR_UNSUPPORTED otherwise), 1 / sqrt(head_dim) usually.
  *  window  0 for none, else >= 1.
  *  out     [T, q_heads, head_dim] fp16 out, contiguous, 8-byte aligned.
  *  lse     [T, q_heads] float32 out, or NULL: log of the sum of exp(scale * q . k_t)

@@ -563,7 +563,9 @@ int wq_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t q_h
   const int rc = check_kv4_args(T, q_heads, c, head_dim, cache);
   if (rc != WQ_OK) return rc;
   if (T != 0 && B != 0 && (!q || !out)) return WQ_ERR_NULL;
-  if (!(scale > 0.0f) || scale > 3.0e38f) return WQ_ERR_UNSUPPORTED;
+  // |q . k| is below 1.2e12 (128 products of fp16 values), so scores times log2 e stay below
+  // 1e29, which the kernels keep apart from the reference of a row that has seen nothing
+  if (!(scale > 0.0f) || scale > 1.0e16f) return WQ_ERR_UNSUPPORTED;
   if (q_heads % kv_heads != 0 || q_stride < q_heads * head_dim || max_q < 0 || max_ctx < 0 || max_ctx > kMaxContext ||
       window < 0 || window >= kMax32)
     return WQ_ERR_SHAPE;

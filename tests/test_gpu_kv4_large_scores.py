@@ -56,3 +56,29 @@ def test_large_scores(gpu_lib, new, ctx, hq, hkv, d, size, sign):
                 eps = 2.0 ** -10 * np.abs(vh).max() + np.exp(-20) * seen * np.abs(vh).max()
                 assert np.all(got[row + i, h] >= lo - eps) and np.all(got[row + i, h] <= hi + eps), (i, h)
         row += n
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e16])
+@pytest.mark.parametrize("new,ctx,hq", [([1], [70], 4), ([300], [300], 8)])
+def test_scale_limits(gpu_lib, new, ctx, hq, scale):
+    """The largest scale makes every row its best token's values (scores some 1e15 apart, all
+    negative), a vanishing one their mean."""
+    import torch
+    rng = np.random.default_rng(1)
+    d, c = 128, ctx[0]
+    k = -np.abs(rng.standard_normal((c, 1, d))).astype(np.float16)
+    q = np.abs(rng.standard_normal((new[0], hq, d))).astype(np.float16)
+    b = Batch(gpu_lib, torch, new, ctx, hq, 1, d, 32, seed=2, k=k, q=q).fill()
+    out, lse = b.attention(scale=scale)
+    got, got_lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    kk, vv = oracle.kv4_values(b.k)[:, 0], oracle.kv4_values(b.v)[:, 0]
+    for i in range(0, new[0], 13):
+        seen = c - new[0] + i + 1
+        x = kk[:seen] @ b.q[i, 0].astype(np.float64)
+        want = vv[x.argmax()] if scale > 1 else vv[:seen].mean(0)
+        size = np.abs(want) if scale > 1 else np.abs(vv[:seen]).mean(0)
+        assert np.all(np.abs(got[i, 0] - want) <= 2.0 ** -10 * size + 2.0 ** -24)
+        if scale > 1:
+            assert abs(got_lse[i, 0] / (scale * x.max()) - 1) < 1e-5
+        else:
+            assert abs(got_lse[i, 0] - np.log(seen)) < 1e-5
