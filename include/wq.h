@@ -476,6 +476,13 @@ int wq_kv4_read(const void* cache, int64_t num_pages, int64_t page_tokens, int64
 size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                         int64_t max_q, int64_t max_ctx);
 
+/* The kernels that wq_kv4_attention launches for these sizes: the sum of 1 (the kernel for
+ * few rows of a sequence), 2 (the one for many rows) and 4 (many rows dealt out in equal
+ * shares and joined), plus 256 times the waves that join a row of the first one's split
+ * sequences (0 where it splits none). 0 for invalid sizes. */
+int wq_kv4_attention_plan(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
+                          int64_t max_ctx, int64_t window);
+
 /*
  * wq_kv4_attention - causal attention of the new tokens (already appended) over the
  * cache: row i of sequence b, at position p = ctx_len[b] - (its rows) + i, sees tokens

@@ -80,6 +80,7 @@ SIGNATURES = {
     "wq_kv4_read": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
                                    _vp]),
     "wq_kv4_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "wq_kv4_attention_plan": (ctypes.c_int, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
     "wq_kv4_attention": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
                                         _i64, _i64, ctypes.c_float, _i64, _vp, _vp, _vp, _sz, _vp]),
     "wq_linear_sparse_noalloc": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64,
@@ -702,6 +703,16 @@ def kv4_read(cache, page_table, seq_start, ctx_len, tokens: int, head_dim: int, 
 
 def kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx):
     return int(load().wq_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx))
+
+
+def kv4_attention_plan(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx, window: int = 0) -> dict:
+    """What ``kv4_attention`` launches for these sizes: ``few_rows`` and ``many_rows``, its two
+    kernels, ``shares`` (many rows dealt out in equal shares), and ``join_waves``, the waves
+    that join a row of split sequences (0 for none)."""
+    p = load().wq_kv4_attention_plan(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx, window)
+    if p == 0:
+        raise ValueError("invalid sizes")
+    return {"few_rows": bool(p & 1), "many_rows": bool(p & 2), "shares": bool(p & 4), "join_waves": p >> 8}
 
 
 def kv4_attention(q, cache, page_table, seq_start, ctx_len, max_q=None, max_ctx=None, scale=None, window: int = 0,

@@ -592,6 +592,7 @@ struct Plan {
   int decode_rows, row_limit;
   int64_t shares, most_shares;  // decode kernel: blocks a head, and their bound
   int pad;            // whether each has one item
+  int64_t parts;      // shares of an item, about
   int64_t tshares, most_tshares;  // tile kernel: the same (0: whole row tiles), and its bound
   int row_tiles, snake;
 };
@@ -672,6 +673,7 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, 
   p.row_limit = p.tile ? (p.decode ? (int)kLimit : 0) : 0x7FFFFFFF;
   p.shares = !p.decode ? 1 : (p.tile ? few : all);
   p.pad = p.tile ? pad_few : pad_all;
+  p.parts = p.shares / (B * ceil_div(p.tile ? kLimit : rows, p.decode_rows)) + 1;
   return p;
 }
 
@@ -683,6 +685,9 @@ int64_t decode_slots(const Plan& pl, int64_t hkv, int64_t shares) {
 int64_t tile_slots(const Plan& pl, int64_t hkv) { return hkv * pl.most_tshares * 2 * kTileRows; }
 size_t part_bytes(int64_t slots, int64_t D) { return round256((size_t)slots * (D * 4 + 8)); }
 
+// waves that join a row of `parts` partials, about: eight each
+int join_waves(int64_t parts) { return parts <= 8 ? 1 : (parts <= 32 ? 4 : 16); }
+
 // items: rows to look at; parts: those of a row, about
 template <int D>
 hipError_t combine(const KvCache& a, const AttnArgs& p, int64_t parts, int64_t items, int by_sequence,
@@ -692,9 +697,9 @@ hipError_t combine(const KvCache& a, const AttnArgs& p, int64_t parts, int64_t i
     constexpr int64_t x = 1 << 20;
     return dim3((unsigned)(blocks < x ? blocks : x), (unsigned)ceil_div(blocks, x));
   };
-  if (parts <= 8)
+  if (join_waves(parts) == 1)
     hipLaunchKernelGGL((kv4_combine_kernel<D, 1>), grid(ceil_div(items, 4)), dim3(256), 0, stream, a, p, by_sequence);
-  else if (parts <= 32)
+  else if (join_waves(parts) == 4)
     hipLaunchKernelGGL((kv4_combine_kernel<D, 4>), grid(items), dim3(256), 0, stream, a, p, by_sequence);
   else
     hipLaunchKernelGGL((kv4_combine_kernel<D, 16>), grid(items), dim3(1024), 0, stream, a, p, by_sequence);
@@ -714,7 +719,7 @@ hipError_t run(const KvCache& a, const AttnArgs& p, const Plan& pl, int64_t B, i
     e = hipGetLastError();
   }
   if (e == hipSuccess && pl.decode && pl.shares > 1)
-    e = combine<D>(a, p, pl.shares / B + 1, pl.tile ? B * hkv * p.row_limit : (int64_t)a.T * p.hq, pl.tile, stream);
+    e = combine<D>(a, p, pl.parts, pl.tile ? B * hkv * p.row_limit : (int64_t)a.T * p.hq, pl.tile, stream);
   return e;
 }
 
@@ -725,6 +730,13 @@ size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t h
   const Plan pl = make_plan(T, B, hq, hkv, head_dim, max_q, max_ctx, 0);
   // whichever kernels run: a shorter batch may take others than the longest
   return part_bytes(decode_slots(pl, hkv, pl.most_shares), head_dim) + part_bytes(tile_slots(pl, hkv), head_dim);
+}
+
+int kv4_attention_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q, int64_t max_ctx,
+                       int64_t window) {
+  const Plan pl = make_plan(T, B, hq, hkv, head_dim, max_q, max_ctx, window);
+  return (pl.decode ? 1 : 0) | (pl.tile ? 2 : 0) | (pl.tile && pl.tshares > 0 ? 4 : 0) |
+         (pl.decode && pl.shares > 1 ? join_waves(pl.parts) << 8 : 0);
 }
 
 hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,

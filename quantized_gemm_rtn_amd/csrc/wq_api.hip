@@ -544,14 +544,26 @@ int wq_kv4_read(const void* cache, int64_t num_pages, int64_t page_tokens, int64
   return hip_status(wq::launch_kv4_read(cache, T, head_dim, max_new, c, k, v, as_stream(stream)));
 }
 
+namespace {
+bool kv4_attention_sizes(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
+                         int64_t max_ctx) {
+  return T >= 1 && B >= 1 && B <= kMaxBatch && kv_heads >= 1 && kv_heads <= kMaxHeads && q_heads >= kv_heads &&
+         q_heads <= kMaxHeads && q_heads % kv_heads == 0 && T < kMax32 / q_heads && B < kMaxBlocks / q_heads &&
+         (head_dim == 64 || head_dim == 128) && max_q >= 0 && max_ctx >= 0 && max_ctx <= kMaxContext;
+}
+}  // namespace
+
 size_t wq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                         int64_t max_q, int64_t max_ctx) {
-  if (T < 1 || B < 1 || B > kMaxBatch || kv_heads < 1 || kv_heads > kMaxHeads || q_heads < kv_heads ||
-      q_heads > kMaxHeads || q_heads % kv_heads != 0 || T >= kMax32 / q_heads ||
-      B >= kMaxBlocks / q_heads || (head_dim != 64 && head_dim != 128))
-    return 0;
-  if (max_q < 0 || max_ctx < 0 || max_ctx > kMaxContext) return 0;
+  if (!kv4_attention_sizes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx)) return 0;
   return wq::kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx);
+}
+
+int wq_kv4_attention_plan(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
+                          int64_t max_ctx, int64_t window) {
+  if (!kv4_attention_sizes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx) || window < 0 || window >= kMax32)
+    return 0;
+  return wq::kv4_attention_plan(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx, window);
 }
 
 int wq_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t q_heads, int64_t kv_heads,

@@ -71,6 +71,9 @@ hipError_t launch_kv4_read(const void* cache, int64_t T, int64_t head_dim, int64
 // at least the bytes launch_kv4_attention uses with the same sizes and any window
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q,
                                      int64_t max_ctx);
+// what wq_kv4_attention_plan returns
+int kv4_attention_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q, int64_t max_ctx,
+                       int64_t window);
 hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t hq, int64_t head_dim,
                                 int64_t max_q, int64_t max_ctx, int64_t window, float scale, const void* cache,
                                 const Kv4View& c, uint16_t* out, float* lse, void* workspace, hipStream_t stream);

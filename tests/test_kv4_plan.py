@@ -1,0 +1,41 @@
+"""What the cache attention launches, from the host's plan (CPU only): the choice itself and
+the shape of the joins."""
+import pytest
+
+import quantized_gemm_rtn_amd as wq
+from test_kv4_abi import lib  # noqa: F401
+
+
+def plan(new, ctx, hq, hkv, d, window=0):
+    return wq.kv4_attention_plan(sum(new), len(new), hq, hkv, d, max(new), max(ctx), window)
+
+
+def test_sizes(lib):  # noqa: F811
+    f = lib.wq_kv4_attention_plan
+    for bad in ((0, 1, 8, 8, 128, 1, 10, 0), (1, 0, 8, 8, 128, 1, 10, 0), (1, 1, 9, 8, 128, 1, 10, 0),
+                (1, 1, 8, 8, 96, 1, 10, 0), (1, 1, 8, 8, 128, -1, 10, 0), (1, 1, 8, 8, 128, 1, -1, 0),
+                (1, 1, 8, 8, 128, 1, 10, -1), (1, 1, 8, 8, 128, 1, 10, 1 << 31)):
+        assert f(*bad) == 0
+    with pytest.raises(ValueError):
+        plan([1], [10], 9, 8, 128)
+
+
+def test_single_tokens(lib):  # noqa: F811
+    """One token each: the kernel for few rows; joined where the sequences are split, by more
+    waves where a row has more partials."""
+    assert plan([1], [32], 32, 8, 128) == dict(few_rows=True, many_rows=False, shares=False, join_waves=0)
+    assert plan([1] * 64, [8192] * 64, 64, 8, 128)["join_waves"] == 1
+    assert plan([1], [131071], 32, 8, 128)["join_waves"] == 16
+
+
+@pytest.mark.parametrize("T,B,hq,hkv,max_q,max_ctx,waves", [
+    (33, 1, 4, 1, 33, 4937, 4),      # 5 items in 512 shares
+    (76, 1, 7, 1, 76, 1914, 4),      # 17 in 512
+    (178, 1, 4, 1, 178, 780, 1),     # 23 in as many shares as items have eights of tiles
+    (2, 2, 8, 1, 1, 17868, 16),      # 2 in 512
+])
+def test_partials_of_a_row(lib, T, B, hq, hkv, max_q, max_ctx, waves):  # noqa: F811
+    """A row's partials are those of its own item of 32 rows, of which a sequence has several:
+    not all shares of the sequence."""
+    p = wq.kv4_attention_plan(T, B, hq, hkv, 128, max_q, max_ctx)
+    assert p["few_rows"] and not p["many_rows"] and p["join_waves"] == waves
