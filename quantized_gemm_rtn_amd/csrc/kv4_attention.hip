@@ -657,16 +657,23 @@ Plan make_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, 
       p.snake = B * hkv * per_seq <= 2 * kCus;
     }
     // Where few rows see long sequences, the decode kernel is faster all the same, and it
-    // saves the pair of launches that a mixed batch takes (10 us): in us, from the same
-    // bounds, 0.35 a tile and 32 rows on a CU and 20 an item a block begins, half of it
-    // with 64 channels, against the tile kernel's cycles at 2.4 GHz. Whole calls
-    // with it and without: 17 tokens after 1200, 16 sequences, 64 heads on 8, 30 and 67 us;
-    // 119 in a window of 2300, 11 sequences, 8 heads, 32 and 63; 54 after 59 000 59 and 76;
-    // 8 after 4000, 43 sequences, 16 heads of 64 on 1, 42 and 36.
+    // saves the pair of launches that a mixed batch takes. Whole calls of either, in us,
+    // fitted to both kernels' times in 1400 batches of 97 to 2000 rows a sequence (1 to 64
+    // sequences of up to 30 000 tokens, 1 to 32 heads, groups of 1 to 32, even and uneven,
+    // with and without windows). In 700 others (to 256 sequences) the kernel it takes was
+    // slower than the faster one by 1.1 % on average and 1.6 times at worst (21 and 13 us);
+    // the tile kernel always by 15 % and 3.1 times, the decode kernel 67 % and 9 times. For
+    // instance (decode, tile): 33 tokens after 4900, 4 heads on 1, 14 and 42; 52 after 6800,
+    // 64 on 8, 43 and 58; 8 after 4000, 43 sequences, 16 heads of 64 on 1, 34 and 43; 17
+    // after 1200, 16 sequences, 64 on 8, 60 and 48; up to 163, 4 sequences, 32 heads of 64
+    // on 4, 31 and 22.
     const int64_t dec_seq = ceil_div(rows, p.decode_rows), dec_rows = ceil_div(T * group, p.decode_rows) + B;
     const double items = (double)hkv * (double)(B * dec_seq < dec_rows ? B * dec_seq : dec_rows);
-    const double by_decode = head_dim / 128.0 * (items * tiles * (0.35 / kCus) + 20 * items / (2 * kCus) + 10);
-    const double by_tile = (whole < shared ? whole : shared) / 2400 + (mixed ? 10 : 0);
+    const double half = 0.5 + head_dim / 256.0;  // 64 channels take three quarters of 128's time
+    const double by_decode = 11 + half * 0.18 * items * tiles / kCus + 4 * items / (2 * kCus) +
+                             0.85e-3 * (head_dim / 128.0) * (double)(T * hq);
+    const double by_tile = 7 + half * 0.38e-3 * (whole < shared ? whole : shared) + 5.0 * blocks / (2 * kCus) +
+                           (whole <= shared ? 0 : 5) + (mixed ? 6.5 : 0);
     p.tile = by_tile <= by_decode;
   }
   p.decode = !p.tile || mixed;

@@ -39,3 +39,20 @@ def test_partials_of_a_row(lib, T, B, hq, hkv, max_q, max_ctx, waves):  # noqa: 
     not all shares of the sequence."""
     p = wq.kv4_attention_plan(T, B, hq, hkv, 128, max_q, max_ctx)
     assert p["few_rows"] and not p["many_rows"] and p["join_waves"] == waves
+
+
+@pytest.mark.parametrize("T,B,hq,hkv,d,max_q,max_ctx,window,many", [
+    (33, 1, 4, 1, 128, 33, 4937, 0, False),        # 14 us, 42 with the other kernel
+    (52, 1, 64, 8, 128, 52, 6838, 0, False),       # 43, 58
+    (344, 43, 16, 1, 64, 8, 4008, 0, False),       # 34, 43
+    (1309, 11, 8, 8, 128, 119, 2419, 2300, False),  # 54, 61
+    (272, 16, 64, 8, 128, 17, 1217, 0, True),      # 48, 60
+    (476, 4, 32, 4, 64, 163, 453, 0, True),        # 22, 31
+    (2048, 1, 32, 8, 128, 2048, 2048, 0, True),
+    (16384, 64, 64, 8, 128, 256, 4096, 0, True),
+])
+def test_the_faster_kernel_is_taken(lib, T, B, hq, hkv, d, max_q, max_ctx, window, many):  # noqa: F811
+    """Batches of more than 96 rows a sequence whose times with either kernel differ by more
+    than a tenth."""
+    p = wq.kv4_attention_plan(T, B, hq, hkv, d, max_q, max_ctx, window)
+    assert p["many_rows"] == many
