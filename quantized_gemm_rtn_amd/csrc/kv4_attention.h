@@ -88,7 +88,11 @@ __device__ __forceinline__ uint32_t min_bits8(const f16x8& v) {
   return of_eight(v, [](u16x2 x, u16x2 y) { return __builtin_elementwise_min(x, y); });
 }
 
-// log2 of the fp16 with these bits
+// log2 of an fp16 value from its bits as they stand (less by at most 0.09), and log2 of the fp16
+// with these bits
+__device__ __forceinline__ float about_log2(f16 v) {
+  return __builtin_fmaf((float)__builtin_bit_cast(uint16_t, v), 0.0009765625f, -15.0f);
+}
 __device__ __forceinline__ float log2_bits(uint32_t bits) {
   return __builtin_amdgcn_logf((float)__builtin_bit_cast(f16, (uint16_t)bits));
 }

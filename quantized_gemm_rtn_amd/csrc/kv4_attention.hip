@@ -339,7 +339,6 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
       }
       float factor = p.c;
       if (__any(move) || far) {
-        const f16x8 lv = __builtin_elementwise_log2(vs);
         float to[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -348,7 +347,7 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
           m = fmaxf(m, __shfl_xor(m, 32));
           float one = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) one = fmaxf(one, __builtin_fmaf(x[n][e], p.c, (float)lv[e]));
+          for (int e = 0; e < 8; ++e) one = fmaxf(one, __builtin_fmaf(x[n][e], p.c, about_log2(vs[e])));
           one = fmaxf(one, __shfl_xor(one, 16));
           one = fmaxf(one, __shfl_xor(one, 32));
           to[n] = moved_reference(ref[n], m, one);

@@ -5,7 +5,7 @@
 // step: two barriers, between which the waves unpack a quarter of the step's codes each
 // into LDS as the products' operands, and after which every wave reads all of them, once
 // for each of its two products (keys . queries^T, values^T . weights^T, 32x32x16). Queries,
-// scores, weights and sums stay in registers: 254 of the 256 that two blocks a CU have, which
+// scores, weights and sums stay in registers: 252 of the 256 that two blocks a CU have, which
 // the build checks (with 258 a prompt of 2048 took 96 us instead of 63; the same bound given
 // to the compiler changes its schedule, 75 us). The codes of the next step are on their way
 // meanwhile.
@@ -30,9 +30,9 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
   constexpr int CT = D / 32;   // channel tiles of the second
   constexpr int RUNS = D / 64;
   // two tiles of 32 tokens: keys [step][lane], values [step][channel tile][lane], 16
-  // bytes each, and the tiles' scales, the values' also as log2
+  // bytes each, and the tiles' scales
   __shared__ __align__(16) uint4 kl[2][KS][64], vl[2][2][CT][64];
-  __shared__ __align__(16) uint4 ksl[2][4], vsl[2][4], lvl[2][4];
+  __shared__ __align__(16) uint4 ksl[2][4], vsl[2][4];
   const int lane = threadIdx.x & 63, c = lane & 31, hl = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // heads next to each other: with eight of them, each XCD's L2 serves one
@@ -164,10 +164,7 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
         for (int t = 0; t < D / 16; ++t)
           vl[sub][g >> 1][t >> 1][32 * (g & 1) + 16 * (t & 1) + c16] =
               __builtin_bit_cast(uint4, kv_value_operand(w[t], magic, zeros));
-        if (lane < 4) {
-          vsl[sub][lane] = scales;
-          lvl[sub][lane] = __builtin_bit_cast(uint4, __builtin_elementwise_log2(as_f16x8(scales)));
-        }
+        if (lane < 4) vsl[sub][lane] = scales;
       }
     };
 
@@ -239,12 +236,10 @@ kv4_tile_kernel(KvCache a, AttnArgs p) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const f16x8 lv = as_f16x8(lvl[u][2 * q + hl]);  // (of a masked token anything: fmaxf drops a NaN)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                one = fmaxf(one, __builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], p.c, (float)lv[e]));
-            }
+                one = fmaxf(one, __builtin_fmaf(sc[u][4 * (q + 2 * (e >> 2)) + (e & 3)], p.c, about_log2(vs[u][q][e])));
         }
         one = fmaxf(one, __shfl_xor(one, 32));
         float to = moved_reference(ref, fmaxf(mx, __shfl_xor(mx, 32)), one);
