@@ -140,6 +140,18 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace_bytes(workspace, like):
+    """Bytes of a workspace that the GPU will write: a whole piece of the inputs' device."""
+    import torch
+    if workspace is None:
+        return 0
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != like.get_device():
+        raise TypeError("workspace must be a tensor on the inputs' device")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def quantize_workspace_bytes(N, K, sparse_k):
     return int(load().wq_quantize_workspace_bytes(N, K, sparse_k))
 
@@ -169,8 +181,8 @@ def quantize_rtn(W, sparse_k: int = 0, group: int = GROUP, workspace=None, bits:
     if workspace is None and nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     rc = lib.wq_quantize_rtn_bits(_p(W), N, K, group, bits, sparse_k, _p(codes), _p(scales), _p(zeros),
-                                  _p(row_ptr), _p(col), _p(val), _p(workspace),
-                                  nbytes if workspace is not None else 0, _stream(W))
+                                  _p(row_ptr), _p(col), _p(val), _p(workspace), _workspace_bytes(workspace, W),
+                                  _stream(W))
     _check("wq_quantize_rtn_bits", rc)
     return dict(codes=codes, scales=scales[:, :G], zeros=zeros[:, :G], row_ptr=row_ptr,
                 col=col[:sparse_k], val=val[:sparse_k])
@@ -254,7 +266,7 @@ def linear_sparse(x, packed, scales, zeros, row_ptr=None, col=None, val=None, ou
         nbytes = int(lib.wq_linear_workspace_bytes(M, N, K))
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    wbytes = _workspace_bytes(workspace, x)
     rc = lib.wq_linear_sparse_bits(_p(x), M, K, _p(packed), bits, _p(scales), _p(zeros), N, group,
                                    _p(row_ptr), _p(col) if nnz else None, _p(val) if nnz else None, nnz,
                                    _p(out), y_dtype, KERNELS[kernel], _p(workspace), wbytes, _stream(x))
@@ -352,7 +364,7 @@ def linear_lowrank(x, packed, scales, zeros, L1, L2, row_ptr=None, col=None, val
     if workspace is None:
         nbytes = int(lib.wq_linear_lowrank_workspace_bytes(max(M, 1), N, K, r))
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
-    wbytes = workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, x)
     rc = lib.wq_linear_lowrank(_p(x), M, K, _p(packed), _p(scales), _p(zeros), N, group,
                                _p(row_ptr) if nnz else None, _p(col) if nnz else None, _p(val) if nnz else None,
                                nnz, _p(L1), _p(L2), r, _p(out), y_dtype, KERNELS[kernel], _p(workspace), wbytes,
@@ -384,7 +396,7 @@ def quantize_rtn_act_order(W, perm, sparse_k: int = 0, group: int = GROUP, works
     nbytes = int(lib.wq_quantize_act_order_workspace_bytes(N, K, sparse_k))
     if workspace is None:
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    wbytes = workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, W)
     rc = lib.wq_quantize_rtn_act_order(_p(W), N, K, group, _p(perm), sparse_k, _p(codes), _p(scales), _p(zeros),
                                        _p(row_ptr), _p(col), _p(val), _p(workspace), wbytes, _stream(W))
     _check("wq_quantize_rtn_act_order", rc)
@@ -434,7 +446,7 @@ def linear_act_order(x, perm, packed, scales, zeros, row_ptr=None, col=None, val
     if workspace is None:
         nbytes = int(lib.wq_linear_act_order_workspace_bytes(max(M, 1), N, K))
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
-    wbytes = workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, x)
     rc = lib.wq_linear_act_order(_p(x), M, K, _p(perm), _p(packed), _p(scales), _p(zeros), N, group,
                                  _p(row_ptr) if row_ptr is not None else None, _p(col) if nnz else None,
                                  _p(val) if nnz else None, nnz, _p(out), y_dtype, KERNELS[kernel], _p(workspace),
@@ -489,7 +501,7 @@ def linear_w4a8(x, outliers, packed, scales, zeros, out_dtype=None, out=None, gr
     if workspace is None:
         nbytes = int(lib.wq_linear_w4a8_workspace_bytes(max(M, 1), N, K))
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
-    wbytes = workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, x)
     n_out = outliers.numel()
     rc = lib.wq_linear_w4a8(_p(x), M, K, _p(outliers) if n_out else None, n_out, _p(packed), _p(scales), _p(zeros),
                             N, group, _p(out), 1 if out_dtype == torch.float32 else 0, _p(workspace), wbytes,
@@ -529,7 +541,7 @@ def linear_w4a8_quantized(xq, sx, xo, outliers, packed, scales, zeros, out_dtype
     if workspace is None:
         workspace = torch.empty(int(lib.wq_linear_w4a8_quantized_workspace_bytes(N)), dtype=torch.uint8,
                                 device=xq.device)
-    wbytes = workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, xq)
     n_out = outliers.numel()
     rc = lib.wq_linear_w4a8_quantized(_p(xq), _p(sx), _p(xo), M, K, _p(outliers) if n_out else None, n_out,
                                       _p(packed), _p(scales), _p(zeros), N, group, _p(out),
@@ -746,7 +758,7 @@ def kv4_attention(q, cache, page_table, seq_start, ctx_len, max_q=None, max_ctx=
         nbytes = int(lib.wq_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q, max_ctx))
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    wbytes = _workspace_bytes(workspace, q)
     rc = lib.wq_kv4_attention(_p(q), qs, T, q_heads, kv_heads, head_dim, _p(seq_start), _p(ctx_len), B, max_q, max_ctx,
                               _p(page_table), max_pages, _p(cache), num_pages, page_tokens,
                               head_dim ** -0.5 if scale is None else scale, window, _p(out), _p(lse), _p(workspace),
