@@ -688,7 +688,9 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 int64_t decode_slots(const Plan& pl, int64_t hkv, int64_t shares) {
   return shares > 1 ? hkv * shares * 2 * pl.decode_rows : 0;
 }
-int64_t tile_slots(const Plan& pl, int64_t hkv) { return hkv * pl.most_tshares * 2 * kTileRows; }
+int64_t tile_slots(const Plan& pl, int64_t hkv, int64_t shares) {
+  return shares > 1 ? hkv * shares * 2 * kTileRows : 0;
+}
 size_t part_bytes(int64_t slots, int64_t D) { return round256((size_t)slots * (D * 4 + 8)); }
 
 // waves that join a row of `parts` partials, about: eight each
@@ -735,7 +737,7 @@ size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t hq, int64_t h
                                      int64_t max_ctx) {
   const Plan pl = make_plan(T, B, hq, hkv, head_dim, max_q, max_ctx, 0);
   // whichever kernels run: a shorter batch may take others than the longest
-  return part_bytes(decode_slots(pl, hkv, pl.most_shares), head_dim) + part_bytes(tile_slots(pl, hkv), head_dim);
+  return part_bytes(decode_slots(pl, hkv, pl.most_shares), head_dim) + part_bytes(tile_slots(pl, hkv, pl.most_tshares), head_dim);
 }
 
 int kv4_attention_plan(int64_t T, int64_t B, int64_t hq, int64_t hkv, int64_t head_dim, int64_t max_q, int64_t max_ctx,
@@ -760,7 +762,7 @@ hipError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, 
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   const int64_t slots = decode_slots(pl, c.kv_heads, pl.shares);
-  const int64_t tslots = pl.tile && pl.tshares > 1 ? tile_slots(pl, c.kv_heads) : 0;
+  const int64_t tslots = pl.tile ? tile_slots(pl, c.kv_heads, pl.tshares) : 0;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_s = reinterpret_cast<float2*>(ws + (size_t)slots * head_dim * 4);
   ws += part_bytes(slots, head_dim);

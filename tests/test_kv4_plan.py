@@ -56,3 +56,12 @@ def test_the_faster_kernel_is_taken(lib, T, B, hq, hkv, d, max_q, max_ctx, windo
     than a tenth."""
     p = wq.kv4_attention_plan(T, B, hq, hkv, d, max_q, max_ctx, window)
     assert p["many_rows"] == many
+
+
+def test_no_workspace_where_nothing_is_split(lib):  # noqa: F811
+    f = lib.wq_kv4_attention_workspace_bytes
+    # more key/value heads than half the blocks that run at once: one share a head
+    for hkv in (257, 512, 600):
+        for T, q in ((1, 1), (200, 200), (2000, 2000)):
+            assert f(T, 1, hkv, hkv, 128, q, 4096) == 0
+    assert f(2000, 1, 256, 256, 128, 2000, 4096) > 0
