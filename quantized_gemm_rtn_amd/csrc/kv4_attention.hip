@@ -92,7 +92,7 @@ __device__ __forceinline__ int64_t share_steps(const AttnArgs& p, int64_t total)
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kDepth = 2;  // tiles of a wave's ring: one in use, one on its way
+constexpr int kDepth = 2;  // tiles of a wave's ring: one in use, one on its way (stages 0 and 1)
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -247,10 +247,9 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
     const auto fetch_next = [&]() {
       if (fetched < end) fetch(stage_in);
       fetched += 4;
-      stage_in = stage_in + 1 == kDepth ? 0 : stage_in + 1;
+      stage_in ^= 1;
     };
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch_next();
+    fetch_next();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -261,18 +260,13 @@ kv4_decode_kernel(KvCache a, AttnArgs p) {
       }
     for (; tile < end; tile += 4) {
       fetch_next();
-      // this tile's loads are done when only the later tiles' are left
-      const int later = (end - 1 - tile) >> 2;
-      if (later >= kDepth - 1)
-        wait_vm<(kDepth - 1) * LOADS>();
-      else if (kDepth > 2 && later == 1)
+      // this tile's loads are done when only the next one's are left
+      if (tile + 4 < end)
         wait_vm<LOADS>();
-      else if (kDepth > 3 && later == 2)
-        wait_vm<2 * LOADS>();
       else
         wait_vm<0>();
       const uint32_t at = ring_at + stage * TILE;
-      stage = stage + 1 == kDepth ? 0 : stage + 1;
+      stage ^= 1;
       TileData<D> cur;
       lds_tile<D>(cur, at, lane);
 
