@@ -433,8 +433,8 @@ int wq_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo
  *              layout inside a page is the library's own.
  *  page_tokens tokens of a page: a positive multiple of 32 (WQ_ERR_UNSUPPORTED otherwise).
  *  page_table  [B, max_pages] int32: token t of sequence b is in page
- *              page_table[b][t / page_tokens]. Only entries of pages that hold a token in
- *              use are read. Sequences may share pages that are only read.
+ *              page_table[b][t / page_tokens]. Entries of pages that hold no token in use
+ *              may be anything. Sequences may share pages that are only read.
  *  seq_start   [B + 1] int32, not falling: sequence b's new tokens are the rows
  *              seq_start[b] .. seq_start[b + 1] - 1 of q, k, v and out.
  *  ctx_len     [B] int32: tokens of sequence b, the new ones last. With fewer tokens
@@ -443,11 +443,12 @@ int wq_dequantize_act_int8(const int8_t* xq, const float* sx, const uint16_t* xo
  *  head_dim    64 or 128 (WQ_ERR_UNSUPPORTED otherwise).
  *  max_new, max_q, max_ctx  the largest number of new tokens, and of tokens, of a
  *              sequence. They only shape the launch: every sequence is handled in full
- *              whatever they are, only slower when they are far off.
+ *              whatever they are, only slower when they are far off. (Another launch may
+ *              split a sequence's sums elsewhere, and so round their last bits otherwise.)
  * Lengths, starts and page numbers outside their arrays are clamped on the device (wrong
  * values, never an invalid access). B up to 2^20 and below 2^24 / heads, heads up to
- * 65535, T = rows of the token-wise arrays below 2^31 / heads, max_pages * page_tokens up to 2^30. T = 0 or
- * B = 0 returns WQ_OK without a launch.
+ * 65535, T = rows of the token-wise arrays below 2^31 / heads, max_pages * page_tokens up
+ * to 2^30. T = 0 or B = 0 returns WQ_OK without a launch.
  */
 
 /* Bytes of one head's page; 0 for sizes the cache does not take. */
@@ -466,7 +467,8 @@ int wq_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
                   int64_t page_tokens, void* stream);
 
 /* wq_kv4_read - the new tokens' keys and values as the cache holds them: k, v
- * [T, kv_heads, head_dim] fp16 out, contiguous, 16-byte aligned. */
+ * [T, kv_heads, head_dim] fp16 out, contiguous, 16-byte aligned. Rows that belong to no
+ * sequence are left unwritten. */
 int wq_kv4_read(const void* cache, int64_t num_pages, int64_t page_tokens, int64_t T, int64_t kv_heads,
                 int64_t head_dim, const int32_t* seq_start, const int32_t* ctx_len, int64_t B, int64_t max_new,
                 const int32_t* page_table, int64_t max_pages, uint16_t* k, uint16_t* v, void* stream);

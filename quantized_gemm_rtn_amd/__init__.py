@@ -700,7 +700,8 @@ def kv4_append(k, v, cache, page_table, seq_start, ctx_len, max_new=None):
 
 def kv4_read(cache, page_table, seq_start, ctx_len, tokens: int, head_dim: int, max_new=None):
     """The keys and values of each sequence's last tokens as ``cache`` holds them: float16
-    [tokens, kv_heads, head_dim] each, rows as in ``kv4_append``."""
+    [tokens, kv_heads, head_dim] each, rows as in ``kv4_append`` (those of no sequence are
+    not written)."""
     import torch
     lib = load()
     B, max_pages, num_pages, page_tokens, kv_heads = _kv4_view(cache, page_table, seq_start, ctx_len, head_dim)
@@ -734,7 +735,8 @@ def kv4_attention(q, cache, page_table, seq_start, ctx_len, max_q=None, max_ctx=
     are already appended; sequences and pages as in ``kv4_append``.
 
     A row sees the tokens up to its own, with ``window`` > 0 only the last ``window`` of
-    them; a row that sees none gives 0. ``scale`` is 1 / sqrt(head_dim) when omitted.
+    them; a row that sees none gives 0, one of no sequence is not written. ``scale`` (at most
+    1e16) is 1 / sqrt(head_dim) when omitted.
     ``max_q`` and ``max_ctx``, the most new tokens and the most tokens of a sequence,
     shape the launch only (the largest possible when omitted). Returns the float16
     output [T, q_heads, head_dim], with ``return_lse`` also float32 [T, q_heads], the log

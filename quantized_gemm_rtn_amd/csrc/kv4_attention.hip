@@ -34,15 +34,15 @@
 //    dealt out in equal shares, one a block, whose four waves take tiles of 32 tokens in
 //    turn and join through LDS at each row tile's end. Bound by the cache's bytes, which
 //    it reads once, through an LDS ring (loads that bypass registers: 127 us without, for
-//    the first of these): 64 sequences of 7100 tokens, 8 heads of 128 98 us (5.0 TB/s); 16
-//    of 2000, 32 heads 30-35 us (4-4.5 TB/s); one of 131 071, 8 heads 30 us (4.8 TB/s). A
+//    the first of these): 64 sequences of 7100 tokens, 8 heads of 128 99 us (5.0 TB/s); 16
+//    of 2000, 32 heads 30-35 us (4-4.5 TB/s); one of 131 071, 8 heads 31 us (4.6 TB/s). A
 //    wave's loop runs at 6.7 TB/s; beginning (lengths, page numbers, first tiles, each
 //    waiting for the one before) and joining take the rest, and a short call all of it:
 //    one sequence of 1000 tokens, 32 heads, 7.4 us.
 //  kv4_tile_kernel     many query rows: 128 a block; a tile of codes is turned into
 //    exact fp16 integers once, in LDS, for all of them (see there).
 //  kv4_combine_kernel  joins the parts of rows that more than one block worked on. Bound
-//    by latency: 4.6 us for 32 rows of 4 parts, 7.6 us for 4096 rows, most of two.
+//    by latency: 4.3 us for 32 rows of 4 parts, 7.7 us for 4096 rows, most of two.
 #include "kv4_attention.h"
 #include "wq_launch.h"
 

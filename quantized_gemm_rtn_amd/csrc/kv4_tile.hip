@@ -11,8 +11,8 @@
 // meanwhile.
 //
 // Measured: 1357 tokens in chunks of 700, 535 and 122 after up to 6000, 32 heads on 8: 126
-// GFLOP in 180 us (0.70 PFLOP/s); a prompt of 2048 62 us, of which its last rows' 32 steps,
-// alone on their CUs, are 56. Two blocks' steps take 5400 cycles a CU: matrix units are
+// GFLOP in 185-195 us (0.66 PFLOP/s); a prompt of 2048 67 us, nearly all of it its last rows'
+// 32 steps, alone on their CUs. Two blocks' steps take 5400 cycles a CU: matrix units are
 // busy for 2048 of them, vector units for 2800, and LDS for 2500 (32 rows a wave need 1 KB
 // of operands a matrix instruction, its full rate at the matrix units' own). None fills the
 // step because each block's phases follow on one another and only two blocks overlap. Tried

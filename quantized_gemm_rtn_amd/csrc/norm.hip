@@ -16,7 +16,7 @@
 // The INT8 values and the fp16 outliers and sums are the only roundings.
 //
 // Bound by memory for many rows, by latency for few. Measured: INT8, 2048 rows of 4096
-// channels with 8 outliers 16.0 us (58.7 MB, 3.7 TB/s; all rows at once, so that reading
+// channels with 8 outliers 16.2 us (58.7 MB, 3.6 TB/s; all rows at once, so that reading
 // and writing do not overlap much), one row 3.8 us; fp16, 33 rows of 8192 4.1 us. Loading
 // weights and outliers only when they are used: 21.8 and 7.0 us.
 #include "wq_device.h"
