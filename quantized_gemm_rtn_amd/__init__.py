@@ -142,14 +142,17 @@ def _need(t, dtype, name):
 
 def _workspace_bytes(workspace, like):
     """Bytes of a workspace that the GPU will write: a whole piece of the inputs' device."""
-    import torch
     if workspace is None:
         return 0
-    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != like.get_device():
+    try:
+        here = workspace.get_device() == like.get_device()
+    except AttributeError:
+        here = False
+    if not here:
         raise TypeError("workspace must be a tensor on the inputs' device")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
 def quantize_workspace_bytes(N, K, sparse_k):
