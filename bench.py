@@ -353,7 +353,7 @@ def measure_offline(wq, torch, index):
     return dict(config=index, N=N, K=K, sparse_k=sk, ms=ms, weights_per_s=N * K / (ms * 1e-3))
 
 
-DECODE_SOURCES = ("gemv_kernels.h", "gemv.hip", "wq_device.h")
+DECODE_SOURCES = ("gemv_kernels.h", "gemv_launch.h", "gemv.hip", "wq_device.h")
 
 
 def kernel_source_hash():

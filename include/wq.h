@@ -282,6 +282,87 @@ int wq_linear_lowrank(const uint16_t* x, int64_t M, int64_t K,
                       void* y, int32_t y_dtype, int32_t kernel,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace wq_linear_adapters needs: t [M, r rounded up to 32] fp16 and the
+ * split-K workspace of wq_linear_workspace_bytes(M, N, K). 0 for invalid sizes (r must be a
+ * multiple of 8 up to 256). */
+size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
+
+/*
+ * wq_linear_adapters - wq_linear_sparse_kernel plus a low-rank adapter that each row names
+ * (many requests' adapters in one batch beside the layer they share; the DeepCompressor
+ * README, SVDQuant section, runs adapters on the low-rank branch without requantizing):
+ *   y[m] = x[m] . dequant(packed)^T + W_sparse . x[m] + s[a] (x[m] . L1[a]^T) . L2[a]^T,
+ *   a = adapter[m].
+ *  L1  [n_adapters, r, K] fp16, L2 [n_adapters, N, r] fp16, both 16-byte aligned (an adapter
+ *      of a smaller rank is padded with zeros).
+ *  adapter_scale  [n_adapters] float32, the s above, or NULL: 1.
+ *  n_adapters     1 to 2^20.   r  a multiple of 8 up to 256 (WQ_ERR_UNSUPPORTED otherwise).
+ *  adapter        [M] int32, on the device like all arrays: rows outside [0, n_adapters) have
+ *                 none. Rows in any order; rows of one adapter next to each other are faster.
+ *  row_ptr / col / val / nnz as in wq_linear_sparse; row_ptr may be NULL when nnz == 0.
+ *  kernel as in wq_linear_sparse_kernel (a single row takes the MFMA decode kernel).
+ *  workspace: required for M >= 1, 256-byte aligned, wq_linear_adapters_workspace_bytes bytes;
+ *  contents on entry do not matter.
+ * t = s x . L1^T is accumulated in fp32 and rounded once to fp16 (it is an MFMA operand);
+ * each output tile adds t . L2^T to its fp32 accumulators before the one store of y. An
+ * adapter's infinities and NaN reach only the rows that name it. Deterministic.
+ */
+int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K,
+                       const uint32_t* packed, const uint16_t* scales, const uint16_t* zeros,
+                       int64_t N, int32_t group,
+                       const int32_t* row_ptr, const int32_t* col, const uint16_t* val, int64_t nnz,
+                       const uint16_t* L1, const uint16_t* L2, const float* adapter_scale, int64_t n_adapters,
+                       int64_t r, const int32_t* adapter, void* y, int32_t y_dtype, int32_t kernel,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * wq_moe_route - a mixture-of-experts router's choice: softmax over each row's logits, the
+ * top_k largest, largest first (equal ones: the lower expert first; NaN counts as the
+ * largest), and their weights.
+ *  logits   [M, E] fp16 or float32 (logits_dtype), 1 <= E <= 1024. An expert at -infinity is
+ *           masked: never chosen.
+ *  top_k    1 to 16, at most E.
+ *  renormalize  0: the weights are the softmax's values, over all E; else they are divided
+ *           by their sum.
+ *  experts  [M, top_k] int32 out, weights [M, top_k] float32 out; where fewer than top_k
+ *           experts are not masked, the last ones are -1 with weight 0.
+ * M * E below 2^31. E or top_k beyond their limits: WQ_ERR_UNSUPPORTED.
+ */
+int wq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int64_t E, int64_t top_k, int32_t renormalize,
+                 int32_t* experts, float* weights, void* stream);
+
+/* Bytes of device workspace wq_moe_experts needs (the inner activations, and the lists of
+ * each 64 rows). 0 for invalid sizes. */
+size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t top_k);
+
+/*
+ * wq_moe_experts - a mixture-of-experts layer of 4-bit matrices for a few tokens (each 64 rows
+ * read the matrices of the experts they name once; a long prompt is better served by a product
+ * for each expert):
+ *   y[m] = sum over j of weights[m, j] ((silu(x[m] . G_e^T) * (x[m] . U_e^T)) . D_e^T),
+ *   e = experts[m, j],  silu(a) = a / (1 + exp(-a)).
+ *  x        [M, H] fp16, 16-byte aligned.
+ *  experts  [M, top_k] int32, on the device; those outside [0, E) stand for nothing. A row
+ *           that names an expert twice has it with the sum of both weights.
+ *  weights  [M, top_k] float32.   top_k 1 to 16, E 1 to 1024 (WQ_ERR_UNSUPPORTED beyond).
+ *  gate_up  [E, 2 I, H/8] uint32 as written by wq_pack, each expert's I rows of G and then its
+ *           I rows of U; gate_up_scales, gate_up_zeros [E, 2 I, H/128] fp16.
+ *  down     [E, H, I/8] uint32; down_scales, down_zeros [E, H, I/128] fp16.
+ *  H, I     multiples of 128, 2 H I below 2^31; M up to 65535 * 64, M * H below 2^31.
+ *  group    128.   y  [M, H] out, fp16 or float32 (y_dtype), 4-byte aligned.
+ *  workspace: required for M >= 1, 256-byte aligned, wq_moe_experts_workspace_bytes bytes;
+ *  contents on entry do not matter.
+ * Sums are fp32; the inner activations silu(..) * (..) are rounded once to fp16, an MFMA
+ * operand (beyond 65504 they are infinite), y once. Two launches. Deterministic: a fixed
+ * order for the same experts (other rows in the batch may split a row's sums elsewhere, and so
+ * round its last bits otherwise; their values never reach it).
+ */
+int wq_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int32_t* experts, const float* weights,
+                   int64_t top_k, int64_t E, const uint32_t* gate_up, const uint16_t* gate_up_scales,
+                   const uint16_t* gate_up_zeros, int64_t I, const uint32_t* down, const uint16_t* down_scales,
+                   const uint16_t* down_zeros, int32_t group, void* y, int32_t y_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
 /*
  * Act-order layers (the GPTQ-R rows, GPTQ with reordering, of the DeepCompressor
  * README perplexity table): the input channels are quantized in a permuted order,

@@ -12,6 +12,10 @@ Entry points (the same names as the C ABI, without the ``wq_`` prefix):
 * ``linear_sparse(x, packed, scales, zeros, row_ptr, col, val)``
 * ``linear_lowrank(x, packed, scales, zeros, L1, L2, row_ptr, col, val)``
   the same plus a rank-r fp16 branch (x . L1^T) . L2^T
+* ``linear_adapters(x, packed, scales, zeros, L1, L2, adapter, ...)``
+  the product with a low-rank adapter that each row names
+* ``moe_route(logits, top_k)``, ``moe_experts(x, experts, weights, ...)``
+  a router's choice of experts, and a mixture-of-experts layer of 4-bit matrices
 * ``quantize_rtn_act_order(W, perm)``, ``linear_act_order(x, perm, ...)``
   act-order layers, kept in the permuted channel order
 * ``quantize_act_int8(x, outliers)``, ``linear_w4a8(x, outliers, ...)``
@@ -57,6 +61,13 @@ SIGNATURES = {
     "wq_linear_lowrank_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "wq_linear_lowrank": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64,
                                          _vp, _vp, _i64, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "wq_linear_adapters_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "wq_linear_adapters": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _vp, _vp,
+                                          _vp, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "wq_moe_route": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "wq_moe_experts_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "wq_moe_experts": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32,
+                                      _vp, _i32, _vp, _sz, _vp]),
     "wq_quantize_act_order_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "wq_quantize_rtn_act_order": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
                                                  _vp, _sz, _vp]),
@@ -373,6 +384,159 @@ def linear_lowrank(x, packed, scales, zeros, L1, L2, row_ptr=None, col=None, val
                                nnz, _p(L1), _p(L2), r, _p(out), y_dtype, KERNELS[kernel], _p(workspace), wbytes,
                                _stream(x))
     _check("wq_linear_lowrank", rc)
+    return out
+
+
+def linear_adapters_workspace_bytes(M, N, K, r):
+    return int(load().wq_linear_adapters_workspace_bytes(M, N, K, r))
+
+
+def _same_device(x, **others):
+    for name, t in others.items():
+        if t is not None and t.get_device() != x.get_device():
+            raise ValueError(f"{name} must be on the device of the activations")
+
+
+def linear_adapters(x, packed, scales, zeros, L1, L2, adapter, adapter_scale=None, row_ptr=None, col=None, val=None,
+                    out_dtype=None, kernel: str = "auto", out=None, group: int = GROUP, workspace=None):
+    """y = x . dequant(packed, scales, zeros)^T (+ W_sparse x when CSR is given)
+    + adapter_scale[a] (x . L1[a]^T) . L2[a]^T with the adapter a = ``adapter[m]`` of each row
+    (int32 [M], on the GPU; outside [0, n): none), L1 [n, r, K] and L2 [n, N, r] fp16 (r a
+    multiple of 8), ``adapter_scale`` float32 [n] (1 when omitted).
+
+    ``workspace`` (uint8 device tensor of ``linear_adapters_workspace_bytes`` bytes) is
+    allocated per call when omitted."""
+    import torch
+    lib = load()
+    out_dtype = torch.float16 if out_dtype is None else out_dtype
+    _need(x, torch.float16, "x")
+    _need(packed, torch.int32, "packed")
+    _need(scales, torch.float16, "scales")
+    _need(zeros, torch.float16, "zeros")
+    _need(L1, torch.float16, "L1")
+    _need(L2, torch.float16, "L2")
+    _need(adapter, torch.int32, "adapter")
+    M, K = x.shape
+    N = packed.shape[0]
+    if packed.shape[1] * 8 != K or scales.shape != (N, K // group) or zeros.shape != scales.shape:
+        raise ValueError("inconsistent shapes")
+    if L1.dim() != 3 or L1.shape[2] != K or L2.shape != (L1.shape[0], N, L1.shape[1]):
+        raise ValueError("L1 must be [n, r, K] and L2 [n, N, r]")
+    if tuple(adapter.shape) != (M,):
+        raise ValueError("adapter must be [M]")
+    n, r = L1.shape[:2]
+    if adapter_scale is not None:
+        _need(adapter_scale, torch.float32, "adapter_scale")
+        if tuple(adapter_scale.shape) != (n,):
+            raise ValueError("adapter_scale must be [n]")
+    nnz = 0
+    if row_ptr is not None:
+        _need(row_ptr, torch.int32, "row_ptr")
+        if row_ptr.numel() != N + 1:
+            raise ValueError("row_ptr must have N+1 entries")
+        nnz = int(col.numel()) if col is not None else 0
+        if nnz:
+            _need(col, torch.int32, "col")
+            _need(val, torch.float16, "val")
+            if val.numel() != nnz:
+                raise ValueError("col and val must have as many entries")
+    if out_dtype not in (torch.float16, torch.float32):
+        raise TypeError("out_dtype must be float16 or float32")
+    if out is None:
+        out = x.new_empty((M, N), dtype=out_dtype)
+    else:
+        _need(out, out_dtype, "out")
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be [M, N]")
+    _same_device(x, packed=packed, scales=scales, zeros=zeros, L1=L1, L2=L2, adapter=adapter,
+                 adapter_scale=adapter_scale, out=out)
+    if nnz:
+        _same_device(x, row_ptr=row_ptr, col=col, val=val)
+    if workspace is None:
+        nbytes = int(lib.wq_linear_adapters_workspace_bytes(max(M, 1), N, K, r))
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+    wbytes = _workspace_bytes(workspace, x)
+    rc = lib.wq_linear_adapters(_p(x), M, K, _p(packed), _p(scales), _p(zeros), N, group, _p(row_ptr) if nnz else None,
+                                _p(col) if nnz else None, _p(val) if nnz else None, nnz, _p(L1), _p(L2),
+                                _p(adapter_scale), n, r, _p(adapter), _p(out), 1 if out_dtype == torch.float32 else 0,
+                                KERNELS[kernel], _p(workspace), wbytes, _stream(x))
+    _check("wq_linear_adapters", rc)
+    return out
+
+
+def moe_route(logits, top_k: int, renormalize: bool = True):
+    """Softmax over each row's logits (float16 or float32 [M, E]) and its ``top_k`` largest:
+    returns ``(experts, weights)``, int32 and float32 [M, top_k], largest first, equal ones by
+    their index. Experts at -infinity are never chosen: -1 with weight 0 where too few are left.
+    The weights are the softmax's values, with ``renormalize`` divided by their sum."""
+    import torch
+    lib = load()
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float16, torch.float32):
+        raise TypeError("logits must be a float16 or float32 tensor")
+    _need(logits, logits.dtype, "logits")
+    M, E = logits.shape
+    experts = logits.new_empty((M, top_k), dtype=torch.int32)
+    weights = logits.new_empty((M, top_k), dtype=torch.float32)
+    _check("wq_moe_route", lib.wq_moe_route(_p(logits), 1 if logits.dtype == torch.float32 else 0, M, E, top_k,
+                                            1 if renormalize else 0, _p(experts), _p(weights), _stream(logits)))
+    return experts, weights
+
+
+def moe_experts_workspace_bytes(M, H, I, top_k):
+    return int(load().wq_moe_experts_workspace_bytes(M, H, I, top_k))
+
+
+def moe_experts(x, experts, weights, gate_up, gate_up_scales, gate_up_zeros, down, down_scales, down_zeros,
+                out_dtype=None, out=None, workspace=None):
+    """A mixture-of-experts layer for a few tokens: y = the sum over a row's experts e of
+    its weight times (silu(x . G_e^T) * (x . U_e^T)) . D_e^T, all matrices in 4 bits.
+
+    ``x`` float16 [M, H]; ``experts`` int32 and ``weights`` float32 [M, top_k], as from
+    ``moe_route`` (experts outside [0, E) stand for nothing); ``gate_up`` int32
+    [E, 2 I, H / 8] (each expert's rows of G, then those of U) with scales and zero-points
+    [E, 2 I, H / 128]; ``down`` int32 [E, H, I / 8] with [E, H, I / 128]. ``workspace`` (uint8
+    device tensor of ``moe_experts_workspace_bytes`` bytes) is allocated per call when
+    omitted."""
+    import torch
+    lib = load()
+    out_dtype = torch.float16 if out_dtype is None else out_dtype
+    _need(x, torch.float16, "x")
+    _need(experts, torch.int32, "experts")
+    _need(weights, torch.float32, "weights")
+    for t, name in ((gate_up, "gate_up"), (down, "down")):
+        _need(t, torch.int32, name)
+    for t, name in ((gate_up_scales, "gate_up_scales"), (gate_up_zeros, "gate_up_zeros"),
+                    (down_scales, "down_scales"), (down_zeros, "down_zeros")):
+        _need(t, torch.float16, name)
+    M, H = x.shape
+    if experts.dim() != 2 or experts.shape[0] != M or weights.shape != experts.shape:
+        raise ValueError("experts and weights must be [M, top_k]")
+    if gate_up.dim() != 3 or down.dim() != 3:
+        raise ValueError("gate_up must be [E, 2 I, H / 8] and down [E, H, I / 8]")
+    E, I, top_k = gate_up.shape[0], down.shape[2] * 8, experts.shape[1]
+    if gate_up.shape != (E, 2 * I, H // 8) or down.shape != (E, H, I // 8) or H % 8:
+        raise ValueError("gate_up must be [E, 2 I, H / 8] and down [E, H, I / 8]")
+    if gate_up_scales.shape != (E, 2 * I, H // GROUP) or gate_up_zeros.shape != gate_up_scales.shape or \
+            down_scales.shape != (E, H, I // GROUP) or down_zeros.shape != down_scales.shape:
+        raise ValueError("scales and zeros must be [E, 2 I, H / 128] and [E, H, I / 128]")
+    if out_dtype not in (torch.float16, torch.float32):
+        raise TypeError("out_dtype must be float16 or float32")
+    if out is None:
+        out = x.new_empty((M, H), dtype=out_dtype)
+    else:
+        _need(out, out_dtype, "out")
+        if tuple(out.shape) != (M, H):
+            raise ValueError("out must be [M, H]")
+    _same_device(x, experts=experts, weights=weights, gate_up=gate_up, gate_up_scales=gate_up_scales,
+                 gate_up_zeros=gate_up_zeros, down=down, down_scales=down_scales, down_zeros=down_zeros, out=out)
+    if workspace is None:
+        nbytes = int(lib.wq_moe_experts_workspace_bytes(max(M, 1), H, I, top_k))
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+    wbytes = _workspace_bytes(workspace, x)
+    rc = lib.wq_moe_experts(_p(x), M, H, _p(experts), _p(weights), top_k, E, _p(gate_up), _p(gate_up_scales),
+                            _p(gate_up_zeros), I, _p(down), _p(down_scales), _p(down_zeros), GROUP, _p(out),
+                            1 if out_dtype == torch.float32 else 0, _p(workspace), wbytes, _stream(x))
+    _check("wq_moe_experts", rc)
     return out
 
 

@@ -25,9 +25,9 @@ PROBE_LIB = os.path.join(HERE, "libwq_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
 
-SOURCES = ["wq_api.hip", "split.hip", "quant.hip", "gemv.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip",
+SOURCES = ["wq_api.hip", "split.hip", "quant.hip", "gemv.hip", "gemv_adapters.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip",
            "lowrank.hip", "actorder.hip", "w4a8.hip", "norm.hip", "kv4_cache.hip", "kv4_attention.hip",
-           "kv4_tile.hip"]
+           "kv4_tile.hip", "adapters.hip", "moe.hip"]
 
 COMMON = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -48,8 +48,8 @@ PER_FILE = {"quant.hip": ["-ffp-contract=off"], "split.hip": ["-ffp-contract=off
             "w4a8.hip": ["-ffp-contract=off", "-mllvm", "-amdgpu-mfma-vgpr-form"]}
 # The product kernels must keep everything in registers and LDS: the compiler
 # reports each kernel's per-lane scratch, and any use of it fails the build.
-NO_SCRATCH = {"gemv.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip", "lowrank.hip", "w4a8.hip", "norm.hip",
-              "kv4_cache.hip", "kv4_attention.hip", "kv4_tile.hip"}
+NO_SCRATCH = {"gemv.hip", "gemv_adapters.hip", "gemv_fmt.hip", "gemv_dot.hip", "gemm.hip", "lowrank.hip", "w4a8.hip", "norm.hip",
+              "kv4_cache.hip", "kv4_attention.hip", "kv4_tile.hip", "adapters.hip", "moe.hip"}
 # Kernels whose plan counts on so many waves a SIMD (two blocks a CU): a register too many
 # would halve them without another sign.
 LEAST_WAVES = {"kv4_tile.hip": {"kv4_tile_kernel": 2}}

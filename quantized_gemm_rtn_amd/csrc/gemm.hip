@@ -70,6 +70,8 @@ struct GemmArgs {
   const f16* lr_t;
   const f16* lr_up;
   int lr_r;
+  const int32_t* lr_row;  // each row's own branch, of lr_n (null: one for all)
+  int lr_n;
   // x^T [K][xt_mp] for a sparse term added in the slice sum (gemm_big_kernel<..., true>)
   f16* xt;
   int xt_mp;
@@ -96,6 +98,44 @@ __device__ __forceinline__ void lowrank_add32(f32x16 (&acc)[MT][NT], const f16* 
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j] = mfma_32x32x16(av[i], bv[j], acc[i][j]);
+  }
+}
+
+// The same where each row names its own branch: subtile by subtile, for each adapter that its 32 rows name one product
+// of all of them, which its own rows keep (an adapter's infinities stay its own).
+template <int MT, int NT>
+__device__ __forceinline__ void adapters_add32(f32x16 (&acc)[MT][NT], const GemmArgs& a, int mbase, int nbase,
+                                               int lane) {
+  const int h = lane >> 5, c32 = lane & 31, r = a.lr_r, tr = (r + 31) & ~31;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = mbase + 32 * i + c32;
+    const int id = a.lr_row[min(m, a.M - 1)];
+    uint32_t left = (uint32_t)__ballot(m < a.M && (uint32_t)id < (uint32_t)a.lr_n);
+    const f16* ta = a.lr_t + (size_t)min(m, a.M - 1) * tr + 8 * h;
+#pragma unroll 1
+    while (left != 0) {
+      const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+      const uint32_t members = (uint32_t)__ballot(id == ad) & left;
+      left &= ~members;
+      const uint32_t mine = members >> (4 * h);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f16* ub = a.lr_up + ((size_t)ad * a.N + min(nbase + 32 * j + c32, a.N - 1)) * r;
+        f32x16 own = {};
+#pragma unroll 1
+        for (int s = 0; s < r; s += 16) {
+          const f16x8 av = as_f16x8(*reinterpret_cast<const uint4*>(ta + s));
+          uint4 b = *reinterpret_cast<const uint4*>(ub + min(s + 8 * h, r - 8));
+          if (s + 8 * h >= r) b = uint4{0, 0, 0, 0};
+          own = mfma_32x32x16(av, as_f16x8(b), own);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] += (mine >> (8 * (e >> 2) + (e & 3))) & 1u ? own[e] : 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -153,7 +193,7 @@ __device__ __forceinline__ void store_output(const f32x16 (&acc)[MT][NT], const 
 // BITS = 3: 3-bit codes, 32 per three words (a lane reads one 12-byte run per K
 // step instead of four words); G64: one (s, z) per 64 input channels, which is one
 // per K step.
-template <int BM, int BN, int WGM, int WGN, bool SPARSE, int BITS = 4, bool G64 = false>
+template <int BM, int BN, int WGM, int WGN, bool SPARSE, int BITS = 4, bool G64 = false, bool AD = false>
 __global__ void __launch_bounds__(64 * WGM * WGN, 2)
 gemm_kernel(GemmArgs a) {
   constexpr int T = 64 * WGM * WGN;
@@ -370,7 +410,11 @@ gemm_kernel(GemmArgs a) {
     __syncthreads();
   }
 
-  if (a.lr_r > 0 && slice == 0) lowrank_add32<MT, NT>(acc, a.lr_t, a.lr_up, a.lr_r, M, N, m0 + wm * WTM, n0 + wn * WTN, lane);
+  if constexpr (AD) {
+    if (slice == 0) adapters_add32<MT, NT>(acc, a, m0 + wm * WTM, n0 + wn * WTN, lane);
+  } else if (a.lr_r > 0 && slice == 0) {
+    lowrank_add32<MT, NT>(acc, a.lr_t, a.lr_up, a.lr_r, M, N, m0 + wm * WTM, n0 + wn * WTN, lane);
+  }
   // store: the final y, or this slice's fp32 partial tile
   store_output<MT, NT>(acc, a, slice, m0 + wm * WTM, n0 + wn * WTN, lane);
 }
@@ -404,7 +448,7 @@ constexpr int kBigSzBytes = 2 * 2 * 256 * 4;  // (s, z) table: 2 buffers x 2 gro
 //    each super-step: 128 / tiles_n (rounded up) input channels of the group for the
 //    block's rows, so that the tiles_n blocks of a row tile and slice cover every
 //    channel once. The slice sum then gathers the sparse term's activations from it.
-template <int BM, int BN, int WGM, int WGN, int MINB, int WS, bool XT>
+template <int BM, int BN, int WGM, int WGN, int MINB, int WS, bool XT, bool AD = false>
 __global__ void __launch_bounds__(64 * WGM * WGN, MINB)
 gemm_big_kernel(GemmArgs a) {
   constexpr int T = 64 * WGM * WGN;
@@ -694,7 +738,11 @@ gemm_big_kernel(GemmArgs a) {
     }
   }
 
-  if (a.lr_r > 0 && slice == 0) lowrank_add32<MT, NT>(acc, a.lr_t, a.lr_up, a.lr_r, M, N, m0 + wm * WTM, n0 + wn * WTN, lane);
+  if constexpr (AD) {
+    if (slice == 0) adapters_add32<MT, NT>(acc, a, m0 + wm * WTM, n0 + wn * WTN, lane);
+  } else if (a.lr_r > 0 && slice == 0) {
+    lowrank_add32<MT, NT>(acc, a.lr_t, a.lr_up, a.lr_r, M, N, m0 + wm * WTM, n0 + wn * WTN, lane);
+  }
   // store: the final y, or this slice's fp32 partial tile
   store_output<MT, NT>(acc, a, slice, m0 + wm * WTM, n0 + wn * WTN, lane);
 }
@@ -991,6 +1039,9 @@ static hipError_t launch_big(GemmArgs a, hipStream_t stream) {
   constexpr size_t lds = 2 * (size_t)BM * kBigSS * sizeof(f16) + kBigSzBytes;
   auto kern = a.xt != nullptr ? gemm_big_kernel<BM, BN, WGM, WGN, MINB, WS, true>
                               : gemm_big_kernel<BM, BN, WGM, WGN, MINB, WS, false>;
+  if (a.lr_row != nullptr)
+    kern = a.xt != nullptr ? gemm_big_kernel<BM, BN, WGM, WGN, MINB, WS, true, true>
+                           : gemm_big_kernel<BM, BN, WGM, WGN, MINB, WS, false, true>;
   {
     const hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(kern), lds);
     if (e != hipSuccess) return e;
@@ -1006,6 +1057,9 @@ template <int BM, int BN, int WGM, int WGN, bool SPARSE, int BITS = 4, bool G64 
 static hipError_t launch_tile(GemmArgs a, hipStream_t stream) {
   constexpr size_t lds = 2 * (size_t)BM * kLdsStride * sizeof(f16);
   auto kern = gemm_kernel<BM, BN, WGM, WGN, SPARSE, BITS, G64>;
+  if constexpr (BITS == 4 && !G64) {
+    if (a.lr_row != nullptr) kern = gemm_kernel<BM, BN, WGM, WGN, SPARSE, BITS, G64, true>;
+  }
   if (lds > 65536) {
     const hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(kern), lds);
     if (e != hipSuccess) return e;
@@ -1080,9 +1134,11 @@ hipError_t launch_gemm(const uint16_t* x, int64_t M, int64_t K, const uint32_t* 
     a.y_f32 = p.sparse_in_reduce ? 1 : y_f32;  // one fp32 slice when not split
     a.ksplit = p.ksplit;
     a.k_per_slice = p.k_per_slice;
-    a.lr_t = lr.r > 0 ? reinterpret_cast<const f16*>(lr.t) + m * lr.r : nullptr;
+    a.lr_t = lr.r > 0 ? reinterpret_cast<const f16*>(lr.t) + m * lr.t_stride() : nullptr;
     a.lr_up = reinterpret_cast<const f16*>(lr.up);
     a.lr_r = (int)lr.r;
+    a.lr_row = lr.row ? lr.row + m : nullptr;
+    a.lr_n = (int)lr.n;
     a.xt = xt_in_gemm ? xt : nullptr;  // written by gemm_big_kernel<..., true>
     a.xt_mp = (int)Mp;
     hipError_t e;

@@ -45,6 +45,7 @@
 // staged values are loaded before the weight prefetch is issued and stored after.
 #include <type_traits>
 
+#include "adapters.h"
 #include "wq_device.h"
 #include "wq_launch.h"
 
@@ -374,13 +375,13 @@ __device__ __forceinline__ void lowrank_add16(f32x4 (&acc)[NT], const LrFirst<NT
 // half of it, so each lane dequantizes (q - z) s into the operand with its own (s, z)
 // (the 128-channel correction per group below cannot split the two halves): the
 // activations are staged unscaled and without the sum tables, and (s, z) in LDS.
-template <int KW, int D, int XC, int SZV, int MR, bool SP, int BITS = 4, bool G64 = false>
+template <int KW, int D, int XC, int SZV, int MR, bool SP, int BITS = 4, bool G64 = false, bool AD = false>
 __global__ void __launch_bounds__(64 * KW)
 gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restrict__ packed,
                 const f16* __restrict__ scales, const f16* __restrict__ zeros, int N,
                 const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ col,
                 const f16* __restrict__ val, void* __restrict__ y, int y_f32, const f16* __restrict__ lr_t,
-                const f16* __restrict__ lr_up, int lr_r) {
+                const f16* __restrict__ lr_up, int lr_r, const int32_t* __restrict__ lr_row, int lr_n) {
   constexpr int T = 64 * KW;
   static_assert(T <= kGemvMaxThreads, "MFMA results of larger blocks were clobbered (see hold_accumulator)");
   extern __shared__ __align__(16) char smem[];
@@ -497,7 +498,7 @@ gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restr
   SparseHead<kSparseBatch, KW> sph;
   if constexpr (SP) sph.load(col, val, sp_e0, sp_e1);
   LrFirst<1> lr_first;
-  if (lr_r > 0 && wave == 0) lr_first.load(lr_t, lr_up, lr_r, M, N, m0, n0, lane);
+  if (!AD && lr_r > 0 && wave == 0) lr_first.load(lr_t, lr_up, lr_r, M, N, m0, n0, lane);
   __syncthreads();
 
   // ---- main loop over this wave's groups
@@ -620,7 +621,11 @@ gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restr
     }
   }
   // low-rank branch, once per output tile (wave 0, before the waves' sum)
-  if (lr_r > 0 && wave == 0) {
+  if constexpr (AD) {
+    f32x4 a1[1] = {acc};
+    adapters_add16<KW, 1>(a1, lr_t, lr_up, lr_r, lr_row, lr_n, M, N, m0, n0, lane, wave);
+    acc = a1[0];
+  } else if (lr_r > 0 && wave == 0) {
     f32x4 a1[1] = {acc};
     lowrank_add16<1>(a1, lr_first, lr_t, lr_up, lr_r, M, N, m0, n0, lane);
     acc = a1[0];
@@ -639,13 +644,13 @@ gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restr
 // SZV == kSzInRegs (128-channel groups, windows starting at multiples of D): each
 // lane loads the (s, z) of its rows for a window of D groups as two vectors,
 // issued with the window's weights, and the block stages nothing.
-template <int KW, int D, int XL, int NT, int SZV, bool SP, int BITS = 4, bool G64 = false>
+template <int KW, int D, int XL, int NT, int SZV, bool SP, int BITS = 4, bool G64 = false, bool AD = false>
 __global__ void __launch_bounds__(64 * KW)
 gemv_ring_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restrict__ packed,
                  const f16* __restrict__ scales, const f16* __restrict__ zeros, int N,
                  const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ col,
                  const f16* __restrict__ val, void* __restrict__ y, int y_f32, const f16* __restrict__ lr_t,
-                 const f16* __restrict__ lr_up, int lr_r) {
+                 const f16* __restrict__ lr_up, int lr_r, const int32_t* __restrict__ lr_row, int lr_n) {
   constexpr int T = 64 * KW;
   static_assert(T <= kGemvMaxThreads, "MFMA results of larger blocks were clobbered (see hold_accumulator)");
   constexpr bool kRegs = SZV == kSzInRegs;
@@ -732,7 +737,7 @@ gemv_ring_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __rest
     for (int j = 0; j < NT; ++j) sph[j].load(col, val, sp_e0[j], sp_e1[j]);
   }
   LrFirst<NT> lr_first;
-  if (lr_r > 0 && wave == 0) lr_first.load(lr_t, lr_up, lr_r, M, N, m0, n0, lane);
+  if (!AD && lr_r > 0 && wave == 0) lr_first.load(lr_t, lr_up, lr_r, M, N, m0, n0, lane);
 
   const f16x2* szr = sz + r * (Gs + 1);
   const uint32_t magic = magic_1024x2();
@@ -860,7 +865,10 @@ gemv_ring_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __rest
     }
   }
   // low-rank branch, once per output tile (wave 0, before the waves' sum)
-  if (lr_r > 0 && wave == 0) lowrank_add16<NT>(acc, lr_first, lr_t, lr_up, lr_r, M, N, m0, n0, lane);
+  if constexpr (AD)
+    adapters_add16<KW, NT>(acc, lr_t, lr_up, lr_r, lr_row, lr_n, M, N, m0, n0, lane, wave);
+  else if (lr_r > 0 && wave == 0)
+    lowrank_add16<NT>(acc, lr_first, lr_t, lr_up, lr_r, M, N, m0, n0, lane);
   reduce_store_tiles<KW, NT>(acc, wave, lane, m0, mrows, n0 + r, N, y, y_f32);
 }
 
@@ -884,8 +892,8 @@ inline hipError_t launch_rows(Kern kern, size_t lds, int cols, const uint16_t* x
                        (int)mc, (int)K, packed, reinterpret_cast<const f16*>(scales),
                        reinterpret_cast<const f16*>(zeros), (int)N, row_ptr, col, reinterpret_cast<const f16*>(val),
                        static_cast<char*>(y) + (size_t)(m * N) * ysz, y_f32,
-                       lr.r > 0 ? reinterpret_cast<const f16*>(lr.t) + m * lr.r : nullptr,
-                       reinterpret_cast<const f16*>(lr.up), (int)lr.r);
+                       lr.r > 0 ? reinterpret_cast<const f16*>(lr.t) + m * lr.t_stride() : nullptr,
+                       reinterpret_cast<const f16*>(lr.up), (int)lr.r, lr.row ? lr.row + m : nullptr, (int)lr.n);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

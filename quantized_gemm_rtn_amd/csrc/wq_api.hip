@@ -23,6 +23,10 @@ namespace {
 constexpr int64_t kGroup = 128;
 constexpr int64_t kMax32 = (int64_t)1 << 31;  // element counts must stay below 2^31
 constexpr int64_t kMaxRank = 256;             // rank of the low-rank branch: multiples of 32 up to this
+constexpr int64_t kMaxAdapters = (int64_t)1 << 20;
+constexpr int64_t kMaxExperts = 1024;         // of a mixture-of-experts layer,
+constexpr int64_t kMaxTopK = 16;              // and of a row
+constexpr int64_t kMaxMoeRows = 65535 * 64;   // 64 rows a block, the grid's limit
 constexpr int64_t kMaxOutliers = 16;          // fp16 outlier channels of the W4A8 product
 
 // t [M][r] fp16 of the low-rank branch, at the start of its workspace
@@ -344,6 +348,96 @@ int wq_linear_lowrank(const uint16_t* x, int64_t M, int64_t K, const uint32_t* p
     e = wq::launch_gemm(x, M, K, packed, scales, zeros, N, rp, col, val, nnz, y, y_f32, gws, gws_bytes, lr,
                         as_stream(stream));
   return hip_status(e);
+}
+
+// t's rows are r rounded up to 32 apart
+size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
+  if (M < 1 || N < 1 || K < kGroup || K % kGroup != 0) return 0;
+  if (N >= kMax32 / K || M >= kMax32 / K || M >= kMax32 / N) return 0;
+  if (r < 8 || r % 8 != 0 || r > kMaxRank) return 0;
+  return lowrank_t_bytes(M, (r + 31) / 32 * 32) + wq::gemm_workspace_bytes(M, N, K);
+}
+
+int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed, const uint16_t* scales,
+                       const uint16_t* zeros, int64_t N, int32_t group, const int32_t* row_ptr, const int32_t* col,
+                       const uint16_t* val, int64_t nnz, const uint16_t* L1, const uint16_t* L2,
+                       const float* adapter_scale, int64_t n_adapters, int64_t r, const int32_t* adapter, void* y,
+                       int32_t y_dtype, int32_t kernel, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_linear_args(x, M, K, packed, scales, zeros, N, group, row_ptr, col, val, nnz, y, y_dtype,
+                                   kernel);
+  if (rc != WQ_OK) return rc;
+  if (!L1 || !L2 || (M != 0 && !adapter)) return WQ_ERR_NULL;
+  if (n_adapters < 1 || n_adapters > kMaxAdapters || r < 1) return WQ_ERR_SHAPE;
+  if (r % 8 != 0 || r > kMaxRank) return WQ_ERR_UNSUPPORTED;
+  if (!aligned(L1, 16) || !aligned(L2, 16) || !aligned(adapter_scale, 4) || !aligned(adapter, 4)) return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  const size_t need = wq_linear_adapters_workspace_bytes(M, N, K, r);
+  if (workspace == nullptr || workspace_bytes < need) return WQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  // workspace: t | the GEMM's split-K workspace
+  char* ws = static_cast<char*>(workspace);
+  const size_t t_bytes = lowrank_t_bytes(M, (r + 31) / 32 * 32);
+  uint16_t* t = reinterpret_cast<uint16_t*>(ws);
+  if (kernel == WQ_KERNEL_AUTO) kernel = wq_auto_kernel(M, N, K);
+  const int y_f32 = y_dtype == WQ_F32;
+  const int32_t* rp = nnz > 0 ? row_ptr : nullptr;  // nnz == 0: no sparse term
+  hipError_t e = wq::launch_adapters_down(x, M, K, wq::Adapters{L1, adapter_scale, adapter, n_adapters}, r, t,
+                                          as_stream(stream));
+  if (e != hipSuccess) return hip_status(e);
+  const wq::LowRank lr{t, L2, r, adapter, n_adapters};
+  if (kernel == WQ_KERNEL_GEMV || kernel == WQ_KERNEL_GEMV_MFMA)
+    e = wq::launch_gemv(x, M, K, packed, scales, zeros, N, rp, col, val, y, y_f32, lr, as_stream(stream));
+  else
+    e = wq::launch_gemm(x, M, K, packed, scales, zeros, N, rp, col, val, nnz, y, y_f32, ws + t_bytes,
+                        workspace_bytes - t_bytes, lr, as_stream(stream));
+  return hip_status(e);
+}
+
+int wq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int64_t E, int64_t top_k, int32_t renormalize,
+                 int32_t* experts, float* weights, void* stream) {
+  if (M != 0 && (!logits || !experts || !weights)) return WQ_ERR_NULL;
+  if (logits_dtype != WQ_F16 && logits_dtype != WQ_F32) return WQ_ERR_UNSUPPORTED;
+  if (E > kMaxExperts || top_k > kMaxTopK) return WQ_ERR_UNSUPPORTED;
+  if (M < 0 || E < 1 || top_k < 1 || top_k > E || M >= kMax32 / E) return WQ_ERR_SHAPE;
+  if (!aligned(logits, logits_dtype == WQ_F32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4))
+    return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  return hip_status(wq::launch_moe_route(logits, logits_dtype == WQ_F32, M, E, top_k, renormalize != 0, experts,
+                                         weights, as_stream(stream)));
+}
+
+namespace {
+bool moe_sizes(int64_t M, int64_t H, int64_t I, int64_t top_k) {
+  return M >= 0 && M <= kMaxMoeRows && H >= kGroup && H % kGroup == 0 && I >= kGroup && I % kGroup == 0 &&
+         top_k >= 1 && H < kMax32 / I / 2 && M < kMax32 / H && M < kMax32 / top_k;
+}
+}  // namespace
+
+size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t top_k) {
+  if (!moe_sizes(M, H, I, top_k) || M < 1 || top_k > kMaxTopK) return 0;
+  return wq::moe_workspace_bytes(M, H, I, top_k);
+}
+
+int wq_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int32_t* experts, const float* weights,
+                   int64_t top_k, int64_t E, const uint32_t* gate_up, const uint16_t* gate_up_scales,
+                   const uint16_t* gate_up_zeros, int64_t I, const uint32_t* down, const uint16_t* down_scales,
+                   const uint16_t* down_zeros, int32_t group, void* y, int32_t y_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (!gate_up || !gate_up_scales || !gate_up_zeros || !down || !down_scales || !down_zeros) return WQ_ERR_NULL;
+  if (M != 0 && (!x || !experts || !weights || !y)) return WQ_ERR_NULL;
+  if (group != kGroup || (y_dtype != WQ_F16 && y_dtype != WQ_F32) || E > kMaxExperts || top_k > kMaxTopK)
+    return WQ_ERR_UNSUPPORTED;
+  if (E < 1 || !moe_sizes(M, H, I, top_k)) return WQ_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(gate_up_scales, 2) ||
+      !aligned(gate_up_zeros, 2) || !aligned(down_scales, 2) || !aligned(down_zeros, 2) || !aligned(experts, 4) ||
+      !aligned(weights, 4) || !aligned(y, 4))
+    return WQ_ERR_ALIGN;
+  if (M == 0) return WQ_OK;
+  if (!workspace || workspace_bytes < wq_moe_experts_workspace_bytes(M, H, I, top_k)) return WQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  return hip_status(wq::launch_moe_experts(x, M, H, experts, weights, top_k, E, gate_up, gate_up_scales, gate_up_zeros,
+                                           I, down, down_scales, down_zeros, y, y_dtype == WQ_F32, workspace,
+                                           as_stream(stream)));
 }
 
 int wq_linear_sparse(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed, const uint16_t* scales,

@@ -84,10 +84,15 @@ hipError_t launch_pack(const uint8_t* codes, int64_t N, int64_t K, uint32_t* pac
 
 // The up-projection of a low-rank branch, added to every output tile before its
 // store: t [M, r] fp16 (the down-projection x . L1^T) and L2 [N, r] fp16; r = 0: none.
+// With `row`, each row has a branch of its own: row[m] of the n that `up` [n, N, r] holds, or none
+// (outside [0, n)); r is then a multiple of 8, and t's rows lie r rounded up to 32 apart, zeros beyond r.
 struct LowRank {
   const uint16_t* t = nullptr;
   const uint16_t* up = nullptr;
   int64_t r = 0;
+  const int32_t* row = nullptr;
+  int64_t n = 0;
+  int64_t t_stride() const { return (r + 31) / 32 * 32; }
 };
 
 // The down-projection t = fp16(x . L1^T) of a low-rank branch (r a multiple of 32),
@@ -95,6 +100,27 @@ struct LowRank {
 size_t lowrank_partial_bytes(int64_t M, int64_t K, int64_t r);
 hipError_t launch_lowrank_down(const uint16_t* x, int64_t M, int64_t K, const uint16_t* L1, int64_t r,
                                float* part, uint16_t* t, hipStream_t stream);
+
+// The down-projections t[m] = fp16(scale[a] x[m] . L1_a^T) of the adapters a = row[m] that rows name, L1 [n, r, K],
+// scale [n] (null: 1), t [M, r rounded up to 32].
+struct Adapters {
+  const uint16_t* L1;
+  const float* scale;
+  const int32_t* row;
+  int64_t n;
+};
+hipError_t launch_adapters_down(const uint16_t* x, int64_t M, int64_t K, const Adapters& ad, int64_t r, uint16_t* t,
+                                hipStream_t stream);
+
+// Softmax of each row's logits ([M, E] fp16, or fp32) and its k largest.
+hipError_t launch_moe_route(const void* logits, int f32, int64_t M, int64_t E, int64_t k, int renormalize,
+                            int32_t* experts, float* weights, hipStream_t stream);
+// A mixture-of-experts layer for a few tokens: up [E, 2 I, H], down [E, H, I] in 4 bits.
+size_t moe_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t k);
+hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int32_t* experts, const float* weights,
+                              int64_t k, int64_t E, const uint32_t* up, const uint16_t* up_s, const uint16_t* up_z,
+                              int64_t I, const uint32_t* down, const uint16_t* down_s, const uint16_t* down_z, void* y,
+                              int y_f32, void* workspace, hipStream_t stream);
 
 // Weight format of a product: 4-bit codes (eight per word) or 3-bit codes (32 per
 // three words, the layout of wq_pack_bits), with one (s, z) per 128 or per 64 input
@@ -110,6 +136,11 @@ hipError_t launch_gemv(const uint16_t* x, int64_t M, int64_t K, const uint32_t* 
                        const uint16_t* scales, const uint16_t* zeros, int64_t N, const int32_t* row_ptr,
                        const int32_t* col, const uint16_t* val, void* y, int y_f32, const LowRank& lr,
                        hipStream_t stream, WFormat f = WFormat{}, bool mfma_only = false);
+// the same with the adapters that rows name (lr.row)
+hipError_t launch_gemv_adapters(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed,
+                                const uint16_t* scales, const uint16_t* zeros, int64_t N, const int32_t* row_ptr,
+                                const int32_t* col, const uint16_t* val, void* y, int y_f32, const LowRank& lr,
+                                hipStream_t stream);
 // the same for the formats other than 4-bit with 128-channel groups (no low-rank branch)
 hipError_t launch_gemv_fmt(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed,
                            const uint16_t* scales, const uint16_t* zeros, int64_t N, const int32_t* row_ptr,
