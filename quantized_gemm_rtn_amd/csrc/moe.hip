@@ -15,11 +15,22 @@
 
 namespace wq {
 
-constexpr int kMoeTokens = 64;      // rows of x that a block's lists hold; more come as further blocks
-constexpr int kMoeMaxPairs = 1024;  // of them, (row, expert) pairs: top_k <= 16
+constexpr int kMoeTokens = 192;     // rows of x that a block's lists hold; more come as further blocks
+constexpr int kMoeMaxPairs = 1024;  // of them, (row, expert) pairs
 constexpr int kMoeMaxExperts = 1024;
-constexpr int kUpWaves = 4, kUpDepth = 4;
-constexpr int kDownWaves = 16, kDownDepth = 4;
+constexpr int kMoeWaves = 8;        // of a block, one block a CU
+constexpr int kMoeUnit = 8;         // groups of 128 channels: what waves' shares are multiples of
+constexpr int kMoeRowHalves = 136;  // of a staged row: 128 and padding (16 rows of a fragment in distinct banks)
+
+// What some rows of x have to do, from their experts: the active experts in ascending order, each with its (row,
+// expert) pairs, row * k + slot, in order. A row that names an expert twice has it once, with the weights' sum.
+struct MoeLists {
+  int32_t active, pad[3];             // experts
+  uint16_t expert[kMoeMaxPairs];      // of the i-th active one,
+  uint16_t start[kMoeMaxPairs + 8];   // its first pair (start[active]: their number),
+  uint16_t tile[kMoeMaxPairs + 8];    // and its first tile of 16 pairs (tile[active]: theirs)
+  uint16_t pair[kMoeMaxPairs];
+};
 
 struct MoeArgs {
   const f16* x;            // [M][H]
@@ -31,28 +42,12 @@ struct MoeArgs {
   const uint32_t* down;    // [E][H][I / 8]
   const f16* down_s;
   const f16* down_z;
-  f16* h;                  // [M * k][I], each 128 channels in the order of moe_h_index
-  int32_t* lists;          // of each 64 rows: see MoeLists
+  f16* h;                  // [M * k][I], each eight channels in the order of perm_x8
+  MoeLists* lists;         // of each `tokens` rows
   void* y;
   int M, H, I, E, k, y_f32;
+  int tokens;
 };
-
-// What 64 rows of x have to do, from their experts: the active experts in ascending order, each
-// with its (row, expert) pairs, and those pairs, row * k + slot. A row that names an expert
-// twice has it once, with the weights' sum.
-struct MoeLists {
-  int32_t active;                      // experts
-  int32_t pad[15];
-  int32_t expert[kMoeMaxPairs];        // of the i-th active one,
-  int32_t start[kMoeMaxPairs + 16];    // its first pair (start[active]: their number)
-  int32_t pair[kMoeMaxPairs];
-};
-
-// Position of inner channel c among the 128 of its group: chunks of eight in the order that the
-// four lane groups of a product's step read them, each in the order of perm_x8.
-__device__ __forceinline__ int moe_h_index(int c) {
-  return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | perm_slot(c & 7);
-}
 
 __device__ __forceinline__ int sum_upto_64(int v, int lane) {
 #pragma unroll
@@ -63,72 +58,84 @@ __device__ __forceinline__ int sum_upto_64(int v, int lane) {
   return v;
 }
 
-// The lists of rows m0 .. m0 + rows - 1, by a block of 256 threads, in its LDS.
-__device__ __forceinline__ void moe_lists(MoeLists& l, int (&ids)[kMoeMaxPairs], int (&count)[kMoeMaxExperts],
-                                          int (&sums)[4], const MoeArgs& a, int m0, int rows) {
+// The lists of rows m0 .. m0 + rows - 1, by the block, in its LDS.
+struct MoeScratch {
+  int16_t ids[kMoeMaxPairs];
+  int32_t count[kMoeMaxExperts];
+  int32_t sums[kMoeWaves][2];
+};
+__device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeArgs& a, int m0, int rows) {
+  constexpr int T = 64 * kMoeWaves, PER = kMoeMaxPairs / T, EPER = kMoeMaxExperts / T;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, pairs = rows * a.k;
-  constexpr int PER = kMoeMaxPairs / 256, EPER = kMoeMaxExperts / 256;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int p = t + 256 * i;
-    int e = p < pairs ? a.experts[(int64_t)m0 * a.k + p] : -1;
-    ids[p] = e = (uint32_t)e < (uint32_t)a.E ? e : -1;
+    const int p = t + T * i;
+    const int e = p < pairs ? a.experts[(int64_t)m0 * a.k + p] : -1;
+    w.ids[p] = (int16_t)((uint32_t)e < (uint32_t)a.E ? e : -1);
   }
 #pragma unroll
-  for (int i = 0; i < EPER; ++i) count[EPER * t + i] = 0;
+  for (int i = 0; i < EPER; ++i) w.count[EPER * t + i] = 0;
   __syncthreads();
-  int place[PER];
+  int place[PER], made[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int p = t + 256 * i, e = ids[p];
+    const int p = t + T * i, e = w.ids[p];
     bool first = e >= 0;
     if (first)
-      for (int q = p / a.k * a.k; q < p; ++q) first = first && ids[q] != e;
-    place[i] = first ? atomicAdd(&count[e], 1) : -1;
+      for (int q = p / a.k * a.k; q < p; ++q) first = first && w.ids[q] != e;
+    place[i] = first ? atomicAdd(&w.count[e], 1) : -1;
   }
   __syncthreads();
-  int made[PER];  // pairs of the pair's expert
 #pragma unroll
-  for (int i = 0; i < PER; ++i) made[i] = place[i] >= 0 ? count[ids[t + 256 * i]] : 0;
-  // experts EPER t .. + EPER - 1: pairs and active ones before them, in one sum
-  int own[EPER], both = 0;
+  for (int i = 0; i < PER; ++i) made[i] = place[i] >= 0 ? w.count[w.ids[t + T * i]] : 0;  // pairs of the pair's expert
+  // experts EPER t .. + EPER - 1: active ones and pairs before them (in one sum), and tiles
+  int own[EPER], both = 0, tiles = 0;
 #pragma unroll
   for (int i = 0; i < EPER; ++i) {
-    own[i] = count[EPER * t + i];
+    own[i] = w.count[EPER * t + i];
     both += own[i] + (own[i] > 0 ? 1 << 16 : 0);
+    tiles += (own[i] + 15) >> 4;
   }
-  const int upto = sum_upto_64(both, lane);
-  if (lane == 63) sums[wave] = upto;
+  const int both_upto = sum_upto_64(both, lane), tiles_upto = sum_upto_64(tiles, lane);
+  if (lane == 63) {
+    w.sums[wave][0] = both_upto;
+    w.sums[wave][1] = tiles_upto;
+  }
   __syncthreads();
-  int before = upto - both, total = 0;
+  int before = both_upto - both, tile = tiles_upto - tiles, total = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    before += w < wave ? sums[w] : 0;
-    total += sums[w];
+  for (int v = 0; v < kMoeWaves; ++v) {
+    before += v < wave ? w.sums[v][0] : 0;
+    tile += v < wave ? w.sums[v][1] : 0;
+    total += w.sums[v][0];
+    all += w.sums[v][1];
   }
 #pragma unroll
   for (int i = 0; i < EPER; ++i)
     if (own[i] > 0) {
-      l.expert[before >> 16] = EPER * t + i;
-      l.start[before >> 16] = before & 0xFFFF;
-      count[EPER * t + i] = before & 0xFFFF;  // where its pairs begin
+      l.expert[before >> 16] = (uint16_t)(EPER * t + i);
+      l.start[before >> 16] = (uint16_t)before;
+      l.tile[before >> 16] = (uint16_t)tile;
+      w.count[EPER * t + i] = before & 0xFFFF;  // where its pairs begin
       before += own[i] + (1 << 16);
+      tile += (own[i] + 15) >> 4;
     }
   if (t == 0) {
     l.active = total >> 16;
-    l.start[total >> 16] = total & 0xFFFF;
+    l.start[total >> 16] = (uint16_t)total;
+    l.tile[total >> 16] = (uint16_t)all;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (place[i] >= 0) l.pair[count[ids[t + 256 * i]] + place[i]] = t + 256 * i;
+    if (place[i] >= 0) l.pair[w.count[w.ids[t + T * i]] + place[i]] = (uint16_t)(t + T * i);
   __syncthreads();
   // in order (the atomics' is any): a pair's tile decides where its sums are split
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int p = t + 256 * i;
+    const int p = t + T * i;
     if (place[i] >= 0) {
-      const int e = ids[p], from = count[e];
+      const int from = w.count[w.ids[p]];
       int rank = 0;
       for (int q = from; q < from + made[i]; ++q) rank += l.pair[q] < p ? 1 : 0;
       place[i] = from + rank;
@@ -137,8 +144,19 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, int (&ids)[kMoeMaxPairs],
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (place[i] >= 0) l.pair[place[i]] = t + 256 * i;
+    if (place[i] >= 0) l.pair[place[i]] = (uint16_t)(t + T * i);
   __syncthreads();
+}
+
+// The active expert whose tiles hold tile `at` (at < tile[active]), the same in all lanes.
+__device__ __forceinline__ int moe_expert_of(const MoeLists& l, int active, int at, int lane) {
+  int i = 0;
+  for (int first = 0; first < active; first += 64) {
+    const int n = __popcll(__ballot(first + lane < active && l.tile[min(first + lane, active - 1) + 1] <= at));
+    i += n;
+    if (n < 64) break;
+  }
+  return i;
 }
 
 // The weight of a pair: of its slot and of later ones with the same expert.
@@ -150,189 +168,267 @@ __device__ __forceinline__ float moe_weight(const MoeArgs& a, int m0, int pair, 
   return w;
 }
 
-__global__ void __launch_bounds__(64 * kUpWaves)
-moe_up_kernel(MoeArgs a) {
-  constexpr int KW = kUpWaves, D = kUpDepth;
-  __shared__ MoeLists l;
-  __shared__ int ids[kMoeMaxPairs], count[kMoeMaxExperts], sums[4];
-  __shared__ f32x4 red[KW - 1][2][64];
-  const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int m0 = blockIdx.z * kMoeTokens, rows = min(kMoeTokens, a.M - m0);
-  moe_lists(l, ids, count, sums, a, m0, rows);
-  if (blockIdx.x == 0 && blockIdx.y == 0) {  // for the second product
-    int32_t* out = a.lists + (int64_t)blockIdx.z * (sizeof(MoeLists) / 4);
-    const int32_t* in = reinterpret_cast<const int32_t*>(&l);
-    for (int i = t; i < (int)(sizeof(MoeLists) / 4); i += 64 * KW) out[i] = in[i];
+// (s, z) of a unit's groups for a lane's row of weights: one load of each where rows begin at multiples of eight
+// groups, else a load a group.
+template <bool VEC>
+struct MoeSz;
+template <>
+struct MoeSz<true> {
+  uint4 s, z;
+  __device__ __forceinline__ void load(const f16* sp, const f16* zp, int g, int) {
+    s = *reinterpret_cast<const uint4*>(sp + g);
+    z = *reinterpret_cast<const uint4*>(zp + g);
   }
-  if ((int)blockIdx.y >= l.active) return;
-  const int e = __builtin_amdgcn_readfirstlane(l.expert[blockIdx.y]);
-  const int start = __builtin_amdgcn_readfirstlane(l.start[blockIdx.y]);
-  const int n_pairs = __builtin_amdgcn_readfirstlane(l.start[blockIdx.y + 1]) - start;
-  const int n0 = blockIdx.x * 16, G = a.H >> 7;
-  const int g_lo = (G * wave) / KW, ng = (G * (wave + 1)) / KW - g_lo;
-  const uint32_t magic = magic_1024x2();
+  __device__ __forceinline__ f16 scale(int i) const { return half_of(s, i); }
+  __device__ __forceinline__ f16 zero(int i) const { return half_of(z, i); }
+};
+template <>
+struct MoeSz<false> {
+  uint32_t s[kMoeUnit], z[kMoeUnit];
+  __device__ __forceinline__ void load(const f16* sp, const f16* zp, int g, int last) {
+#pragma unroll
+    for (int i = 0; i < kMoeUnit; ++i) {
+      s[i] = reinterpret_cast<const uint16_t*>(sp)[min(g + i, last)];
+      z[i] = reinterpret_cast<const uint16_t*>(zp)[min(g + i, last)];
+    }
+  }
+  __device__ __forceinline__ f16 scale(int i) const { return bits_to_f16((uint16_t)s[i]); }
+  __device__ __forceinline__ f16 zero(int i) const { return bits_to_f16((uint16_t)z[i]); }
+};
 
-  // rows n0 + r of the gate (j = 0) and of the up projection (j = 1)
-  const uint32_t* wrow[2];
-  const f16 *srow[2], *zrow[2];
+// acc[j] += x . w[j]^T over groups g0 .. g0 + ng - 1 (g0 a multiple of kMoeUnit), for 16 rows of x and NW tiles of 16
+// rows of weights, by one wave: D groups are in flight, each group's rows of x pass through the wave's slot of LDS
+// into the order of the product's operand (4 XL rows; PERM: reordered to the codes' on the way).
+//  w[j], sp[j], zp[j]: of the lane's row of weights, group 0 (w: its four words of a group).
+//  xp[j]: the lane's eight channels of group 0 of row h + 4 j.
+template <int NW, int XL, int D, bool VEC, bool PERM>
+__device__ __forceinline__ void moe_stream(f32x4 (&acc)[NW], const uint32_t* const (&w)[NW],
+                                           const f16* const (&sp)[NW], const f16* const (&zp)[NW],
+                                           const f16* const (&xp)[XL], f16* slot, int g0, int ng, int lane) {
+  static_assert(kMoeUnit % D == 0, "slots of a unit");
+  const int r = lane & 15, h = lane >> 4;
+  const uint32_t magic = magic_1024x2();
+  const f16* frag = slot + min(r, 4 * XL - 1) * kMoeRowHalves + 32 * h;
+  const int last = g0 + ng - 1;
+  uint4 wbuf[D][NW], xbuf[D][XL];
+  MoeSz<VEC> sz[NW], next[NW];
+  const auto fetch = [&](int i, int g) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t n = ((int64_t)e * 2 + j) * a.I + n0 + r;
-    wrow[j] = a.up + n * (16 * G) + 4 * h;
-    srow[j] = a.up_s + n * G;
-    zrow[j] = a.up_z + n * G;
+    for (int j = 0; j < NW; ++j) wbuf[i][j] = *reinterpret_cast<const uint4*>(w[j] + (int64_t)g * 16);
+#pragma unroll
+    for (int j = 0; j < XL; ++j) xbuf[i][j] = *reinterpret_cast<const uint4*>(xp[j] + (int64_t)g * 128);
+  };
+  const auto group = [&](int i, int u) {  // slot i, u-th of its unit
+#pragma unroll
+    for (int j = 0; j < XL; ++j)
+      *reinterpret_cast<uint4*>(slot + (h + 4 * j) * kMoeRowHalves + 8 * r) = PERM ? perm_x8(xbuf[i][j]) : xbuf[i][j];
+    uint4 xa[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) xa[s] = *reinterpret_cast<const uint4*>(frag + 8 * s);
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      const f16 b = (f16)1024.0f + sz[j].zero(u), nb = (f16)960.0f - b;
+      f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        part = mfma_16x16x32(as_f16x8(xa[s]),
+                             as_f16x8(step_operand<false>(wbuf[i][j], s, magic, f16x2{b, b}, f16x2{nb, nb}, f16x2{})),
+                             part);
+      acc[j] += (float)sz[j].scale(u) * part;
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < NW; ++j) next[j].load(sp[j], zp[j], g0, last);
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(i, min(g0 + i, last));
+  int g = g0;
+  for (; g + kMoeUnit <= last; g += kMoeUnit) {  // (a unit with another after it is whole)
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      sz[j] = next[j];
+      next[j].load(sp[j], zp[j], g + kMoeUnit, last);
+    }
+#pragma unroll
+    for (int u = 0; u < kMoeUnit; ++u) {
+      group(u % D, u);
+      fetch(u % D, min(g + u + D, last));
+      __builtin_amdgcn_sched_barrier(kSchedKeepGroups);  // the refill stays next to its consumption
+    }
   }
-  for (int r0 = 0; r0 < n_pairs; r0 += 16) {
-    const int pair = l.pair[start + min(r0 + r, n_pairs - 1)];
-    const f16* xrow = a.x + (int64_t)(m0 + pair / a.k) * a.H + 32 * h;
-    uint4 wbuf[D][2], xbuf[D][4];
-    f16 sbuf[D][2], zbuf[D][2];
-    const auto fetch = [&](int i, int g) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        wbuf[i][j] = *reinterpret_cast<const uint4*>(wrow[j] + (int64_t)g * 16);
-        sbuf[i][j] = srow[j][g];
-        zbuf[i][j] = zrow[j][g];
-      }
+  for (int j = 0; j < NW; ++j) sz[j] = next[j];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) xbuf[i][s] = *reinterpret_cast<const uint4*>(xrow + (int64_t)g * 128 + 8 * s);
-    };
-    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    const auto group = [&](int i) {
-      uint4 xa[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) xa[s] = perm_x8(xbuf[i][s]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const f16 b = (f16)1024.0f + zbuf[i][j], nb = (f16)960.0f - b;
-        f32x4 part = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          part = mfma_16x16x32(as_f16x8(xa[s]),
-                               as_f16x8(step_operand<false>(wbuf[i][j], s, magic, f16x2{b, b}, f16x2{nb, nb}, f16x2{})),
-                               part);
-        acc[j] += (float)sbuf[i][j] * part;
-      }
-    };
-    const int last = max(ng - 1, 0);
-    const int gl = min(g_lo, G - 1);
-#pragma unroll
-    for (int i = 0; i < D; ++i) fetch(i, gl + min(i, last));
-    for (int b = 0; b < ng; b += D) {
-#pragma unroll
-      for (int i = 0; i < D; ++i) {
-        if (b + i < ng) group(i);
-        fetch(i, gl + min(b + D + i, last));
-      }
+  for (int u = 0; u < kMoeUnit; ++u) {
+    if (g + u <= last) {
+      group(u % D, u);
+      if constexpr (D < kMoeUnit)
+        if (u + D < kMoeUnit) fetch(u % D, min(g + u + D, last));
     }
-    if (wave > 0) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) red[wave - 1][j][lane] = acc[j];
-    }
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 0; w < KW - 1; ++w)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j] += red[w][j][lane];
-      const int at = moe_h_index(n0 + r);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 4 * h + i;
-        if (row < n_pairs) {
-          const float gate = acc[0][i], v = gate / (1.0f + expf(-gate)) * acc[1][i];
-          a.h[((int64_t)m0 * a.k + l.pair[start + row]) * a.I + at] = (f16)v;
-        }
-      }
-    }
-    __syncthreads();
   }
 }
 
-__global__ void __launch_bounds__(64 * kDownWaves)
-moe_down_kernel(MoeArgs a) {
-  constexpr int KW = kDownWaves, D = kDownDepth;
-  extern __shared__ __align__(16) float sums[];  // [KW][rows][16]
+// h of 16 pairs and 16 inner channels from their sums: rows 4 (lane / 16) + i
+__device__ __forceinline__ void moe_store_h(const MoeArgs& a, const MoeLists& l, const f32x4 (&acc)[2], int m0, int c0,
+                                            int first, int count, int lane) {
+  const int r = lane & 15, h = lane >> 4, at = c0 + (r & 8) + perm_slot(r & 7);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * h + i;
+    if (row < count) {
+      const float gate = acc[0][i], v = gate / (1.0f + expf(-gate)) * acc[1][i];
+      a.h[((int64_t)m0 * a.k + l.pair[first + row]) * a.I + at] = (f16)v;
+    }
+  }
+}
+
+struct MoeUpLds {
+  MoeLists l;
+  MoeScratch scratch;
+  f32x4 part[kMoeWaves][2][2][64];  // a wave's sums of an item that it shares: the one it goes on with, the one it begins
+  f16 slot[kMoeWaves][16 * kMoeRowHalves];
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(64 * kMoeWaves)
+moe_up_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  MoeUpLds& lds = *reinterpret_cast<MoeUpLds*>(smem);
+  const MoeLists& l = lds.l;
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int m0 = blockIdx.z * kMoeTokens, rows = min(kMoeTokens, a.M - m0);
-  const MoeLists* l = reinterpret_cast<const MoeLists*>(a.lists + (int64_t)blockIdx.z * (sizeof(MoeLists) / 4));
-  float* mine = sums + wave * rows * 16;
-  for (int i = lane; i < rows * 16; i += 64) mine[i] = 0.0f;
-  const int n0 = blockIdx.x * 16, G = a.I >> 7;
-  const uint32_t magic = magic_1024x2();
-  const int active = l->active;
-  // steps: an expert's groups for each 16 of its pairs
-  int items = 0;
-  for (int i = 0; i < active; ++i) items += (l->start[i + 1] - l->start[i] + 15) >> 4;
-  const int total = items * G;
-  const int s_lo = (int)((int64_t)total * wave / KW), s_hi = (int)((int64_t)total * (wave + 1) / KW);
-  // the item that step s_lo is of
-  int i0 = 0, r0 = 0;
-  for (int left = s_lo / G; i0 < active; ++i0) {
-    const int tiles = (l->start[i0 + 1] - l->start[i0] + 15) >> 4;
-    if (left < tiles) {
-      r0 = 16 * left;
-      break;
-    }
-    left -= tiles;
+  const int m0 = blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
+  moe_lists(lds.l, lds.scratch, a, m0, rows);
+  if (blockIdx.x == 0) {  // for the second product
+    int32_t* out = reinterpret_cast<int32_t*>(a.lists + blockIdx.y);
+    const int32_t* in = reinterpret_cast<const int32_t*>(&l);
+    for (int i = t; i < (int)(sizeof(MoeLists) / 4); i += 64 * kMoeWaves) out[i] = in[i];
   }
-  for (int s = s_lo; s < s_hi;) {
-    const int e = l->expert[i0], start = l->start[i0], n_pairs = l->start[i0 + 1] - start;
-    const int g_lo = s % G, ng = min(G - g_lo, s_hi - s);
-    const int pair = l->pair[start + min(r0 + r, n_pairs - 1)];
-    const f16* hrow = a.h + ((int64_t)m0 * a.k + pair) * a.I + 8 * h;
-    const int64_t n = (int64_t)e * a.H + n0 + r;
-    const uint32_t* wrow = a.down + n * (16 * G) + 4 * h;
-    const f16 *srow = a.down_s + n * G, *zrow = a.down_z + n * G;
-    uint4 wbuf[D], xbuf[D][4];
-    f16 sbuf[D], zbuf[D];
-    const auto fetch = [&](int i, int g) {
-      wbuf[i] = *reinterpret_cast<const uint4*>(wrow + (int64_t)g * 16);
-      sbuf[i] = srow[g];
-      zbuf[i] = zrow[g];
+  const int active = __builtin_amdgcn_readfirstlane(l.active);
+  const int G = a.H >> 7, U = (G + kMoeUnit - 1) / kMoeUnit, C = a.I >> 4;
+  // items: (expert, 16 channels, 16 pairs), the pairs fastest; the block's, whole, and the wave's share of their units
+  const int64_t items = (int64_t)l.tile[active] * C;
+  const int64_t i_lo = items * blockIdx.x / gridDim.x, i_hi = items * (blockIdx.x + 1) / gridDim.x;
+  const int64_t units = (i_hi - i_lo) * U;
+  const int64_t u_lo = units * wave / kMoeWaves, u_hi = units * (wave + 1) / kMoeWaves;
+  int which = 0;
+  int open_c0 = 0, open_first = 0, open_count = 0;  // of the item that the wave begins and others finish
+  int64_t open_end = 0;
+  if (u_lo < u_hi) which = moe_expert_of(l, active, (int)((i_lo + u_lo / U) / C), lane);
+  for (int64_t u = u_lo; u < u_hi;) {
+    const int64_t item = i_lo + u / U;
+    const int q = (int)(u % U), n_units = (int)(U - q < u_hi - u ? U - q : u_hi - u);
+    while (item >= (int64_t)l.tile[which + 1] * C) ++which;
+    const int e = __builtin_amdgcn_readfirstlane(l.expert[which]);
+    const int tiles = __builtin_amdgcn_readfirstlane(l.tile[which + 1] - l.tile[which]);
+    const int rem = (int)(item - (int64_t)l.tile[which] * C);
+    const int c0 = 16 * (rem / tiles), r0 = 16 * (rem % tiles);
+    const int first = l.start[which] + r0, count = min(16, (int)l.start[which + 1] - first);
+    const uint32_t* w[2];
+    const f16 *sp[2], *zp[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) xbuf[i][q] = *reinterpret_cast<const uint4*>(hrow + (int64_t)g * 128 + 32 * q);
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = ((int64_t)e * 2 + j) * a.I + c0 + r;
+      w[j] = a.up + n * (16 * G) + 4 * h;
+      sp[j] = a.up_s + n * G;
+      zp[j] = a.up_z + n * G;
+    }
+    const int g0 = kMoeUnit * q, ng = min(kMoeUnit * n_units, G - g0);
+    const auto row_of = [&](int row) {
+      return a.x + (int64_t)(m0 + l.pair[first + min(row, count - 1)] / a.k) * a.H + 8 * r;
     };
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D; ++i) fetch(i, g_lo + min(i, ng - 1));
-    for (int b = 0; b < ng; b += D) {
-#pragma unroll
-      for (int i = 0; i < D; ++i) {
-        if (b + i < ng) {
-          const f16 bi = (f16)1024.0f + zbuf[i], nb = (f16)960.0f - bi;
-          f32x4 part = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            part = mfma_16x16x32(as_f16x8(xbuf[i][q]),
-                                 as_f16x8(step_operand<false>(wbuf[i], q, magic, f16x2{bi, bi}, f16x2{nb, nb}, f16x2{})),
-                                 part);
-          acc += (float)sbuf[i] * part;
-        }
-        fetch(i, g_lo + min(b + D + i, ng - 1));
-      }
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    if (count <= 4) {
+      const f16* xp[1] = {row_of(h)};
+      moe_stream<2, 1, 8, VEC, true>(acc, w, sp, zp, xp, lds.slot[wave], g0, ng, lane);
+    } else {
+      const f16* xp[4] = {row_of(h), row_of(h + 4), row_of(h + 8), row_of(h + 12)};
+      moe_stream<2, 4, 4, VEC, true>(acc, w, sp, zp, xp, lds.slot[wave], g0, ng, lane);
     }
+    u += n_units;
+    if (n_units == U) {
+      moe_store_h(a, l, acc, m0, c0, first, count, lane);
+    } else {
+      const int begun = q == 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = r0 + 4 * h + i;
-      if (row < n_pairs) {
-        const int p = l->pair[start + row];
-        mine[p / a.k * 16 + r] += moe_weight(a, m0, p, e) * acc[i];
+      for (int j = 0; j < 2; ++j) lds.part[wave][begun][j][lane] = acc[j];
+      if (begun) {
+        open_end = u - n_units + U;
+        open_c0 = c0;
+        open_first = first;
+        open_count = count;
       }
-    }
-    s += ng;
-    r0 += 16;
-    if (r0 >= n_pairs) {
-      r0 = 0;
-      ++i0;
     }
   }
   __syncthreads();
-  for (int i = t; i < rows * 16; i += 64 * KW) {
+  if (open_count > 0) {
+    f32x4 acc[2] = {lds.part[wave][1][0][lane], lds.part[wave][1][1][lane]};
+    for (int v = wave + 1; v < kMoeWaves && units * v / kMoeWaves < open_end; ++v) {
+      if (units * v / kMoeWaves == units * (v + 1) / kMoeWaves) continue;  // (a wave without units)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[j] += lds.part[v][0][j][lane];
+    }
+    moe_store_h(a, l, acc, m0, open_c0, open_first, open_count, lane);
+  }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(64 * kMoeWaves)
+moe_down_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int m0 = blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
+  MoeLists& l = *reinterpret_cast<MoeLists*>(smem);
+  f16* slot = reinterpret_cast<f16*>(smem + sizeof(MoeLists)) + wave * 16 * kMoeRowHalves;
+  float* sums = reinterpret_cast<float*>(smem + sizeof(MoeLists) + kMoeWaves * 16 * kMoeRowHalves * 2);  // [wave][rows][16]
+  float* mine = sums + wave * rows * 16;
+  {
+    const uint4* in = reinterpret_cast<const uint4*>(a.lists + blockIdx.y);
+    for (int i = t; i < (int)(sizeof(MoeLists) / 16); i += 64 * kMoeWaves) reinterpret_cast<uint4*>(&l)[i] = in[i];
+  }
+  for (int i = lane; i < rows * 16; i += 64) mine[i] = 0.0f;
+  __syncthreads();
+  const int active = __builtin_amdgcn_readfirstlane(l.active);
+  const int n0 = blockIdx.x * 16, G = a.I >> 7, U = (G + kMoeUnit - 1) / kMoeUnit;
+  // items: (expert, 16 pairs); the wave's share of their units
+  const int units = l.tile[active] * U;
+  const int u_lo = units * wave / kMoeWaves, u_hi = units * (wave + 1) / kMoeWaves;
+  int which = u_lo < u_hi ? moe_expert_of(l, active, u_lo / U, lane) : 0;
+  for (int u = u_lo; u < u_hi;) {
+    const int item = u / U, q = u % U, n_units = min(U - q, u_hi - u);
+    while (item >= l.tile[which + 1]) ++which;
+    const int e = __builtin_amdgcn_readfirstlane(l.expert[which]);
+    const int first = l.start[which] + 16 * (item - l.tile[which]);
+    const int count = min(16, (int)l.start[which + 1] - first);
+    const int64_t n = (int64_t)e * a.H + n0 + r;
+    const uint32_t* w[1] = {a.down + n * (16 * G) + 4 * h};
+    const f16 *sp[1] = {a.down_s + n * G}, *zp[1] = {a.down_z + n * G};
+    const int g0 = kMoeUnit * q, ng = min(kMoeUnit * n_units, G - g0);
+    const auto row_of = [&](int row) {
+      return a.h + ((int64_t)m0 * a.k + l.pair[first + min(row, count - 1)]) * a.I + 8 * r;
+    };
+    f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+    if (count <= 4) {
+      const f16* xp[1] = {row_of(h)};
+      moe_stream<1, 1, 8, VEC, false>(acc, w, sp, zp, xp, slot, g0, ng, lane);
+    } else {
+      const f16* xp[4] = {row_of(h), row_of(h + 4), row_of(h + 8), row_of(h + 12)};
+      moe_stream<1, 4, 8, VEC, false>(acc, w, sp, zp, xp, slot, g0, ng, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * h + i;
+      if (row < count) {
+        const int p = l.pair[first + row];
+        mine[p / a.k * 16 + r] += moe_weight(a, m0, p, e) * acc[0][i];
+      }
+    }
+    u += n_units;
+  }
+  __syncthreads();
+  for (int i = t; i < rows * 16; i += 64 * kMoeWaves) {
     float v = sums[i];
-    for (int w = 1; w < KW; ++w) v += sums[w * rows * 16 + i];
+    for (int k = 1; k < kMoeWaves; ++k) v += sums[k * rows * 16 + i];
     const int64_t o = (int64_t)(m0 + (i >> 4)) * a.H + n0 + (i & 15);
     if (a.y_f32)
       static_cast<float*>(a.y)[o] = v;
@@ -341,11 +437,15 @@ moe_down_kernel(MoeArgs a) {
   }
 }
 
-static int64_t moe_chunks(int64_t M) { return (M + kMoeTokens - 1) / kMoeTokens; }
+static int64_t moe_tokens(int64_t M, int64_t k) {
+  const int64_t most = kMoeMaxPairs / k < kMoeTokens ? kMoeMaxPairs / k : kMoeTokens;
+  return M < most ? M : most;
+}
+static int64_t moe_chunks(int64_t M, int64_t k) { return (M + moe_tokens(M, k) - 1) / moe_tokens(M, k); }
 static size_t moe_h_bytes(int64_t M, int64_t I, int64_t k) { return ((size_t)(M * k) * I * 2 + 255) / 256 * 256; }
 
 size_t moe_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t k) {
-  return moe_h_bytes(M, I, k) + (size_t)moe_chunks(M) * sizeof(MoeLists);
+  return moe_h_bytes(M, I, k) + (size_t)moe_chunks(M, k) * sizeof(MoeLists);
 }
 
 hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int32_t* experts, const float* weights,
@@ -363,7 +463,7 @@ hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int
   a.down_s = reinterpret_cast<const f16*>(down_s);
   a.down_z = reinterpret_cast<const f16*>(down_z);
   a.h = static_cast<f16*>(workspace);
-  a.lists = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + moe_h_bytes(M, I, k));
+  a.lists = reinterpret_cast<MoeLists*>(static_cast<char*>(workspace) + moe_h_bytes(M, I, k));
   a.y = y;
   a.M = (int)M;
   a.H = (int)H;
@@ -371,18 +471,26 @@ hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int
   a.E = (int)E;
   a.k = (int)k;
   a.y_f32 = y_f32;
-  const int64_t tokens = M < kMoeTokens ? M : kMoeTokens, most = tokens * k < E ? tokens * k : E;
-  const unsigned chunks = (unsigned)moe_chunks(M);
-  hipLaunchKernelGGL(moe_up_kernel, dim3((unsigned)(I / 16), (unsigned)most, chunks), dim3(64 * kUpWaves), 0, stream,
-                     a);
-  hipError_t e = hipGetLastError();
+  a.tokens = (int)moe_tokens(M, k);
+  const unsigned chunks = (unsigned)moe_chunks(M, k);
+  const auto vec = [](int64_t K, const void* s, const void* z) {  // rows of (s, z) begin at multiples of 16 bytes
+    return K / 128 % 8 == 0 && ((reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+  };
+  // a block a CU, or fewer where there are fewer items
+  const int64_t pairs = a.tokens * k, tiles = pairs < E + pairs / 16 ? pairs : E + pairs / 16;
+  const int64_t items = tiles * (I / 16);
+  const auto up_kernel = vec(H, up_s, up_z) ? moe_up_kernel<true> : moe_up_kernel<false>;
+  hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(up_kernel), sizeof(MoeUpLds));
   if (e != hipSuccess) return e;
-  const size_t lds = (size_t)kDownWaves * tokens * 64;
-  if (lds > 65536) {
-    e = set_dynamic_lds(reinterpret_cast<const void*>(moe_down_kernel), lds);
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(H / 16), 1, chunks), dim3(64 * kDownWaves), lds, stream, a);
+  hipLaunchKernelGGL(up_kernel, dim3((unsigned)(items < kNumCu ? items : kNumCu), chunks), dim3(64 * kMoeWaves),
+                     sizeof(MoeUpLds), stream, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const auto down_kernel = vec(I, down_s, down_z) ? moe_down_kernel<true> : moe_down_kernel<false>;
+  const size_t lds = sizeof(MoeLists) + kMoeWaves * (16 * kMoeRowHalves * 2 + (size_t)a.tokens * 64);
+  e = set_dynamic_lds(reinterpret_cast<const void*>(down_kernel), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(down_kernel, dim3((unsigned)(H / 16), chunks), dim3(64 * kMoeWaves), lds, stream, a);
   return hipGetLastError();
 }
 
