@@ -348,12 +348,12 @@ size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t t
  *  gate_up  [E, 2 I, H/8] uint32 as written by wq_pack, each expert's I rows of G and then its
  *           I rows of U; gate_up_scales, gate_up_zeros [E, 2 I, H/128] fp16.
  *  down     [E, H, I/8] uint32; down_scales, down_zeros [E, H, I/128] fp16.
- *  H, I     multiples of 128, 2 H I below 2^31; M up to 65535 * 64, M * H below 2^31.
+ *  H, I     multiples of 128 up to 65536, 2 H I below 2^31; M up to 65535 * 64, M * H below 2^31.
  *  group    128.   y  [M, H] out, fp16 or float32 (y_dtype), 4-byte aligned.
  *  workspace: required for M >= 1, 256-byte aligned, wq_moe_experts_workspace_bytes bytes;
  *  contents on entry do not matter.
  * Sums are fp32; the inner activations silu(..) * (..) are rounded once to fp16, an MFMA
- * operand (beyond 65504 they are infinite), y once. Two launches. Deterministic: a fixed
+ * operand (beyond 65504 they are infinite), y once. Two launches for up to 4 rows, else three. Deterministic: a fixed
  * order for the same experts (other rows in the batch may split a row's sums elsewhere, and so
  * round its last bits otherwise; their values never reach it).
  */

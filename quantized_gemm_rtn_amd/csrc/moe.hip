@@ -20,6 +20,8 @@ constexpr int kMoeMaxPairs = 1024;  // of them, (row, expert) pairs
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeWaves = 8;        // of a block, one block a CU
 constexpr int kMoeUnit = 8;         // groups of 128 channels: what waves' shares are multiples of
+constexpr int kMoePairs = 32;       // (row, expert) pairs of an item
+constexpr int kMoeFew = 4;          // rows of a batch up to which the kernels for few rows run
 constexpr int kMoeRowHalves = 136;  // of a staged row: 128 and padding (16 rows of a fragment in distinct banks)
 
 // What some rows of x have to do, from their experts: the active experts in ascending order, each with its (row,
@@ -28,7 +30,7 @@ struct MoeLists {
   int32_t active, pad[3];             // experts
   uint16_t expert[kMoeMaxPairs];      // of the i-th active one,
   uint16_t start[kMoeMaxPairs + 8];   // its first pair (start[active]: their number),
-  uint16_t tile[kMoeMaxPairs + 8];    // and its first tile of 16 pairs (tile[active]: theirs)
+  uint16_t tile[kMoeMaxPairs + 8];    // and its first tile of kMoePairs pairs (tile[active]: theirs)
   uint16_t pair[kMoeMaxPairs];
 };
 
@@ -43,6 +45,7 @@ struct MoeArgs {
   const f16* down_s;
   const f16* down_z;
   f16* h;                  // [M * k][I], each eight channels in the order of perm_x8
+  float* v;                // [M * k][H]: the pairs' sums, unless few rows
   MoeLists* lists;         // of each `tokens` rows
   void* y;
   int M, H, I, E, k, y_f32;
@@ -94,7 +97,7 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
   for (int i = 0; i < EPER; ++i) {
     own[i] = w.count[EPER * t + i];
     both += own[i] + (own[i] > 0 ? 1 << 16 : 0);
-    tiles += (own[i] + 15) >> 4;
+    tiles += (own[i] + kMoePairs - 1) / kMoePairs;
   }
   const int both_upto = sum_upto_64(both, lane), tiles_upto = sum_upto_64(tiles, lane);
   if (lane == 63) {
@@ -118,7 +121,7 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
       l.tile[before >> 16] = (uint16_t)tile;
       w.count[EPER * t + i] = before & 0xFFFF;  // where its pairs begin
       before += own[i] + (1 << 16);
-      tile += (own[i] + 15) >> 4;
+      tile += (own[i] + kMoePairs - 1) / kMoePairs;
     }
   if (t == 0) {
     l.active = total >> 16;
@@ -168,86 +171,110 @@ __device__ __forceinline__ float moe_weight(const MoeArgs& a, int m0, int pair, 
   return w;
 }
 
-// (s, z) of a unit's groups for a lane's row of weights: one load of each where rows begin at multiples of eight
-// groups, else a load a group.
-template <bool VEC>
-struct MoeSz;
-template <>
-struct MoeSz<true> {
-  uint4 s, z;
-  __device__ __forceinline__ void load(const f16* sp, const f16* zp, int g, int) {
-    s = *reinterpret_cast<const uint4*>(sp + g);
-    z = *reinterpret_cast<const uint4*>(zp + g);
-  }
-  __device__ __forceinline__ f16 scale(int i) const { return half_of(s, i); }
-  __device__ __forceinline__ f16 zero(int i) const { return half_of(z, i); }
-};
-template <>
-struct MoeSz<false> {
-  uint32_t s[kMoeUnit], z[kMoeUnit];
-  __device__ __forceinline__ void load(const f16* sp, const f16* zp, int g, int last) {
+// NW tiles of 16 rows of one expert's weights: bases that all lanes share, and offsets in 32 bits. The lane's row of a tile
+// is lane % 16 (w: its four words of a group); its (s, z) row is that of tile lane / 16 % NW.
+template <int NW>
+struct MoeTiles {
+  const uint8_t* w[NW];
+  const uint8_t *s, *z;   // of the expert
+  uint32_t w_off, s_off;  // bytes
+  uint32_t s_end;         // from s to the array's end, at most 2^31
+  // tile j begins at row n[j] of the expert's `rows`
+  __device__ __forceinline__ void set(const uint32_t* w0, const f16* s0, const f16* z0, int e, int E, int rows,
+                                      const int (&n)[NW], int G, int lane) {
+    int mine = n[0];
+    const int64_t row0 = (int64_t)e * rows;
 #pragma unroll
-    for (int i = 0; i < kMoeUnit; ++i) {
-      s[i] = reinterpret_cast<const uint16_t*>(sp)[min(g + i, last)];
-      z[i] = reinterpret_cast<const uint16_t*>(zp)[min(g + i, last)];
+    for (int j = 0; j < NW; ++j) {
+      w[j] = reinterpret_cast<const uint8_t*>(w0) + (row0 + n[j]) * (64 * G);
+      mine = (lane >> 4) % NW == j ? n[j] : mine;
     }
+    w_off = (uint32_t)(lane & 15) * (64 * G) + 16 * (lane >> 4);
+    s = reinterpret_cast<const uint8_t*>(s0) + row0 * (2 * G);
+    z = reinterpret_cast<const uint8_t*>(z0) + row0 * (2 * G);
+    s_off = (uint32_t)(mine + (lane & 15)) * (2 * G);
+    const int64_t left = (int64_t)(E - e) * rows * (2 * G);
+    s_end = (uint32_t)(left < (int64_t)1 << 31 ? left : (int64_t)1 << 31);
   }
-  __device__ __forceinline__ f16 scale(int i) const { return bits_to_f16((uint16_t)s[i]); }
-  __device__ __forceinline__ f16 zero(int i) const { return bits_to_f16((uint16_t)z[i]); }
+};
+struct __attribute__((packed, aligned(2))) EightHalves {
+  uint4 v;
 };
 
-// acc[j] += x . w[j]^T over groups g0 .. g0 + ng - 1 (g0 a multiple of kMoeUnit), for 16 rows of x and NW tiles of 16
-// rows of weights, by one wave: D groups are in flight, each group's rows of x pass through the wave's slot of LDS
-// into the order of the product's operand (4 XL rows; PERM: reordered to the codes' on the way).
-//  w[j], sp[j], zp[j]: of the lane's row of weights, group 0 (w: its four words of a group).
-//  xp[j]: the lane's eight channels of group 0 of row h + 4 j.
-template <int NW, int XL, int D, bool VEC, bool PERM>
-__device__ __forceinline__ void moe_stream(f32x4 (&acc)[NW], const uint32_t* const (&w)[NW],
-                                           const f16* const (&sp)[NW], const f16* const (&zp)[NW],
-                                           const f16* const (&xp)[XL], f16* slot, int g0, int ng, int lane) {
-  static_assert(kMoeUnit % D == 0, "slots of a unit");
+// acc[i][j] += x . w[j]^T over groups g0 .. g0 + ng - 1 (g0 a multiple of kMoeUnit), for 16 MT rows of x and NW tiles of
+// weights, by one wave: D groups are in flight; each group's rows of x pass through the wave's slot of LDS into the
+// order of the product's operand (4 XL rows; PERM: reordered to the codes' on the way), and a unit's (s, 1024 + z)
+// through its table, loaded a tile for each 16 lanes, eight groups at once at any alignment.
+//  xs + xo[j] bytes: the lane's eight channels of group 0 of row lane / 16 + 4 j.
+template <int MT, int NW, int XL, int D, bool PERM>
+__device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<NW>& tiles, const uint8_t* xs,
+                                           const uint32_t (&xo)[XL], f16* slot, uint32_t* table, int g0, int ng, int lane) {
+  static_assert(kMoeUnit % D == 0 && XL <= 4 * MT && (MT == 1 || XL == 4 * MT), "slots of a unit, rows");
   const int r = lane & 15, h = lane >> 4;
   const uint32_t magic = magic_1024x2();
   const f16* frag = slot + min(r, 4 * XL - 1) * kMoeRowHalves + 32 * h;
   const int last = g0 + ng - 1;
   uint4 wbuf[D][NW], xbuf[D][XL];
-  MoeSz<VEC> sz[NW], next[NW];
+  uint4 s8, z8;
+  int off;
+  const auto fetch_sz = [&](int g) {
+    // eight from group g on, those of the array's end instead where it has fewer left
+    const uint32_t want = tiles.s_off + 2 * g, at = min(want, tiles.s_end - 16);
+    off = (int)(want - at) >> 1;
+    s8 = reinterpret_cast<const EightHalves*>(tiles.s + at)->v;
+    z8 = reinterpret_cast<const EightHalves*>(tiles.z + at)->v;
+  };
+  const auto put_sz = [&]() {
+    const f16x8 s = as_f16x8(s8), z = as_f16x8(z8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= off) table[(i - off) * 16 * NW + h % NW * 16 + r] = as_u32(f16x2{s[i], (f16)((f16)1024.0f + z[i])});
+    __builtin_amdgcn_wave_barrier();
+  };
   const auto fetch = [&](int i, int g) {
 #pragma unroll
-    for (int j = 0; j < NW; ++j) wbuf[i][j] = *reinterpret_cast<const uint4*>(w[j] + (int64_t)g * 16);
+    for (int j = 0; j < NW; ++j) wbuf[i][j] = *reinterpret_cast<const uint4*>(tiles.w[j] + 64 * g + tiles.w_off);
 #pragma unroll
-    for (int j = 0; j < XL; ++j) xbuf[i][j] = *reinterpret_cast<const uint4*>(xp[j] + (int64_t)g * 128);
+    for (int j = 0; j < XL; ++j) xbuf[i][j] = *reinterpret_cast<const uint4*>(xs + 256 * g + xo[j]);
   };
   const auto group = [&](int i, int u) {  // slot i, u-th of its unit
 #pragma unroll
     for (int j = 0; j < XL; ++j)
       *reinterpret_cast<uint4*>(slot + (h + 4 * j) * kMoeRowHalves + 8 * r) = PERM ? perm_x8(xbuf[i][j]) : xbuf[i][j];
-    uint4 xa[4];
+    uint4 xa[MT][4];
+    uint32_t sz[NW];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) xa[s] = *reinterpret_cast<const uint4*>(frag + 8 * s);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) xa[m][s] = *reinterpret_cast<const uint4*>(frag + m * 16 * kMoeRowHalves + 8 * s);
+#pragma unroll
+    for (int j = 0; j < NW; ++j) sz[j] = table[(u * NW + j) * 16 + r];
 #pragma unroll
     for (int j = 0; j < NW; ++j) {
-      const f16 b = (f16)1024.0f + sz[j].zero(u), nb = (f16)960.0f - b;
-      f32x4 part = {0.f, 0.f, 0.f, 0.f};
+      if (MT > 1) __builtin_amdgcn_sched_barrier(0);  // (else the tiles' unpacked codes are all held at once, and spill)
+      const f16x2 v = as_f16x2(sz[j]);
+      const f16 nb = (f16)960.0f - v[1];
+      f32x4 part[MT];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        part = mfma_16x16x32(as_f16x8(xa[s]),
-                             as_f16x8(step_operand<false>(wbuf[i][j], s, magic, f16x2{b, b}, f16x2{nb, nb}, f16x2{})),
-                             part);
-      acc[j] += (float)sz[j].scale(u) * part;
+      for (int m = 0; m < MT; ++m) part[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const f16x8 b =
+            as_f16x8(step_operand<false>(wbuf[i][j], s, magic, f16x2{v[1], v[1]}, f16x2{nb, nb}, f16x2{}));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) part[m] = mfma_16x16x32(as_f16x8(xa[m][s]), b, part[m]);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m][j] += (float)v[0] * part[m];
     }
   };
-#pragma unroll
-  for (int j = 0; j < NW; ++j) next[j].load(sp[j], zp[j], g0, last);
+  fetch_sz(g0);
 #pragma unroll
   for (int i = 0; i < D; ++i) fetch(i, min(g0 + i, last));
   int g = g0;
   for (; g + kMoeUnit <= last; g += kMoeUnit) {  // (a unit with another after it is whole)
-#pragma unroll
-    for (int j = 0; j < NW; ++j) {
-      sz[j] = next[j];
-      next[j].load(sp[j], zp[j], g + kMoeUnit, last);
-    }
+    put_sz();
+    fetch_sz(g + kMoeUnit);
 #pragma unroll
     for (int u = 0; u < kMoeUnit; ++u) {
       group(u % D, u);
@@ -255,8 +282,7 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[NW], const uint32_t* con
       __builtin_amdgcn_sched_barrier(kSchedKeepGroups);  // the refill stays next to its consumption
     }
   }
-#pragma unroll
-  for (int j = 0; j < NW; ++j) sz[j] = next[j];
+  put_sz();
 #pragma unroll
   for (int u = 0; u < kMoeUnit; ++u) {
     if (g + u <= last) {
@@ -264,172 +290,219 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[NW], const uint32_t* con
       if constexpr (D < kMoeUnit)
         if (u + D < kMoeUnit) fetch(u % D, min(g + u + D, last));
     }
+    __builtin_amdgcn_sched_barrier(kSchedKeepGroups);
   }
 }
 
-// h of 16 pairs and 16 inner channels from their sums: rows 4 (lane / 16) + i
-__device__ __forceinline__ void moe_store_h(const MoeArgs& a, const MoeLists& l, const f32x4 (&acc)[2], int m0, int c0,
-                                            int first, int count, int lane) {
-  const int r = lane & 15, h = lane >> 4, at = c0 + (r & 8) + perm_slot(r & 7);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 4 * h + i;
-    if (row < count) {
-      const float gate = acc[0][i], v = gate / (1.0f + expf(-gate)) * acc[1][i];
-      a.h[((int64_t)m0 * a.k + l.pair[first + row]) * a.I + at] = (f16)v;
-    }
-  }
-}
-
-struct MoeUpLds {
-  MoeLists l;
-  MoeScratch scratch;
-  f32x4 part[kMoeWaves][2][2][64];  // a wave's sums of an item that it shares: the one it goes on with, the one it begins
-  f16 slot[kMoeWaves][16 * kMoeRowHalves];
+// An item of the first (UP) or second product: 16 NW rows of weights of one expert (UP: half of them the gate's, half
+// the up projection's) and up to kMoePairs of its pairs.
+struct MoeItem {
+  int which, e;      // active expert
+  int c0;            // first channel
+  int first, count;  // pairs
 };
 
-template <bool VEC>
+// What a wave makes of an item's sums, acc[i][j]: rows 16 i + 4 (lane / 16) + 0..3, channel lane % 16 of tile j.
+template <bool UP, int MT, int NW>
+__device__ __forceinline__ void moe_store(const MoeArgs& a, const MoeLists& l, const f32x4 (&acc)[MT][NW],
+                                          const MoeItem& t, int m0, int lane) {
+  const int r = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * m + 4 * h + i;
+      if (row < t.count) {
+        const int64_t pair = (int64_t)m0 * a.k + l.pair[t.first + row];
+        if constexpr (UP) {
+#pragma unroll
+          for (int j = 0; j < NW / 2; ++j) {
+            const float gate = acc[m][j][i], v = gate / (1.0f + expf(-gate)) * acc[m][j + NW / 2][i];
+            a.h[pair * a.I + t.c0 + 16 * j + (r & 8) + perm_slot(r & 7)] = (f16)v;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NW; ++j) a.v[pair * a.H + t.c0 + 16 * j + r] = acc[m][j][i];
+        }
+      }
+    }
+}
+
+template <int MT, int NW>
+struct MoeRowsLds {
+  MoeLists l;
+  f32x4 part[kMoeWaves][MT * NW][64];  // a wave's sums of the item that it goes on with
+  union {
+    MoeScratch scratch;
+    struct {
+      f16 slot[kMoeWaves][16 * MT * kMoeRowHalves];
+      uint32_t table[kMoeWaves][kMoeUnit * NW * 16];
+    };
+  };
+};
+
+// One of the layer's two products, for all pairs: items in equal runs for one block a CU, a block's units (an item's
+// groups, eight at a time) in equal shares for its waves; what waves share of an item they join through LDS.
+// FEW: batches of up to kMoeFew rows, none of whose items has more pairs.
+template <bool UP, bool FEW>
 __global__ void __launch_bounds__(64 * kMoeWaves)
-moe_up_kernel(MoeArgs a) {
+moe_rows_kernel(MoeArgs a) {
+  constexpr int MT = FEW ? 1 : 2, NW = FEW ? 2 : 4;
   extern __shared__ __align__(16) char smem[];
-  MoeUpLds& lds = *reinterpret_cast<MoeUpLds*>(smem);
-  const MoeLists& l = lds.l;
+  MoeRowsLds<MT, NW>& lds = *reinterpret_cast<MoeRowsLds<MT, NW>*>(smem);
+  MoeLists& l = lds.l;
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int m0 = blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
-  moe_lists(lds.l, lds.scratch, a, m0, rows);
-  if (blockIdx.x == 0) {  // for the second product
-    int32_t* out = reinterpret_cast<int32_t*>(a.lists + blockIdx.y);
-    const int32_t* in = reinterpret_cast<const int32_t*>(&l);
-    for (int i = t; i < (int)(sizeof(MoeLists) / 4); i += 64 * kMoeWaves) out[i] = in[i];
+  if constexpr (UP) {
+    moe_lists(l, lds.scratch, a, m0, rows);
+    if (blockIdx.x == 0) {  // for the second product
+      uint4* out = reinterpret_cast<uint4*>(a.lists + blockIdx.y);
+      for (int i = t; i < (int)(sizeof(MoeLists) / 16); i += 64 * kMoeWaves) out[i] = reinterpret_cast<uint4*>(&l)[i];
+    }
+  } else {
+    const uint4* in = reinterpret_cast<const uint4*>(a.lists + blockIdx.y);
+    for (int i = t; i < (int)(sizeof(MoeLists) / 16); i += 64 * kMoeWaves) reinterpret_cast<uint4*>(&l)[i] = in[i];
+    __syncthreads();
   }
   const int active = __builtin_amdgcn_readfirstlane(l.active);
-  const int G = a.H >> 7, U = (G + kMoeUnit - 1) / kMoeUnit, C = a.I >> 4;
-  // items: (expert, 16 channels, 16 pairs), the pairs fastest; the block's, whole, and the wave's share of their units
+  const int K = UP ? a.H : a.I, N = UP ? a.I : a.H;
+  constexpr int CH = UP ? 8 * NW : 16 * NW;  // channels of an item
+  const int G = K >> 7, U = (G + kMoeUnit - 1) / kMoeUnit, C = N / CH;
+  // items: (expert, channels, pairs), the pairs fastest
   const int64_t items = (int64_t)l.tile[active] * C;
   const int64_t i_lo = items * blockIdx.x / gridDim.x, i_hi = items * (blockIdx.x + 1) / gridDim.x;
   const int64_t units = (i_hi - i_lo) * U;
   const int64_t u_lo = units * wave / kMoeWaves, u_hi = units * (wave + 1) / kMoeWaves;
-  int which = 0;
-  int open_c0 = 0, open_first = 0, open_count = 0;  // of the item that the wave begins and others finish
+  MoeItem it = {};
+  bool open = false;  // the wave begins an item that others finish
   int64_t open_end = 0;
-  if (u_lo < u_hi) which = moe_expert_of(l, active, (int)((i_lo + u_lo / U) / C), lane);
+  f32x4 acc[MT][NW];
+  if (u_lo < u_hi) it.which = moe_expert_of(l, active, (int)((i_lo + u_lo / U) / C), lane);
   for (int64_t u = u_lo; u < u_hi;) {
     const int64_t item = i_lo + u / U;
     const int q = (int)(u % U), n_units = (int)(U - q < u_hi - u ? U - q : u_hi - u);
-    while (item >= (int64_t)l.tile[which + 1] * C) ++which;
-    const int e = __builtin_amdgcn_readfirstlane(l.expert[which]);
-    const int tiles = __builtin_amdgcn_readfirstlane(l.tile[which + 1] - l.tile[which]);
-    const int rem = (int)(item - (int64_t)l.tile[which] * C);
-    const int c0 = 16 * (rem / tiles), r0 = 16 * (rem % tiles);
-    const int first = l.start[which] + r0, count = min(16, (int)l.start[which + 1] - first);
-    const uint32_t* w[2];
-    const f16 *sp[2], *zp[2];
+    while (item >= (int64_t)l.tile[it.which + 1] * C) ++it.which;
+    it.e = __builtin_amdgcn_readfirstlane(l.expert[it.which]);
+    const int before = __builtin_amdgcn_readfirstlane(l.tile[it.which]);
+    const int n_tiles = __builtin_amdgcn_readfirstlane(l.tile[it.which + 1]) - before;
+    const int rem = (int)(item - (int64_t)before * C);
+    it.c0 = CH * (rem / n_tiles);
+    it.first = __builtin_amdgcn_readfirstlane(l.start[it.which]) + kMoePairs * (rem % n_tiles);
+    it.count = min(kMoePairs, __builtin_amdgcn_readfirstlane(l.start[it.which + 1]) - it.first);
+    MoeTiles<NW> tiles;
+    int n[NW];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t n = ((int64_t)e * 2 + j) * a.I + c0 + r;
-      w[j] = a.up + n * (16 * G) + 4 * h;
-      sp[j] = a.up_s + n * G;
-      zp[j] = a.up_z + n * G;
-    }
+    for (int j = 0; j < NW; ++j)
+      n[j] = UP ? j / (NW / 2) * a.I + it.c0 + 16 * (j % (NW / 2)) : it.c0 + 16 * j;
+    if constexpr (UP)
+      tiles.set(a.up, a.up_s, a.up_z, it.e, a.E, 2 * a.I, n, G, lane);
+    else
+      tiles.set(a.down, a.down_s, a.down_z, it.e, a.E, a.H, n, G, lane);
     const int g0 = kMoeUnit * q, ng = min(kMoeUnit * n_units, G - g0);
+    const uint8_t* xs = reinterpret_cast<const uint8_t*>(UP ? a.x + (int64_t)m0 * a.H : a.h + (int64_t)m0 * a.k * a.I);
     const auto row_of = [&](int row) {
-      return a.x + (int64_t)(m0 + l.pair[first + min(row, count - 1)] / a.k) * a.H + 8 * r;
+      const uint32_t p = l.pair[it.first + min(row, it.count - 1)];
+      return (UP ? p / (uint32_t)a.k : p) * (256u * G) + 16 * r;
     };
-    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    if (count <= 4) {
-      const f16* xp[1] = {row_of(h)};
-      moe_stream<2, 1, 8, VEC, true>(acc, w, sp, zp, xp, lds.slot[wave], g0, ng, lane);
-    } else {
-      const f16* xp[4] = {row_of(h), row_of(h + 4), row_of(h + 8), row_of(h + 12)};
-      moe_stream<2, 4, 4, VEC, true>(acc, w, sp, zp, xp, lds.slot[wave], g0, ng, lane);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NW; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f16* slot = lds.slot[wave];
+    uint32_t* table = lds.table[wave];
+    f32x4(&top)[1][NW] = reinterpret_cast<f32x4(&)[1][NW]>(acc[0]);
+    if (it.count <= 4) {
+      const uint32_t xo[1] = {row_of(h)};
+      moe_stream<1, NW, 1, FEW ? 8 : 4, UP>(top, tiles, xs, xo, slot, table, g0, ng, lane);
+    } else if constexpr (!FEW) {
+      if (it.count <= 16) {
+        uint32_t xo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xo[j] = row_of(h + 4 * j);
+        moe_stream<1, NW, 4, 4, UP>(top, tiles, xs, xo, slot, table, g0, ng, lane);
+      } else {
+        uint32_t xo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xo[j] = row_of(h + 4 * j);
+        moe_stream<2, NW, 8, 2, UP>(acc, tiles, xs, xo, slot, table, g0, ng, lane);
+      }
     }
     u += n_units;
     if (n_units == U) {
-      moe_store_h(a, l, acc, m0, c0, first, count, lane);
+      moe_store<UP>(a, l, acc, it, m0, lane);
+    } else if (q == 0) {
+      open = true;
+      open_end = u - n_units + U;
     } else {
-      const int begun = q == 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) lds.part[wave][begun][j][lane] = acc[j];
-      if (begun) {
-        open_end = u - n_units + U;
-        open_c0 = c0;
-        open_first = first;
-        open_count = count;
-      }
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NW; ++j) lds.part[wave][m * NW + j][lane] = acc[m][j];
     }
   }
   __syncthreads();
-  if (open_count > 0) {
-    f32x4 acc[2] = {lds.part[wave][1][0][lane], lds.part[wave][1][1][lane]};
+  if (open) {
     for (int v = wave + 1; v < kMoeWaves && units * v / kMoeWaves < open_end; ++v) {
       if (units * v / kMoeWaves == units * (v + 1) / kMoeWaves) continue;  // (a wave without units)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[j] += lds.part[v][0][j][lane];
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NW; ++j) acc[m][j] += lds.part[v][m * NW + j][lane];
     }
-    moe_store_h(a, l, acc, m0, open_c0, open_first, open_count, lane);
+    moe_store<UP>(a, l, acc, it, m0, lane);
   }
 }
 
-template <bool VEC>
+// The second product of up to kMoeFew rows, and the sum over experts with it: a block for each 16 output channels, all
+// active experts' units in equal shares for its waves, each wave's sums in LDS.
 __global__ void __launch_bounds__(64 * kMoeWaves)
-moe_down_kernel(MoeArgs a) {
-  extern __shared__ __align__(16) char smem[];
+moe_down_few_kernel(MoeArgs a) {
+  __shared__ __align__(16) MoeLists l;
+  __shared__ __align__(16) f16 slots[kMoeWaves][4 * kMoeRowHalves];
+  __shared__ uint32_t tables[kMoeWaves][kMoeUnit * 16];
+  __shared__ float sums[kMoeWaves][kMoeFew * 16];
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int m0 = blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
-  MoeLists& l = *reinterpret_cast<MoeLists*>(smem);
-  f16* slot = reinterpret_cast<f16*>(smem + sizeof(MoeLists)) + wave * 16 * kMoeRowHalves;
-  float* sums = reinterpret_cast<float*>(smem + sizeof(MoeLists) + kMoeWaves * 16 * kMoeRowHalves * 2);  // [wave][rows][16]
-  float* mine = sums + wave * rows * 16;
   {
-    const uint4* in = reinterpret_cast<const uint4*>(a.lists + blockIdx.y);
+    const uint4* in = reinterpret_cast<const uint4*>(a.lists);
     for (int i = t; i < (int)(sizeof(MoeLists) / 16); i += 64 * kMoeWaves) reinterpret_cast<uint4*>(&l)[i] = in[i];
   }
-  for (int i = lane; i < rows * 16; i += 64) mine[i] = 0.0f;
+  float* mine = sums[wave];
+  mine[lane] = 0.0f;
   __syncthreads();
   const int active = __builtin_amdgcn_readfirstlane(l.active);
   const int n0 = blockIdx.x * 16, G = a.I >> 7, U = (G + kMoeUnit - 1) / kMoeUnit;
-  // items: (expert, 16 pairs); the wave's share of their units
-  const int units = l.tile[active] * U;
+  const int units = active * U;  // (an expert has one tile)
   const int u_lo = units * wave / kMoeWaves, u_hi = units * (wave + 1) / kMoeWaves;
-  int which = u_lo < u_hi ? moe_expert_of(l, active, u_lo / U, lane) : 0;
   for (int u = u_lo; u < u_hi;) {
-    const int item = u / U, q = u % U, n_units = min(U - q, u_hi - u);
-    while (item >= l.tile[which + 1]) ++which;
+    const int which = u / U, q = u % U, n_units = min(U - q, u_hi - u);
     const int e = __builtin_amdgcn_readfirstlane(l.expert[which]);
-    const int first = l.start[which] + 16 * (item - l.tile[which]);
-    const int count = min(16, (int)l.start[which + 1] - first);
-    const int64_t n = (int64_t)e * a.H + n0 + r;
-    const uint32_t* w[1] = {a.down + n * (16 * G) + 4 * h};
-    const f16 *sp[1] = {a.down_s + n * G}, *zp[1] = {a.down_z + n * G};
+    const int first = __builtin_amdgcn_readfirstlane(l.start[which]);
+    const int count = __builtin_amdgcn_readfirstlane(l.start[which + 1]) - first;
+    const int n[1] = {n0};
+    MoeTiles<1> tiles;
+    tiles.set(a.down, a.down_s, a.down_z, e, a.E, a.H, n, G, lane);
     const int g0 = kMoeUnit * q, ng = min(kMoeUnit * n_units, G - g0);
-    const auto row_of = [&](int row) {
-      return a.h + ((int64_t)m0 * a.k + l.pair[first + min(row, count - 1)]) * a.I + 8 * r;
-    };
-    f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-    if (count <= 4) {
-      const f16* xp[1] = {row_of(h)};
-      moe_stream<1, 1, 8, VEC, false>(acc, w, sp, zp, xp, slot, g0, ng, lane);
-    } else {
-      const f16* xp[4] = {row_of(h), row_of(h + 4), row_of(h + 8), row_of(h + 12)};
-      moe_stream<1, 4, 8, VEC, false>(acc, w, sp, zp, xp, slot, g0, ng, lane);
-    }
+    const uint32_t xo[1] = {l.pair[first + min(h, count - 1)] * (256u * G) + 16 * r};
+    f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+    moe_stream<1, 1, 1, 8, false>(acc, tiles, reinterpret_cast<const uint8_t*>(a.h), xo, slots[wave], tables[wave], g0, ng, lane);
+    if (h == 0) {  // rows 0 .. 3
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 4 * h + i;
-      if (row < count) {
-        const int p = l.pair[first + row];
-        mine[p / a.k * 16 + r] += moe_weight(a, m0, p, e) * acc[0][i];
-      }
+      for (int i = 0; i < 4; ++i)
+        if (i < count) {
+          const int p = l.pair[first + i];
+          mine[p / a.k * 16 + r] += moe_weight(a, 0, p, e) * acc[0][0][i];
+        }
     }
     u += n_units;
   }
   __syncthreads();
-  for (int i = t; i < rows * 16; i += 64 * kMoeWaves) {
-    float v = sums[i];
-    for (int k = 1; k < kMoeWaves; ++k) v += sums[k * rows * 16 + i];
-    const int64_t o = (int64_t)(m0 + (i >> 4)) * a.H + n0 + (i & 15);
+  if (t < a.M * 16) {
+    float v = sums[0][t];
+#pragma unroll
+    for (int k = 1; k < kMoeWaves; ++k) v += sums[k][t];
+    const int64_t o = (int64_t)(t >> 4) * a.H + n0 + (t & 15);
     if (a.y_f32)
       static_cast<float*>(a.y)[o] = v;
     else
@@ -437,15 +510,47 @@ moe_down_kernel(MoeArgs a) {
   }
 }
 
+// y of a row from its pairs' sums, in the order of its slots, four channels a thread.
+__global__ void __launch_bounds__(256)
+moe_join_kernel(MoeArgs a) {
+  const int m = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (c >= a.H) return;
+  const int32_t* e = a.experts + (int64_t)m * a.k;
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < a.k; ++j) {
+    bool first = (uint32_t)e[j] < (uint32_t)a.E;
+    for (int i = 0; i < j; ++i) first = first && e[i] != e[j];
+    if (first) y += moe_weight(a, m, j, e[j]) * *reinterpret_cast<const f32x4*>(a.v + ((int64_t)m * a.k + j) * a.H + c);
+  }
+  const int64_t o = (int64_t)m * a.H + c;
+  if (a.y_f32)
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + o) = y;
+  else
+    *reinterpret_cast<f16x4*>(static_cast<f16*>(a.y) + o) = f16x4{(f16)y[0], (f16)y[1], (f16)y[2], (f16)y[3]};
+}
+
 static int64_t moe_tokens(int64_t M, int64_t k) {
   const int64_t most = kMoeMaxPairs / k < kMoeTokens ? kMoeMaxPairs / k : kMoeTokens;
   return M < most ? M : most;
 }
 static int64_t moe_chunks(int64_t M, int64_t k) { return (M + moe_tokens(M, k) - 1) / moe_tokens(M, k); }
-static size_t moe_h_bytes(int64_t M, int64_t I, int64_t k) { return ((size_t)(M * k) * I * 2 + 255) / 256 * 256; }
+static size_t moe_round(size_t n) { return (n + 255) / 256 * 256; }
+static size_t moe_h_bytes(int64_t M, int64_t I, int64_t k) { return moe_round((size_t)(M * k) * I * 2); }
+static size_t moe_v_bytes(int64_t M, int64_t H, int64_t k) { return M <= kMoeFew ? 0 : moe_round((size_t)(M * k) * H * 4); }
 
 size_t moe_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t k) {
-  return moe_h_bytes(M, I, k) + (size_t)moe_chunks(M, k) * sizeof(MoeLists);
+  return moe_h_bytes(M, I, k) + moe_v_bytes(M, H, k) + (size_t)moe_chunks(M, k) * sizeof(MoeLists);
+}
+
+template <bool UP, bool FEW>
+static hipError_t launch_rows_product(const MoeArgs& a, int64_t items, unsigned chunks, hipStream_t stream) {
+  constexpr size_t lds = sizeof(MoeRowsLds<FEW ? 1 : 2, FEW ? 2 : 4>);
+  const hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(moe_rows_kernel<UP, FEW>), lds);
+  if (e != hipSuccess) return e;
+  // a block a CU, or fewer where there are fewer items
+  hipLaunchKernelGGL((moe_rows_kernel<UP, FEW>), dim3((unsigned)(items < kNumCu ? items : kNumCu), chunks),
+                     dim3(64 * kMoeWaves), lds, stream, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int32_t* experts, const float* weights,
@@ -453,6 +558,7 @@ hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int
                               int64_t I, const uint32_t* down, const uint16_t* down_s, const uint16_t* down_z, void* y,
                               int y_f32, void* workspace, hipStream_t stream) {
   MoeArgs a;
+  char* ws = static_cast<char*>(workspace);
   a.x = reinterpret_cast<const f16*>(x);
   a.experts = experts;
   a.weights = weights;
@@ -462,8 +568,9 @@ hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int
   a.down = down;
   a.down_s = reinterpret_cast<const f16*>(down_s);
   a.down_z = reinterpret_cast<const f16*>(down_z);
-  a.h = static_cast<f16*>(workspace);
-  a.lists = reinterpret_cast<MoeLists*>(static_cast<char*>(workspace) + moe_h_bytes(M, I, k));
+  a.h = reinterpret_cast<f16*>(ws);
+  a.v = reinterpret_cast<float*>(ws + moe_h_bytes(M, I, k));
+  a.lists = reinterpret_cast<MoeLists*>(ws + moe_h_bytes(M, I, k) + moe_v_bytes(M, H, k));
   a.y = y;
   a.M = (int)M;
   a.H = (int)H;
@@ -473,24 +580,18 @@ hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int
   a.y_f32 = y_f32;
   a.tokens = (int)moe_tokens(M, k);
   const unsigned chunks = (unsigned)moe_chunks(M, k);
-  const auto vec = [](int64_t K, const void* s, const void* z) {  // rows of (s, z) begin at multiples of 16 bytes
-    return K / 128 % 8 == 0 && ((reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-  };
-  // a block a CU, or fewer where there are fewer items
-  const int64_t pairs = a.tokens * k, tiles = pairs < E + pairs / 16 ? pairs : E + pairs / 16;
-  const int64_t items = tiles * (I / 16);
-  const auto up_kernel = vec(H, up_s, up_z) ? moe_up_kernel<true> : moe_up_kernel<false>;
-  hipError_t e = set_dynamic_lds(reinterpret_cast<const void*>(up_kernel), sizeof(MoeUpLds));
+  // tiles of pairs, at most
+  const int64_t pairs = a.tokens * k, tiles = pairs < E + pairs / kMoePairs ? pairs : E + pairs / kMoePairs;
+  if (M <= kMoeFew) {
+    const hipError_t e = launch_rows_product<true, true>(a, tiles * (I / 16), chunks, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(H / 16)), dim3(64 * kMoeWaves), 0, stream, a);
+    return hipGetLastError();
+  }
+  hipError_t e = launch_rows_product<true, false>(a, tiles * (I / 32), chunks, stream);
+  if (e == hipSuccess) e = launch_rows_product<false, false>(a, tiles * (H / 64), chunks, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(up_kernel, dim3((unsigned)(items < kNumCu ? items : kNumCu), chunks), dim3(64 * kMoeWaves),
-                     sizeof(MoeUpLds), stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const auto down_kernel = vec(I, down_s, down_z) ? moe_down_kernel<true> : moe_down_kernel<false>;
-  const size_t lds = sizeof(MoeLists) + kMoeWaves * (16 * kMoeRowHalves * 2 + (size_t)a.tokens * 64);
-  e = set_dynamic_lds(reinterpret_cast<const void*>(down_kernel), lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(down_kernel, dim3((unsigned)(H / 16), chunks), dim3(64 * kMoeWaves), lds, stream, a);
+  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)M, (unsigned)((H + 1023) / 1024)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -26,6 +26,7 @@ constexpr int64_t kMaxRank = 256;             // rank of the low-rank branch: mu
 constexpr int64_t kMaxAdapters = (int64_t)1 << 20;
 constexpr int64_t kMaxExperts = 1024;         // of a mixture-of-experts layer,
 constexpr int64_t kMaxTopK = 16;              // and of a row
+constexpr int64_t kMaxMoeWidth = 65536;       // channels: a few rows' offsets stay within 32 bits
 constexpr int64_t kMaxMoeRows = 65535 * 64;   // 64 rows a block, the grid's limit
 constexpr int64_t kMaxOutliers = 16;          // fp16 outlier channels of the W4A8 product
 
@@ -409,7 +410,8 @@ int wq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int64_t E,
 namespace {
 bool moe_sizes(int64_t M, int64_t H, int64_t I, int64_t top_k) {
   return M >= 0 && M <= kMaxMoeRows && H >= kGroup && H % kGroup == 0 && I >= kGroup && I % kGroup == 0 &&
-         top_k >= 1 && H < kMax32 / I / 2 && M < kMax32 / H && M < kMax32 / top_k;
+         H <= kMaxMoeWidth && I <= kMaxMoeWidth && top_k >= 1 && H < kMax32 / I / 2 && M < kMax32 / H &&
+         M < kMax32 / top_k;
 }
 }  // namespace
 
