@@ -19,7 +19,7 @@ constexpr int kMoeTokens = 192;     // rows of x that a block's lists hold; more
 constexpr int kMoeMaxPairs = 1024;  // of them, (row, expert) pairs
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeWaves = 8;        // of a block, one block a CU
-constexpr int kMoeUnit = 8;         // groups of 128 channels: what waves' shares are multiples of
+constexpr int kMoeUnit = 8;         // groups of 128 channels whose (s, z) a wave loads at once
 constexpr int kMoePairs = 32;       // (row, expert) pairs of an item
 constexpr int kMoeFew = 4;          // rows of a batch up to which the kernels for few rows run
 constexpr int kMoeRowHalves = 136;  // of a staged row: 128 and padding (16 rows of a fragment in distinct banks)
@@ -201,7 +201,7 @@ struct __attribute__((packed, aligned(2))) EightHalves {
   uint4 v;
 };
 
-// acc[i][j] += x . w[j]^T over groups g0 .. g0 + ng - 1 (g0 a multiple of kMoeUnit), for 16 MT rows of x and NW tiles of
+// acc[i][j] += x . w[j]^T over groups g0 .. g0 + ng - 1, for 16 MT rows of x and NW tiles of
 // weights, by one wave: D groups are in flight; each group's rows of x pass through the wave's slot of LDS into the
 // order of the product's operand (4 XL rows; PERM: reordered to the codes' on the way), and a unit's (s, 1024 + z)
 // through its table, loaded a tile for each 16 lanes, eight groups at once at any alignment.
@@ -341,8 +341,8 @@ struct MoeRowsLds {
   };
 };
 
-// One of the layer's two products, for all pairs: items in equal runs for one block a CU, a block's units (an item's
-// groups, eight at a time) in equal shares for its waves; what waves share of an item they join through LDS.
+// One of the layer's two products, for all pairs: items dealt in turn to one block a CU, a block's groups (G an item)
+// in equal shares for its waves; what waves share of an item they join through LDS.
 // FEW: batches of up to kMoeFew rows, none of whose items has more pairs.
 template <bool UP, bool FEW>
 __global__ void __launch_bounds__(64 * kMoeWaves)
@@ -368,20 +368,20 @@ moe_rows_kernel(MoeArgs a) {
   const int active = __builtin_amdgcn_readfirstlane(l.active);
   const int K = UP ? a.H : a.I, N = UP ? a.I : a.H;
   constexpr int CH = UP ? 8 * NW : 16 * NW;  // channels of an item
-  const int G = K >> 7, U = (G + kMoeUnit - 1) / kMoeUnit, C = N / CH;
+  const int G = K >> 7, C = N / CH;
   // items: (expert, channels, pairs), the pairs fastest
   const int64_t items = (int64_t)l.tile[active] * C;
-  const int64_t i_lo = items * blockIdx.x / gridDim.x, i_hi = items * (blockIdx.x + 1) / gridDim.x;
-  const int64_t units = (i_hi - i_lo) * U;
-  const int64_t u_lo = units * wave / kMoeWaves, u_hi = units * (wave + 1) / kMoeWaves;
+  const int64_t mine = (items - blockIdx.x + gridDim.x - 1) / gridDim.x;  // blockIdx.x, blockIdx.x + gridDim.x, ..
+  const int64_t groups = mine * G;
+  const int64_t u_lo = groups * wave / kMoeWaves, u_hi = groups * (wave + 1) / kMoeWaves;
   MoeItem it = {};
   bool open = false;  // the wave begins an item that others finish
   int64_t open_end = 0;
   f32x4 acc[MT][NW];
-  if (u_lo < u_hi) it.which = moe_expert_of(l, active, (int)((i_lo + u_lo / U) / C), lane);
+  if (u_lo < u_hi) it.which = moe_expert_of(l, active, (int)((blockIdx.x + u_lo / G * gridDim.x) / C), lane);
   for (int64_t u = u_lo; u < u_hi;) {
-    const int64_t item = i_lo + u / U;
-    const int q = (int)(u % U), n_units = (int)(U - q < u_hi - u ? U - q : u_hi - u);
+    const int64_t item = blockIdx.x + u / G * gridDim.x;
+    const int g0 = (int)(u % G), ng = (int)(G - g0 < u_hi - u ? G - g0 : u_hi - u);
     while (item >= (int64_t)l.tile[it.which + 1] * C) ++it.which;
     it.e = __builtin_amdgcn_readfirstlane(l.expert[it.which]);
     const int before = __builtin_amdgcn_readfirstlane(l.tile[it.which]);
@@ -399,7 +399,6 @@ moe_rows_kernel(MoeArgs a) {
       tiles.set(a.up, a.up_s, a.up_z, it.e, a.E, 2 * a.I, n, G, lane);
     else
       tiles.set(a.down, a.down_s, a.down_z, it.e, a.E, a.H, n, G, lane);
-    const int g0 = kMoeUnit * q, ng = min(kMoeUnit * n_units, G - g0);
     const uint8_t* xs = reinterpret_cast<const uint8_t*>(UP ? a.x + (int64_t)m0 * a.H : a.h + (int64_t)m0 * a.k * a.I);
     const auto row_of = [&](int row) {
       const uint32_t p = l.pair[it.first + min(row, it.count - 1)];
@@ -428,12 +427,12 @@ moe_rows_kernel(MoeArgs a) {
         moe_stream<2, NW, 8, 2, UP>(acc, tiles, xs, xo, slot, table, g0, ng, lane);
       }
     }
-    u += n_units;
-    if (n_units == U) {
+    u += ng;
+    if (ng == G) {
       moe_store<UP>(a, l, acc, it, m0, lane);
-    } else if (q == 0) {
+    } else if (g0 == 0) {
       open = true;
-      open_end = u - n_units + U;
+      open_end = u - ng + G;
     } else {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -443,8 +442,8 @@ moe_rows_kernel(MoeArgs a) {
   }
   __syncthreads();
   if (open) {
-    for (int v = wave + 1; v < kMoeWaves && units * v / kMoeWaves < open_end; ++v) {
-      if (units * v / kMoeWaves == units * (v + 1) / kMoeWaves) continue;  // (a wave without units)
+    for (int v = wave + 1; v < kMoeWaves && groups * v / kMoeWaves < open_end; ++v) {
+      if (groups * v / kMoeWaves == groups * (v + 1) / kMoeWaves) continue;  // (a wave without any)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -455,7 +454,7 @@ moe_rows_kernel(MoeArgs a) {
 }
 
 // The second product of up to kMoeFew rows, and the sum over experts with it: a block for each 16 output channels, all
-// active experts' units in equal shares for its waves, each wave's sums in LDS.
+// active experts' groups in equal shares for its waves, each wave's sums in LDS.
 __global__ void __launch_bounds__(64 * kMoeWaves)
 moe_down_few_kernel(MoeArgs a) {
   __shared__ __align__(16) MoeLists l;
@@ -472,18 +471,17 @@ moe_down_few_kernel(MoeArgs a) {
   mine[lane] = 0.0f;
   __syncthreads();
   const int active = __builtin_amdgcn_readfirstlane(l.active);
-  const int n0 = blockIdx.x * 16, G = a.I >> 7, U = (G + kMoeUnit - 1) / kMoeUnit;
-  const int units = active * U;  // (an expert has one tile)
-  const int u_lo = units * wave / kMoeWaves, u_hi = units * (wave + 1) / kMoeWaves;
-  for (int u = u_lo; u < u_hi;) {
-    const int which = u / U, q = u % U, n_units = min(U - q, u_hi - u);
+  const int n0 = blockIdx.x * 16, G = a.I >> 7;
+  const int64_t groups = (int64_t)active * G;  // (an expert has one tile)
+  const int64_t u_lo = groups * wave / kMoeWaves, u_hi = groups * (wave + 1) / kMoeWaves;
+  for (int64_t u = u_lo; u < u_hi;) {
+    const int which = (int)(u / G), g0 = (int)(u % G), ng = (int)(G - g0 < u_hi - u ? G - g0 : u_hi - u);
     const int e = __builtin_amdgcn_readfirstlane(l.expert[which]);
     const int first = __builtin_amdgcn_readfirstlane(l.start[which]);
     const int count = __builtin_amdgcn_readfirstlane(l.start[which + 1]) - first;
     const int n[1] = {n0};
     MoeTiles<1> tiles;
     tiles.set(a.down, a.down_s, a.down_z, e, a.E, a.H, n, G, lane);
-    const int g0 = kMoeUnit * q, ng = min(kMoeUnit * n_units, G - g0);
     const uint32_t xo[1] = {l.pair[first + min(h, count - 1)] * (256u * G) + 16 * r};
     f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
     moe_stream<1, 1, 1, 8, false>(acc, tiles, reinterpret_cast<const uint8_t*>(a.h), xo, slots[wave], tables[wave], g0, ng, lane);
@@ -495,7 +493,7 @@ moe_down_few_kernel(MoeArgs a) {
           mine[p / a.k * 16 + r] += moe_weight(a, 0, p, e) * acc[0][0][i];
         }
     }
-    u += n_units;
+    u += ng;
   }
   __syncthreads();
   if (t < a.M * 16) {
