@@ -151,6 +151,37 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
   __syncthreads();
 }
 
+// The same for up to 64 pairs, by the block's first wave: a pair a lane, the experts in the order of their first pairs.
+__device__ __forceinline__ void moe_few_lists(MoeLists& l, const MoeArgs& a, int rows) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x, pairs = rows * a.k, row = lane / a.k;
+    const int id = lane < pairs ? a.experts[lane] : -1;
+    const uint64_t below = ((uint64_t)1 << lane) - 1, row_below = below & ~(((uint64_t)1 << row * a.k) - 1);
+    uint64_t left = __ballot((uint32_t)id < (uint32_t)a.E);
+    int n = 0, at = 0;
+    for (; left != 0; ++n) {
+      const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      const uint64_t same = __ballot(id == e);
+      const bool first = id == e && (same & row_below) == 0;
+      const uint64_t members = __ballot(first);
+      if (first) l.pair[at + __popcll(members & below)] = (uint16_t)lane;
+      if (lane == 0) {
+        l.expert[n] = (uint16_t)e;
+        l.start[n] = (uint16_t)at;
+        l.tile[n] = (uint16_t)n;
+      }
+      at += __popcll(members);
+      left &= ~same;
+    }
+    if (lane == 0) {
+      l.active = n;
+      l.start[n] = (uint16_t)at;
+      l.tile[n] = (uint16_t)n;
+    }
+  }
+  __syncthreads();
+}
+
 // The active expert whose tiles hold tile `at` (at < tile[active]), the same in all lanes.
 __device__ __forceinline__ int moe_expert_of(const MoeLists& l, int active, int at, int lane) {
   int i = 0;
@@ -354,7 +385,9 @@ moe_rows_kernel(MoeArgs a) {
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int m0 = blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
-  if constexpr (UP) {
+  if constexpr (FEW) {
+    moe_few_lists(l, a, rows);
+  } else if constexpr (UP) {
     moe_lists(l, lds.scratch, a, m0, rows);
     if (blockIdx.x == 0) {  // for the second product
       uint4* out = reinterpret_cast<uint4*>(a.lists + blockIdx.y);
@@ -463,13 +496,9 @@ moe_down_few_kernel(MoeArgs a) {
   __shared__ float sums[kMoeWaves][kMoeFew * 16];
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  {
-    const uint4* in = reinterpret_cast<const uint4*>(a.lists);
-    for (int i = t; i < (int)(sizeof(MoeLists) / 16); i += 64 * kMoeWaves) reinterpret_cast<uint4*>(&l)[i] = in[i];
-  }
   float* mine = sums[wave];
   mine[lane] = 0.0f;
-  __syncthreads();
+  moe_few_lists(l, a, a.M);
   const int active = __builtin_amdgcn_readfirstlane(l.active);
   const int n0 = blockIdx.x * 16, G = a.I >> 7;
   const int64_t groups = (int64_t)active * G;  // (an expert has one tile)
@@ -511,14 +540,43 @@ moe_down_few_kernel(MoeArgs a) {
 // y of a row from its pairs' sums, in the order of its slots, four channels a thread.
 __global__ void __launch_bounds__(256)
 moe_join_kernel(MoeArgs a) {
+  __shared__ int slots[16], n_slots;
+  __shared__ float weight[16];
   const int m = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (threadIdx.x < 64) {
+    // slots that stand for an expert's pair, and their weights
+    const int lane = threadIdx.x;
+    const int id = lane < a.k ? a.experts[(int64_t)m * a.k + lane] : -1;
+    const float w = lane < a.k ? a.weights[(int64_t)m * a.k + lane] : 0.0f;
+    bool first = (uint32_t)id < (uint32_t)a.E;
+    float sum = w;
+    for (int j = 0; j < a.k; ++j) {
+      const int other = __builtin_amdgcn_readlane(id, j);
+      const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j));
+      first = first && !(j < lane && other == id);
+      sum += j > lane && other == id ? v : 0.0f;
+    }
+    const uint64_t mask = __ballot(first);
+    if (first) {
+      const int at = __popcll(mask & (((uint64_t)1 << lane) - 1));
+      slots[at] = lane;
+      weight[at] = sum;
+    }
+    if (lane == 0) n_slots = __popcll(mask);
+  }
+  __syncthreads();
   if (c >= a.H) return;
-  const int32_t* e = a.experts + (int64_t)m * a.k;
+  const float* v = a.v + (int64_t)m * a.k * a.H + c;
+  const int n = n_slots;
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < a.k; ++j) {
-    bool first = (uint32_t)e[j] < (uint32_t)a.E;
-    for (int i = 0; i < j; ++i) first = first && e[i] != e[j];
-    if (first) y += moe_weight(a, m, j, e[j]) * *reinterpret_cast<const f32x4*>(a.v + ((int64_t)m * a.k + j) * a.H + c);
+  constexpr int AHEAD = 4;  // slots whose loads are in flight together
+  for (int j = 0; j < n; j += AHEAD) {
+    f32x4 p[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) p[i] = *reinterpret_cast<const f32x4*>(v + (int64_t)slots[min(j + i, n - 1)] * a.H);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (j + i < n) y += weight[j + i] * p[i];
   }
   const int64_t o = (int64_t)m * a.H + c;
   if (a.y_f32)
