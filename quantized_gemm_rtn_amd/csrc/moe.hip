@@ -65,7 +65,7 @@ __device__ __forceinline__ int sum_upto_64(int v, int lane) {
 struct MoeScratch {
   int16_t ids[kMoeMaxPairs];
   int32_t count[kMoeMaxExperts];
-  int32_t sums[kMoeWaves][2];
+  int32_t sums[kMoeWaves];
 };
 __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeArgs& a, int m0, int rows) {
   constexpr int T = 64 * kMoeWaves, PER = kMoeMaxPairs / T, EPER = kMoeMaxExperts / T;
@@ -84,49 +84,51 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
   for (int i = 0; i < PER; ++i) {
     const int p = t + T * i, e = w.ids[p];
     bool first = e >= 0;
-    if (first)
-      for (int q = p / a.k * a.k; q < p; ++q) first = first && w.ids[q] != e;
+    const int begin = p / a.k * a.k;
+    for (int j = 0; j < a.k - 1; j += 4) {  // earlier slots of the row, four reads at a time
+      int other[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) other[v] = w.ids[min(begin + j + v, p)];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) first = first && !(begin + j + v < p && other[v] == e);
+    }
     place[i] = first ? atomicAdd(&w.count[e], 1) : -1;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < PER; ++i) made[i] = place[i] >= 0 ? w.count[w.ids[t + T * i]] : 0;  // pairs of the pair's expert
-  // experts EPER t .. + EPER - 1: active ones and pairs before them (in one sum), and tiles
-  int own[EPER], both = 0, tiles = 0;
+  // experts EPER t .. + EPER - 1: pairs, tiles beyond an expert's first, and active ones, in one sum (11, 6 and 11 bits)
+  const auto packed = [](int n) { return n == 0 ? 0 : n | ((n - 1) / kMoePairs) << 11 | 1 << 17; };
+  int own[EPER], sum = 0;
 #pragma unroll
   for (int i = 0; i < EPER; ++i) {
     own[i] = w.count[EPER * t + i];
-    both += own[i] + (own[i] > 0 ? 1 << 16 : 0);
-    tiles += (own[i] + kMoePairs - 1) / kMoePairs;
+    sum += packed(own[i]);
   }
-  const int both_upto = sum_upto_64(both, lane), tiles_upto = sum_upto_64(tiles, lane);
-  if (lane == 63) {
-    w.sums[wave][0] = both_upto;
-    w.sums[wave][1] = tiles_upto;
-  }
+  const int upto = sum_upto_64(sum, lane);
+  if (lane == 63) w.sums[wave] = upto;
   __syncthreads();
-  int before = both_upto - both, tile = tiles_upto - tiles, total = 0, all = 0;
+  int before = upto - sum, total = 0;
 #pragma unroll
   for (int v = 0; v < kMoeWaves; ++v) {
-    before += v < wave ? w.sums[v][0] : 0;
-    tile += v < wave ? w.sums[v][1] : 0;
-    total += w.sums[v][0];
-    all += w.sums[v][1];
+    before += v < wave ? w.sums[v] : 0;
+    total += w.sums[v];
   }
+  const auto put = [&](int at, int v) {
+    l.start[at] = (uint16_t)(v & 2047);
+    l.tile[at] = (uint16_t)(at + ((v >> 11) & 63));
+  };
 #pragma unroll
   for (int i = 0; i < EPER; ++i)
     if (own[i] > 0) {
-      l.expert[before >> 16] = (uint16_t)(EPER * t + i);
-      l.start[before >> 16] = (uint16_t)before;
-      l.tile[before >> 16] = (uint16_t)tile;
-      w.count[EPER * t + i] = before & 0xFFFF;  // where its pairs begin
-      before += own[i] + (1 << 16);
-      tile += (own[i] + kMoePairs - 1) / kMoePairs;
+      l.expert[before >> 17] = (uint16_t)(EPER * t + i);
+      put(before >> 17, before);
+      w.count[EPER * t + i] = before & 2047;  // where its pairs begin
+      before += packed(own[i]);
     }
   if (t == 0) {
-    l.active = total >> 16;
-    l.start[total >> 16] = (uint16_t)total;
-    l.tile[total >> 16] = (uint16_t)all;
+    l.active = total >> 17;
+    put(total >> 17, total);
   }
   __syncthreads();
 #pragma unroll
@@ -140,7 +142,13 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
     if (place[i] >= 0) {
       const int from = w.count[w.ids[p]];
       int rank = 0;
-      for (int q = from; q < from + made[i]; ++q) rank += l.pair[q] < p ? 1 : 0;
+      for (int q = 0; q < made[i]; q += 8) {  // eight reads at a time
+        int other[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) other[v] = l.pair[from + min(q + v, made[i] - 1)];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) rank += q + v < made[i] && other[v] < p ? 1 : 0;
+      }
       place[i] = from + rank;
     }
   }
@@ -384,7 +392,7 @@ moe_rows_kernel(MoeArgs a) {
   MoeLists& l = lds.l;
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int m0 = blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
+  const int m0 = (int)blockIdx.y * a.tokens, rows = min(a.tokens, a.M - m0);
   if constexpr (FEW) {
     moe_few_lists(l, a, rows);
   } else if constexpr (UP) {
@@ -403,25 +411,28 @@ moe_rows_kernel(MoeArgs a) {
   constexpr int CH = UP ? 8 * NW : 16 * NW;  // channels of an item
   const int G = K >> 7, C = N / CH;
   // items: (expert, channels, pairs), the pairs fastest
-  const int64_t items = (int64_t)l.tile[active] * C;
-  const int64_t mine = (items - blockIdx.x + gridDim.x - 1) / gridDim.x;  // blockIdx.x, blockIdx.x + gridDim.x, ..
-  const int64_t groups = mine * G;
-  const int64_t u_lo = groups * wave / kMoeWaves, u_hi = groups * (wave + 1) / kMoeWaves;
+  // (32 bits hold 1024 tiles of 2048 channels' items, and a block's groups: 64-bit divisions took 1 us here)
+  const uint32_t items = (uint32_t)l.tile[active] * C, nb = gridDim.x;
+  const uint32_t mine = items > blockIdx.x ? (items - blockIdx.x + nb - 1) / nb : 0;  // blockIdx.x, blockIdx.x + nb, ..
+  const uint32_t groups = mine * G;
+  const uint32_t u_lo = groups * wave / kMoeWaves, u_hi = groups * (wave + 1) / kMoeWaves;
   MoeItem it = {};
   bool open = false;  // the wave begins an item that others finish
-  int64_t open_end = 0;
+  uint32_t open_end = 0;
   f32x4 acc[MT][NW];
-  if (u_lo < u_hi) it.which = moe_expert_of(l, active, (int)((blockIdx.x + u_lo / G * gridDim.x) / C), lane);
-  for (int64_t u = u_lo; u < u_hi;) {
-    const int64_t item = blockIdx.x + u / G * gridDim.x;
-    const int g0 = (int)(u % G), ng = (int)(G - g0 < u_hi - u ? G - g0 : u_hi - u);
-    while (item >= (int64_t)l.tile[it.which + 1] * C) ++it.which;
+  uint32_t item = blockIdx.x + u_lo / G * nb;
+  int g0 = (int)(u_lo % G);
+  if (u_lo < u_hi) it.which = moe_expert_of(l, active, (int)(item / C), lane);
+  for (uint32_t u = u_lo; u < u_hi; item += nb, g0 = 0) {
+    const int ng = min(G - g0, (int)(u_hi - u));
+    while (item >= (uint32_t)l.tile[it.which + 1] * C) ++it.which;
     it.e = __builtin_amdgcn_readfirstlane(l.expert[it.which]);
     const int before = __builtin_amdgcn_readfirstlane(l.tile[it.which]);
     const int n_tiles = __builtin_amdgcn_readfirstlane(l.tile[it.which + 1]) - before;
-    const int rem = (int)(item - (int64_t)before * C);
-    it.c0 = CH * (rem / n_tiles);
-    it.first = __builtin_amdgcn_readfirstlane(l.start[it.which]) + kMoePairs * (rem % n_tiles);
+    const int rem = (int)item - before * C;
+    const int c = n_tiles == 1 ? rem : rem / n_tiles;
+    it.c0 = CH * c;
+    it.first = __builtin_amdgcn_readfirstlane(l.start[it.which]) + kMoePairs * (rem - c * n_tiles);
     it.count = min(kMoePairs, __builtin_amdgcn_readfirstlane(l.start[it.which + 1]) - it.first);
     MoeTiles<NW> tiles;
     int n[NW];
@@ -501,10 +512,11 @@ moe_down_few_kernel(MoeArgs a) {
   moe_few_lists(l, a, a.M);
   const int active = __builtin_amdgcn_readfirstlane(l.active);
   const int n0 = blockIdx.x * 16, G = a.I >> 7;
-  const int64_t groups = (int64_t)active * G;  // (an expert has one tile)
-  const int64_t u_lo = groups * wave / kMoeWaves, u_hi = groups * (wave + 1) / kMoeWaves;
-  for (int64_t u = u_lo; u < u_hi;) {
-    const int which = (int)(u / G), g0 = (int)(u % G), ng = (int)(G - g0 < u_hi - u ? G - g0 : u_hi - u);
+  const int groups = active * G;  // (an expert has one tile; at most 64 experts)
+  const int u_lo = groups * wave / kMoeWaves, u_hi = groups * (wave + 1) / kMoeWaves;
+  int which = u_lo / G, g0 = u_lo % G;
+  for (int u = u_lo; u < u_hi; ++which, g0 = 0) {
+    const int ng = min(G - g0, u_hi - u);
     const int e = __builtin_amdgcn_readfirstlane(l.expert[which]);
     const int first = __builtin_amdgcn_readfirstlane(l.start[which]);
     const int count = __builtin_amdgcn_readfirstlane(l.start[which + 1]) - first;
