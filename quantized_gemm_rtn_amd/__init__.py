@@ -391,10 +391,28 @@ def linear_adapters_workspace_bytes(M, N, K, r):
     return int(load().wq_linear_adapters_workspace_bytes(M, N, K, r))
 
 
-def _same_device(x, **others):
-    for name, t in others.items():
-        if t is not None and t.get_device() != x.get_device():
-            raise ValueError(f"{name} must be on the device of the activations")
+def _on_current_device(t, name):
+    """The device of ``t``, which must be the current one (the kernels are launched there)."""
+    import torch
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device")
+    return dev
+
+
+def _need_all(dev, *tensors):
+    """``_need`` of several (tensor, dtype, name), all on device ``dev``: one pass of the cheap tests (2 us a call
+    less with nine tensors), the reasons only where one fails."""
+    for t, dtype, name in tensors:
+        try:
+            if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _need(t, dtype, name)
+        raise ValueError(f"{name} must be on the device of the activations")
 
 
 def linear_adapters(x, packed, scales, zeros, L1, L2, adapter, adapter_scale=None, row_ptr=None, col=None, val=None,
@@ -408,59 +426,54 @@ def linear_adapters(x, packed, scales, zeros, L1, L2, adapter, adapter_scale=Non
     allocated per call when omitted."""
     import torch
     lib = load()
-    out_dtype = torch.float16 if out_dtype is None else out_dtype
-    _need(x, torch.float16, "x")
-    _need(packed, torch.int32, "packed")
-    _need(scales, torch.float16, "scales")
-    _need(zeros, torch.float16, "zeros")
-    _need(L1, torch.float16, "L1")
-    _need(L2, torch.float16, "L2")
-    _need(adapter, torch.int32, "adapter")
+    f16, i32 = torch.float16, torch.int32
+    out_dtype = f16 if out_dtype is None else out_dtype
+    if out_dtype is not f16 and out_dtype is not torch.float32:
+        raise TypeError("out_dtype must be float16 or float32")
+    dev = _on_current_device(x, "x")
+    _need_all(dev, (x, f16, "x"), (packed, i32, "packed"), (scales, f16, "scales"), (zeros, f16, "zeros"),
+              (L1, f16, "L1"), (L2, f16, "L2"), (adapter, i32, "adapter"))
     M, K = x.shape
-    N = packed.shape[0]
-    if packed.shape[1] * 8 != K or scales.shape != (N, K // group) or zeros.shape != scales.shape:
+    N, words = packed.shape
+    G = K // group
+    if words * 8 != K or scales.shape != (N, G) or zeros.shape != (N, G):
         raise ValueError("inconsistent shapes")
-    if L1.dim() != 3 or L1.shape[2] != K or L2.shape != (L1.shape[0], N, L1.shape[1]):
+    n, r, k1 = L1.shape if L1.dim() == 3 else (0, 0, -1)
+    if k1 != K or L2.shape != (n, N, r):
         raise ValueError("L1 must be [n, r, K] and L2 [n, N, r]")
-    if tuple(adapter.shape) != (M,):
+    if adapter.shape != (M,):
         raise ValueError("adapter must be [M]")
-    n, r = L1.shape[:2]
     if adapter_scale is not None:
-        _need(adapter_scale, torch.float32, "adapter_scale")
-        if tuple(adapter_scale.shape) != (n,):
+        _need_all(dev, (adapter_scale, torch.float32, "adapter_scale"))
+        if adapter_scale.shape != (n,):
             raise ValueError("adapter_scale must be [n]")
     nnz = 0
     if row_ptr is not None:
-        _need(row_ptr, torch.int32, "row_ptr")
+        _need_all(dev, (row_ptr, i32, "row_ptr"))
         if row_ptr.numel() != N + 1:
             raise ValueError("row_ptr must have N+1 entries")
         nnz = int(col.numel()) if col is not None else 0
         if nnz:
-            _need(col, torch.int32, "col")
-            _need(val, torch.float16, "val")
+            _need_all(dev, (col, i32, "col"), (val, f16, "val"))
             if val.numel() != nnz:
                 raise ValueError("col and val must have as many entries")
-    if out_dtype not in (torch.float16, torch.float32):
-        raise TypeError("out_dtype must be float16 or float32")
     if out is None:
         out = x.new_empty((M, N), dtype=out_dtype)
     else:
-        _need(out, out_dtype, "out")
-        if tuple(out.shape) != (M, N):
+        _need_all(dev, (out, out_dtype, "out"))
+        if out.shape != (M, N):
             raise ValueError("out must be [M, N]")
-    _same_device(x, packed=packed, scales=scales, zeros=zeros, L1=L1, L2=L2, adapter=adapter,
-                 adapter_scale=adapter_scale, out=out)
-    if nnz:
-        _same_device(x, row_ptr=row_ptr, col=col, val=val)
     if workspace is None:
         nbytes = int(lib.wq_linear_adapters_workspace_bytes(max(M, 1), N, K, r))
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
     wbytes = _workspace_bytes(workspace, x)
-    rc = lib.wq_linear_adapters(_p(x), M, K, _p(packed), _p(scales), _p(zeros), N, group, _p(row_ptr) if nnz else None,
-                                _p(col) if nnz else None, _p(val) if nnz else None, nnz, _p(L1), _p(L2),
-                                _p(adapter_scale), n, r, _p(adapter), _p(out), 1 if out_dtype == torch.float32 else 0,
-                                KERNELS[kernel], _p(workspace), wbytes, _stream(x))
-    _check("wq_linear_adapters", rc)
+    rc = lib.wq_linear_adapters(x.data_ptr(), M, K, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, group,
+                                _p(row_ptr) if nnz else None, _p(col) if nnz else None, _p(val) if nnz else None, nnz,
+                                L1.data_ptr(), L2.data_ptr(), _p(adapter_scale), n, r, adapter.data_ptr(),
+                                out.data_ptr(), 0 if out_dtype is f16 else 1, KERNELS[kernel], workspace.data_ptr(),
+                                wbytes, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check("wq_linear_adapters", rc)
     return out
 
 
@@ -471,14 +484,19 @@ def moe_route(logits, top_k: int, renormalize: bool = True):
     The weights are the softmax's values, with ``renormalize`` divided by their sum."""
     import torch
     lib = load()
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float16, torch.float32):
+    dev = _on_current_device(logits, "logits")
+    f32 = logits.dtype is torch.float32
+    if not f32 and logits.dtype is not torch.float16:
         raise TypeError("logits must be a float16 or float32 tensor")
-    _need(logits, logits.dtype, "logits")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
     M, E = logits.shape
     experts = logits.new_empty((M, top_k), dtype=torch.int32)
     weights = logits.new_empty((M, top_k), dtype=torch.float32)
-    _check("wq_moe_route", lib.wq_moe_route(_p(logits), 1 if logits.dtype == torch.float32 else 0, M, E, top_k,
-                                            1 if renormalize else 0, _p(experts), _p(weights), _stream(logits)))
+    rc = lib.wq_moe_route(logits.data_ptr(), 1 if f32 else 0, M, E, top_k, 1 if renormalize else 0,
+                          experts.data_ptr(), weights.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check("wq_moe_route", rc)
     return experts, weights
 
 
@@ -499,44 +517,43 @@ def moe_experts(x, experts, weights, gate_up, gate_up_scales, gate_up_zeros, dow
     omitted."""
     import torch
     lib = load()
-    out_dtype = torch.float16 if out_dtype is None else out_dtype
-    _need(x, torch.float16, "x")
-    _need(experts, torch.int32, "experts")
-    _need(weights, torch.float32, "weights")
-    for t, name in ((gate_up, "gate_up"), (down, "down")):
-        _need(t, torch.int32, name)
-    for t, name in ((gate_up_scales, "gate_up_scales"), (gate_up_zeros, "gate_up_zeros"),
-                    (down_scales, "down_scales"), (down_zeros, "down_zeros")):
-        _need(t, torch.float16, name)
-    M, H = x.shape
-    if experts.dim() != 2 or experts.shape[0] != M or weights.shape != experts.shape:
-        raise ValueError("experts and weights must be [M, top_k]")
-    if gate_up.dim() != 3 or down.dim() != 3:
-        raise ValueError("gate_up must be [E, 2 I, H / 8] and down [E, H, I / 8]")
-    E, I, top_k = gate_up.shape[0], down.shape[2] * 8, experts.shape[1]
-    if gate_up.shape != (E, 2 * I, H // 8) or down.shape != (E, H, I // 8) or H % 8:
-        raise ValueError("gate_up must be [E, 2 I, H / 8] and down [E, H, I / 8]")
-    if gate_up_scales.shape != (E, 2 * I, H // GROUP) or gate_up_zeros.shape != gate_up_scales.shape or \
-            down_scales.shape != (E, H, I // GROUP) or down_zeros.shape != down_scales.shape:
-        raise ValueError("scales and zeros must be [E, 2 I, H / 128] and [E, H, I / 128]")
-    if out_dtype not in (torch.float16, torch.float32):
+    f16, i32, f32 = torch.float16, torch.int32, torch.float32
+    out_dtype = f16 if out_dtype is None else out_dtype
+    if out_dtype is not f16 and out_dtype is not f32:
         raise TypeError("out_dtype must be float16 or float32")
+    dev = _on_current_device(x, "x")
+    _need_all(dev, (x, f16, "x"), (experts, i32, "experts"), (weights, f32, "weights"), (gate_up, i32, "gate_up"),
+              (gate_up_scales, f16, "gate_up_scales"), (gate_up_zeros, f16, "gate_up_zeros"), (down, i32, "down"),
+              (down_scales, f16, "down_scales"), (down_zeros, f16, "down_zeros"))
+    M, H = x.shape
+    rows, top_k = experts.shape if experts.dim() == 2 else (-1, 0)
+    if rows != M or weights.shape != (M, top_k):
+        raise ValueError("experts and weights must be [M, top_k]")
+    E, _, words = down.shape if down.dim() == 3 else (0, 0, 0)
+    I = 8 * words
+    if gate_up.shape != (E, 2 * I, H // 8) or down.shape != (E, H, words) or H % 8:
+        raise ValueError("gate_up must be [E, 2 I, H / 8] and down [E, H, I / 8]")
+    up_sz, down_sz = (E, 2 * I, H // GROUP), (E, H, I // GROUP)
+    if gate_up_scales.shape != up_sz or gate_up_zeros.shape != up_sz or \
+            down_scales.shape != down_sz or down_zeros.shape != down_sz:
+        raise ValueError("scales and zeros must be [E, 2 I, H / 128] and [E, H, I / 128]")
     if out is None:
         out = x.new_empty((M, H), dtype=out_dtype)
     else:
-        _need(out, out_dtype, "out")
-        if tuple(out.shape) != (M, H):
+        _need_all(dev, (out, out_dtype, "out"))
+        if out.shape != (M, H):
             raise ValueError("out must be [M, H]")
-    _same_device(x, experts=experts, weights=weights, gate_up=gate_up, gate_up_scales=gate_up_scales,
-                 gate_up_zeros=gate_up_zeros, down=down, down_scales=down_scales, down_zeros=down_zeros, out=out)
     if workspace is None:
         nbytes = int(lib.wq_moe_experts_workspace_bytes(max(M, 1), H, I, top_k))
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
     wbytes = _workspace_bytes(workspace, x)
-    rc = lib.wq_moe_experts(_p(x), M, H, _p(experts), _p(weights), top_k, E, _p(gate_up), _p(gate_up_scales),
-                            _p(gate_up_zeros), I, _p(down), _p(down_scales), _p(down_zeros), GROUP, _p(out),
-                            1 if out_dtype == torch.float32 else 0, _p(workspace), wbytes, _stream(x))
-    _check("wq_moe_experts", rc)
+    rc = lib.wq_moe_experts(x.data_ptr(), M, H, experts.data_ptr(), weights.data_ptr(), top_k, E, gate_up.data_ptr(),
+                            gate_up_scales.data_ptr(), gate_up_zeros.data_ptr(), I, down.data_ptr(),
+                            down_scales.data_ptr(), down_zeros.data_ptr(), GROUP, out.data_ptr(),
+                            0 if out_dtype is f16 else 1, workspace.data_ptr(), wbytes,
+                            torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check("wq_moe_experts", rc)
     return out
 
 
