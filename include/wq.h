@@ -282,8 +282,9 @@ int wq_linear_lowrank(const uint16_t* x, int64_t M, int64_t K,
                       void* y, int32_t y_dtype, int32_t kernel,
                       void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace wq_linear_adapters needs: t [M, r rounded up to 32] fp16 and the
- * split-K workspace of wq_linear_workspace_bytes(M, N, K). 0 for invalid sizes (r must be a
+/* Bytes of device workspace wq_linear_adapters needs: t [M, r rounded up to 32] fp16, the
+ * fp32 partials of the K chunks it may be summed over, and the split-K workspace of
+ * wq_linear_workspace_bytes(M, N, K). 0 for invalid sizes (r must be a
  * multiple of 8 up to 256). */
 size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 
@@ -300,7 +301,9 @@ size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64
  *  adapter        [M] int32, on the device like all arrays: rows outside [0, n_adapters) have
  *                 none. Rows in any order; rows of one adapter next to each other are faster.
  *  row_ptr / col / val / nnz as in wq_linear_sparse; row_ptr may be NULL when nnz == 0.
- *  kernel as in wq_linear_sparse_kernel (a single row takes the MFMA decode kernel).
+ *  kernel as in wq_linear_sparse_kernel, but AUTO keeps to the decode kernels also for more rows
+ *  (ceil(M / 16) N K up to 2^27, with eight adapters or more 2^28), and a single row takes the
+ *  MFMA decode kernel.
  *  workspace: required for M >= 1, 256-byte aligned, wq_linear_adapters_workspace_bytes bytes;
  *  contents on entry do not matter.
  * t = s x . L1^T is accumulated in fp32 and rounded once to fp16 (it is an MFMA operand);

@@ -5,8 +5,8 @@
 // t [M, r rounded up to 32]: zeros beyond r; rows of no adapter are left as they are, and nothing reads them.
 //
 //  adapters_down_dot_kernel  (few rows) a block for each row and few components: dot products, the waves split K.
-//  adapters_down_kernel      (more rows) a block for each 16 rows and 16 or 32 components: one pass of 16x16x32
-//    products for each adapter that the rows name, of which each row keeps its own.
+//  adapters_down_kernel      (more rows) a block for each 16 rows, 16 components and chunk of K: 16x16x32 products, its
+//    waves dealt to the adapters that the rows name; several chunks' partials are summed by adapters_finish_kernel.
 #include "wq_device.h"
 #include "wq_launch.h"
 
@@ -24,6 +24,10 @@ adapters_down_dot_kernel(const f16* __restrict__ x, int K, const f16* __restrict
   const int m = blockIdx.y, j0 = blockIdx.x * NC;
   const int a = __builtin_amdgcn_readfirstlane(adapter[m]);
   if ((uint32_t)a >= (uint32_t)n) return;
+  if (j0 >= r) {
+    if (threadIdx.x < NC) t[(int64_t)m * tr + j0 + threadIdx.x] = (f16)0.0f;
+    return;
+  }
   const f16* xrow = x + (int64_t)m * K + 8 * lane;
   const f16* lrow[NC];
 #pragma unroll
@@ -75,81 +79,141 @@ adapters_down_dot_kernel(const f16* __restrict__ x, int K, const f16* __restrict
 }
 
 constexpr int kRowWaves = 16;
-constexpr int kRowSteps = 8;                           // of a wave in a chunk of K
-constexpr int kRowChunk = 32 * kRowWaves * kRowSteps;  // input channels of a chunk
+constexpr int kRowBatch = 4;  // pairs of 32-channel steps whose loads a wave issues together
 
-template <int CT>
+// The waves are dealt to the adapters that the block's 16 rows name: all sixteen split K for one adapter, each has an
+// adapter of its own from nine on. (Adapter after adapter, 96 rows of as many adapters took 250 us at K = 8192.) A
+// wave's steps come in pairs, whole 128-byte lines of its rows.
 __global__ void __launch_bounds__(64 * kRowWaves)
 adapters_down_kernel(const f16* __restrict__ x, int M, int K, const f16* __restrict__ L1,
                      const float* __restrict__ scale, int n, int r, const int32_t* __restrict__ adapter,
-                     f16* __restrict__ t, int tr) {
-  constexpr int U = CT / 16;  // 16x16 tiles
+                     f16* __restrict__ t, int tr, int chunk, float* __restrict__ part) {
   const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int j0 = blockIdx.x * CT, m0 = blockIdx.y * 16;
+  const int j0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+  const int c_lo = blockIdx.z * chunk, c_hi = min(K, c_lo + chunk);
+  __shared__ f32x4 red[kRowWaves][64];
   const int id = adapter[min(m0 + q, M - 1)];
-  uint32_t left = (uint32_t)__ballot(m0 + q < M && (uint32_t)id < (uint32_t)n) & 0xFFFFu;
-  const f16* xr = x + (int64_t)min(m0 + q, M - 1) * K + 8 * h;
-  __shared__ f32x4 red[kRowWaves - 1][U][64];
-  uint4 av[kRowSteps];
-  for (bool first = true; left != 0; first = false) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    const uint32_t members = (uint32_t)__ballot(id == a) & left;
-    left &= ~members;
-    const f16* lr0 = L1 + ((int64_t)a * r + min(j0 + q, r - 1)) * K + 8 * h;
-    const f16* lr1 = L1 + ((int64_t)a * r + min(j0 + 16 + q, r - 1)) * K + 8 * h;
-    f32x4 acc[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 0; c0 < K; c0 += kRowChunk) {
-      // a wave's steps of 32 channels: every 16th of the chunk (K a multiple of 128: whole steps)
-      uint4 bv[kRowSteps][U];
-#pragma unroll
-      for (int i = 0; i < kRowSteps; ++i) {
-        const int c = c0 + 32 * (wave + kRowWaves * i);
-        if (c < K) {  // wave-uniform
-          if (first || K > kRowChunk) av[i] = *reinterpret_cast<const uint4*>(xr + c);
-          bv[i][0] = *reinterpret_cast<const uint4*>(lr0 + c);
-          if constexpr (U > 1) bv[i][U - 1] = *reinterpret_cast<const uint4*>(lr1 + c);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kRowSteps; ++i)
-        if (c0 + 32 * (wave + kRowWaves * i) < K) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) acc[u] = mfma_16x16x32(as_f16x8(av[i]), as_f16x8(bv[i][u]), acc[u]);
-        }
+  const uint32_t all = (uint32_t)__ballot(m0 + q < M && (uint32_t)id < (uint32_t)n) & 0xFFFFu;
+  int count = 0;  // of adapters
+  for (uint32_t left = all; left != 0; ++count)
+    left &= ~(uint32_t)__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctz(left)));
+  int shift = 4;  // log2 of the waves of an adapter
+  while ((kRowWaves >> shift) < count) --shift;
+  const int which = wave >> shift, sub = wave & ((1 << shift) - 1), per = 1 << shift;
+  uint32_t members = 0;
+  int a = 0;
+  if (which < count) {
+    uint32_t left = all;
+    for (int i = 0; i <= which; ++i) {
+      a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+      members = (uint32_t)__ballot(id == a) & left;
+      left &= ~members;
     }
-    if (wave > 0) {
+    // rows of other adapters: a row that is read anyway
+    const int row = (members >> q) & 1u ? q : __builtin_ctz(members);
+    const f16* xr = x + (int64_t)(m0 + row) * K + 8 * h;
+    const f16* lr = L1 + ((int64_t)a * r + min(j0 + q, r - 1)) * K + 8 * h;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = c_lo + 64 * sub; c0 < c_hi; c0 += 64 * per * kRowBatch) {
+      uint4 av[kRowBatch][2], bv[kRowBatch][2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) red[wave - 1][u][lane] = acc[u];
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const float s = scale ? scale[a] : 1.0f;
+      for (int i = 0; i < kRowBatch; ++i)
+        if (c0 + 64 * per * i < c_hi) {  // wave-uniform; chunks are multiples of 64
 #pragma unroll
-      for (int w = 0; w < kRowWaves - 1; ++w)
+          for (int u = 0; u < 2; ++u) {
+            av[i][u] = *reinterpret_cast<const uint4*>(xr + c0 + 64 * per * i + 32 * u);
+            bv[i][u] = *reinterpret_cast<const uint4*>(lr + c0 + 64 * per * i + 32 * u);
+          }
+        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) acc[u] += red[w][u][lane];
-      // row 4 h + i, component j0 + 16 u + q
+      for (int i = 0; i < kRowBatch; ++i)
+        if (c0 + 64 * per * i < c_hi) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = j0 + 16 * u + q;
-          if ((members >> (4 * h + i)) & 1u) t[(int64_t)(m0 + 4 * h + i) * tr + c] = c < r ? (f16)(s * acc[u][i]) : (f16)0.0f;
+          for (int u = 0; u < 2; ++u) acc = mfma_16x16x32(as_f16x8(av[i][u]), as_f16x8(bv[i][u]), acc);
         }
     }
-    __syncthreads();  // red is refilled
+    red[wave][lane] = acc;
+  }
+  __syncthreads();
+  if (which >= count || sub != 0) return;
+  f32x4 acc = red[wave][lane];
+  for (int w = 1; w < per; ++w) acc += red[wave + w][lane];
+  // row 4 h + i, component j0 + q
+  const bool last = blockIdx.x == gridDim.x - 1;
+  const float s = scale ? scale[a] : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!((members >> (4 * h + i)) & 1u)) continue;
+    const int64_t row = (int64_t)(m0 + 4 * h + i) * tr;
+    if (part != nullptr) {
+      part[(int64_t)blockIdx.z * M * tr + row + j0 + q] = acc[i];
+    } else {
+      t[row + j0 + q] = j0 + q < r ? (f16)(s * acc[i]) : (f16)0.0f;
+      if (last && j0 + 16 + q < tr) t[row + j0 + 16 + q] = (f16)0.0f;
+    }
   }
 }
 
-hipError_t launch_adapters_down(const uint16_t* x, int64_t M, int64_t K, const Adapters& ad, int64_t r, uint16_t* t,
-                                hipStream_t stream) {
-  const int tr = (int)((r + 31) / 32 * 32);
+// t from the partials of the chunks of K, in order; a thread for each value.
+__global__ void __launch_bounds__(256)
+adapters_finish_kernel(const float* __restrict__ part, int chunks, int M, const float* __restrict__ scale, int n, int r,
+                       const int32_t* __restrict__ adapter, f16* __restrict__ t, int tr) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)M * tr;
+  if (i >= all) return;
+  const int a = adapter[i / tr], c = (int)(i % tr);
+  if ((uint32_t)a >= (uint32_t)n) return;
+  float v = 0.0f;
+  if (c < r) {
+    for (int k = 0; k < chunks; k += 4) {
+      float p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = part[min(k + u, chunks - 1) * all + i];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v += k + u < chunks ? p[u] : 0.0f;
+    }
+    v *= scale ? scale[a] : 1.0f;
+  }
+  t[i] = (f16)v;
+}
+
+// Whether each row reads its adapter for itself: up to 64 MB in all, at worst from HBM. (The other kernel reads an adapter
+// once for 16 rows, but a wave alone reads it where they name many: in whole calls of 96 rows and 4096 x 4096, 16
+// components, 24 us where all rows name one adapter, 43 where each names its own.)
+static bool few_rows(int64_t M, int64_t K, int64_t r) { return M * r <= ((int64_t)1 << 25) / K; }
+static int64_t t_stride(int64_t r) { return (r + 31) / 32 * 32; }
+
+// Chunks of K (64 channels' multiples) that give half of the CUs a block, each at least 1024 channels.
+struct DownPlan {
+  int64_t chunk, chunks;
+};
+static DownPlan down_plan(int64_t M, int64_t K, int64_t r) {
+  const int64_t tiles = (M + 15) / 16 * ((r + 15) / 16), want = (128 + tiles - 1) / tiles, most = K / 1024;
+  int64_t chunks = want < most ? want : most;
+  chunks = chunks < 1 ? 1 : chunks;
+  const int64_t chunk = ((K + chunks - 1) / chunks + 63) / 64 * 64;
+  return DownPlan{chunk, (K + chunk - 1) / chunk};
+}
+
+constexpr int64_t kRowsPerLaunch = 65535 * 16;  // gridDim.y limit
+
+size_t adapters_partial_bytes(int64_t M, int64_t K, int64_t r) {
+  if (few_rows(M, K, r)) return 0;
+  size_t most = 0;
+  for (const int64_t rows : {M < kRowsPerLaunch ? M : kRowsPerLaunch, M % kRowsPerLaunch}) {
+    if (rows == 0) continue;
+    const DownPlan p = down_plan(rows, K, r);
+    const size_t b = p.chunks > 1 ? ((size_t)p.chunks * rows * t_stride(r) * 4 + 255) / 256 * 256 : 0;
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+hipError_t launch_adapters_down(const uint16_t* x, int64_t M, int64_t K, const Adapters& ad, int64_t r, float* part,
+                                uint16_t* t, hipStream_t stream) {
+  const int tr = (int)t_stride(r);
   const f16* L1 = reinterpret_cast<const f16*>(ad.L1);
-  constexpr int64_t kFew = 64;
-  if (M <= kFew) {
+  if (few_rows(M, K, r)) {
     int64_t w = (K / 128 + 7) / 8;  // about two steps of 512 channels a wave
     w = w < 1 ? 1 : (w > kDotWaves ? kDotWaves : w);
     if (M * tr <= 1024)
@@ -162,14 +226,22 @@ hipError_t launch_adapters_down(const uint16_t* x, int64_t M, int64_t K, const A
                          reinterpret_cast<f16*>(t), tr);
     return hipGetLastError();
   }
-  constexpr int64_t kRowsPerLaunch = 65535 * 16;  // gridDim.y limit
   for (int64_t m = 0; m < M; m += kRowsPerLaunch) {
     const int64_t mc = M - m < kRowsPerLaunch ? M - m : kRowsPerLaunch;
-    hipLaunchKernelGGL(adapters_down_kernel<16>, dim3((unsigned)(tr / 16), (unsigned)((mc + 15) / 16)),
+    const DownPlan p = down_plan(mc, K, r);
+    f16* tm = reinterpret_cast<f16*>(t) + m * tr;
+    hipLaunchKernelGGL(adapters_down_kernel, dim3((unsigned)((r + 15) / 16), (unsigned)((mc + 15) / 16),
+                                                  (unsigned)p.chunks),
                        dim3(64 * kRowWaves), 0, stream, reinterpret_cast<const f16*>(x) + m * K, (int)mc, (int)K, L1,
-                       ad.scale, (int)ad.n, (int)r, ad.row + m, reinterpret_cast<f16*>(t) + m * tr, tr);
-    const hipError_t e = hipGetLastError();
+                       ad.scale, (int)ad.n, (int)r, ad.row + m, tm, tr, (int)p.chunk, p.chunks > 1 ? part : nullptr);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (p.chunks > 1) {
+      hipLaunchKernelGGL(adapters_finish_kernel, dim3((unsigned)((mc * tr + 255) / 256)), dim3(256), 0, stream, part,
+                         (int)p.chunks, (int)mc, ad.scale, (int)ad.n, (int)r, ad.row + m, tm, tr);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   return hipSuccess;
 }

@@ -102,37 +102,66 @@ __device__ __forceinline__ void lowrank_add32(f32x16 (&acc)[MT][NT], const f16* 
 }
 
 // The same where each row names its own branch: subtile by subtile, for each adapter that its 32 rows name one product
-// of all of them, which its own rows keep (an adapter's infinities stay its own).
+// of all of them, which its own rows keep (an adapter's infinities stay its own). The K slices take the adapters in turn
+// (their partials are summed anyway). The loads of UN adapters go out together, with no branch between them: one after
+// another, 64 rows of as many adapters of rank 64 took 75 us at 8192 x 3584 instead of 25.
 template <int MT, int NT>
-__device__ __forceinline__ void adapters_add32(f32x16 (&acc)[MT][NT], const GemmArgs& a, int mbase, int nbase,
+__device__ __forceinline__ void adapters_add32(f32x16 (&acc)[MT][NT], const GemmArgs& a, int slice, int mbase, int nbase,
                                                int lane) {
+  constexpr int UN = MT * NT <= 4 ? 4 : 1;  // (128 rows a wave: prompts, with an adapter or two a subtile)
   const int h = lane >> 5, c32 = lane & 31, r = a.lr_r, tr = (r + 31) & ~31;
+  int turn = 0;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int m = mbase + 32 * i + c32;
     const int id = a.lr_row[min(m, a.M - 1)];
     uint32_t left = (uint32_t)__ballot(m < a.M && (uint32_t)id < (uint32_t)a.lr_n);
     const f16* ta = a.lr_t + (size_t)min(m, a.M - 1) * tr + 8 * h;
+    int ad = 0;
 #pragma unroll 1
     while (left != 0) {
-      const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-      const uint32_t members = (uint32_t)__ballot(id == ad) & left;
-      left &= ~members;
-      const uint32_t mine = members >> (4 * h);
+      uint32_t members[UN];
+      int ads[UN];
+#pragma unroll
+      for (int v = 0; v < UN; ++v) {  // the slice's next ones (none left: no rows)
+        members[v] = 0;
+        while (left != 0 && members[v] == 0) {
+          ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+          const uint32_t same = (uint32_t)__ballot(id == ad) & left;
+          left &= ~same;
+          members[v] = turn == slice ? same : 0;
+          turn = turn + 1 < a.ksplit ? turn + 1 : 0;
+        }
+        ads[v] = ad;
+      }
+      if (members[0] == 0) break;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const f16* ub = a.lr_up + ((size_t)ad * a.N + min(nbase + 32 * j + c32, a.N - 1)) * r;
-        f32x16 own = {};
+        const f16* up = a.lr_up + (size_t)min(nbase + 32 * j + c32, a.N - 1) * r;
 #pragma unroll 1
-        for (int s = 0; s < r; s += 16) {
-          const f16x8 av = as_f16x8(*reinterpret_cast<const uint4*>(ta + s));
-          uint4 b = *reinterpret_cast<const uint4*>(ub + min(s + 8 * h, r - 8));
-          if (s + 8 * h >= r) b = uint4{0, 0, 0, 0};
-          own = mfma_32x32x16(av, as_f16x8(b), own);
-        }
+        for (int s = 0; s < r; s += 32) {
+          uint4 av[2], bv[UN][2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] += (mine >> (8 * (e >> 2) + (e & 3))) & 1u ? own[e] : 0.0f;
-        __builtin_amdgcn_sched_barrier(0);
+          for (int u = 0; u < 2; ++u) {
+            av[u] = *reinterpret_cast<const uint4*>(ta + s + 16 * u);
+#pragma unroll
+            for (int v = 0; v < UN; ++v)
+              bv[v][u] = *reinterpret_cast<const uint4*>(up + (size_t)ads[v] * a.N * r + min(s + 16 * u + 8 * h, r - 8));
+          }
+#pragma unroll
+          for (int v = 0; v < UN; ++v) {
+            f32x16 own = {};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (s + 16 * u + 8 * h >= r) bv[v][u] = uint4{0, 0, 0, 0};
+              own = mfma_32x32x16(as_f16x8(av[u]), as_f16x8(bv[v][u]), own);
+            }
+            const uint32_t mine = members[v] >> (4 * h);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] += (mine >> (8 * (e >> 2) + (e & 3))) & 1u ? own[e] : 0.0f;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -411,7 +440,7 @@ gemm_kernel(GemmArgs a) {
   }
 
   if constexpr (AD) {
-    if (slice == 0) adapters_add32<MT, NT>(acc, a, m0 + wm * WTM, n0 + wn * WTN, lane);
+    adapters_add32<MT, NT>(acc, a, slice, m0 + wm * WTM, n0 + wn * WTN, lane);
   } else if (a.lr_r > 0 && slice == 0) {
     lowrank_add32<MT, NT>(acc, a.lr_t, a.lr_up, a.lr_r, M, N, m0 + wm * WTM, n0 + wn * WTN, lane);
   }
@@ -739,7 +768,7 @@ gemm_big_kernel(GemmArgs a) {
   }
 
   if constexpr (AD) {
-    if (slice == 0) adapters_add32<MT, NT>(acc, a, m0 + wm * WTM, n0 + wn * WTN, lane);
+    adapters_add32<MT, NT>(acc, a, slice, m0 + wm * WTM, n0 + wn * WTN, lane);
   } else if (a.lr_r > 0 && slice == 0) {
     lowrank_add32<MT, NT>(acc, a.lr_t, a.lr_up, a.lr_r, M, N, m0 + wm * WTM, n0 + wn * WTN, lane);
   }

@@ -414,6 +414,8 @@ gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restr
 
   // ---- prologue: staging loads, weight prefetch, staging stores
   // CSR bounds of the lane's row go out first: the wait on the staging loads covers them
+  int ad_row = -1;  // the adapter of row m0 + r
+  if constexpr (AD) ad_row = lr_row[min(m0 + r, M - 1)];
   int sp_e0 = 0, sp_e1 = 0;
   if constexpr (SP) {
     sp_e0 = row_ptr[n_ld] + wave;
@@ -623,7 +625,7 @@ gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restr
   // low-rank branch, once per output tile (wave 0, before the waves' sum)
   if constexpr (AD) {
     f32x4 a1[1] = {acc};
-    adapters_add16<KW, 1>(a1, lr_t, lr_up, lr_r, lr_row, lr_n, M, N, m0, n0, lane, wave);
+    adapters_add16<KW, 1>(a1, lr_t, lr_up, lr_r, ad_row, lr_n, M, N, m0, n0, lane, wave);
     acc = a1[0];
   } else if (lr_r > 0 && wave == 0) {
     f32x4 a1[1] = {acc};
@@ -685,6 +687,8 @@ gemv_ring_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __rest
 
   // CSR bounds of the lane's rows go out first: the wait on the staging loads covers
   // them (ragged N: a valid row is walked and never stored)
+  int ad_row = -1;  // the adapter of row m0 + r
+  if constexpr (AD) ad_row = lr_row[min(m0 + r, M - 1)];
   int sp_e0[NT], sp_e1[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
@@ -866,7 +870,7 @@ gemv_ring_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __rest
   }
   // low-rank branch, once per output tile (wave 0, before the waves' sum)
   if constexpr (AD)
-    adapters_add16<KW, NT>(acc, lr_t, lr_up, lr_r, lr_row, lr_n, M, N, m0, n0, lane, wave);
+    adapters_add16<KW, NT>(acc, lr_t, lr_up, lr_r, ad_row, lr_n, M, N, m0, n0, lane, wave);
   else if (lr_r > 0 && wave == 0)
     lowrank_add16<NT>(acc, lr_first, lr_t, lr_up, lr_r, M, N, m0, n0, lane);
   reduce_store_tiles<KW, NT>(acc, wave, lane, m0, mrows, n0 + r, N, y, y_f32);

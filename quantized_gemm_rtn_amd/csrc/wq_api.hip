@@ -356,8 +356,20 @@ size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64
   if (M < 1 || N < 1 || K < kGroup || K % kGroup != 0) return 0;
   if (N >= kMax32 / K || M >= kMax32 / K || M >= kMax32 / N) return 0;
   if (r < 8 || r % 8 != 0 || r > kMaxRank) return 0;
-  return lowrank_t_bytes(M, (r + 31) / 32 * 32) + wq::gemm_workspace_bytes(M, N, K);
+  return lowrank_t_bytes(M, (r + 31) / 32 * 32) + wq::adapters_partial_bytes(M, K, r) +
+         wq::gemm_workspace_bytes(M, N, K);
 }
+
+namespace {
+// The decode kernels read the weights once for each 16 rows; their waves share out a tile's adapters, where the GEMM's
+// take a column's one after another. In us, decode kernels / GEMM, all rows of one adapter of rank 16: 96 rows of
+// 4096 x 4096 24.5 / 37, of 12000 x 1408 34 / 41, 300 of 4000 x 1408 35 / 40, 64 of 8192 x 3584 26 / 23, of 11008 x 4096
+// 34 / 29, 300 of 4096 x 4096 52 / 39; each row its own: 64 rows of 8192 x 3584 31 / 38, of 11008 x 4096 40 / 40, 96 of it
+// 72 / 78, 300 of 4096 x 4096 75 / 75, of 8192 x 3584 125 / 107. (Of many adapters rows of a batch may still name one.)
+int adapters_auto_kernel(int64_t M, int64_t N, int64_t K, int64_t n_adapters) {
+  return (M + 15) / 16 * N * K <= (int64_t)1 << (n_adapters < 8 ? 27 : 28) ? WQ_KERNEL_GEMV : wq_auto_kernel(M, N, K);
+}
+}  // namespace
 
 int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed, const uint16_t* scales,
                        const uint16_t* zeros, int64_t N, int32_t group, const int32_t* row_ptr, const int32_t* col,
@@ -375,14 +387,15 @@ int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K, const uint32_t* 
   const size_t need = wq_linear_adapters_workspace_bytes(M, N, K, r);
   if (workspace == nullptr || workspace_bytes < need) return WQ_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
-  // workspace: t | the GEMM's split-K workspace
+  // workspace: t | the down-projection's partials | the GEMM's split-K workspace
   char* ws = static_cast<char*>(workspace);
-  const size_t t_bytes = lowrank_t_bytes(M, (r + 31) / 32 * 32);
   uint16_t* t = reinterpret_cast<uint16_t*>(ws);
-  if (kernel == WQ_KERNEL_AUTO) kernel = wq_auto_kernel(M, N, K);
+  float* part = reinterpret_cast<float*>(ws + lowrank_t_bytes(M, (r + 31) / 32 * 32));
+  const size_t t_bytes = lowrank_t_bytes(M, (r + 31) / 32 * 32) + wq::adapters_partial_bytes(M, K, r);
+  if (kernel == WQ_KERNEL_AUTO) kernel = adapters_auto_kernel(M, N, K, n_adapters);
   const int y_f32 = y_dtype == WQ_F32;
   const int32_t* rp = nnz > 0 ? row_ptr : nullptr;  // nnz == 0: no sparse term
-  hipError_t e = wq::launch_adapters_down(x, M, K, wq::Adapters{L1, adapter_scale, adapter, n_adapters}, r, t,
+  hipError_t e = wq::launch_adapters_down(x, M, K, wq::Adapters{L1, adapter_scale, adapter, n_adapters}, r, part, t,
                                           as_stream(stream));
   if (e != hipSuccess) return hip_status(e);
   const wq::LowRank lr{t, L2, r, adapter, n_adapters};

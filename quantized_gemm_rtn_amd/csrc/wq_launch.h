@@ -109,8 +109,9 @@ struct Adapters {
   const int32_t* row;
   int64_t n;
 };
-hipError_t launch_adapters_down(const uint16_t* x, int64_t M, int64_t K, const Adapters& ad, int64_t r, uint16_t* t,
-                                hipStream_t stream);
+size_t adapters_partial_bytes(int64_t M, int64_t K, int64_t r);  // of `part`: fp32 partials of K chunks
+hipError_t launch_adapters_down(const uint16_t* x, int64_t M, int64_t K, const Adapters& ad, int64_t r, float* part,
+                                uint16_t* t, hipStream_t stream);
 
 // Softmax of each row's logits ([M, E] fp16, or fp32) and its k largest.
 hipError_t launch_moe_route(const void* logits, int f32, int64_t M, int64_t E, int64_t k, int renormalize,

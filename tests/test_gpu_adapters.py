@@ -18,9 +18,12 @@ SHAPES = [
     (16, 1, 128, 8, 7, 0, "auto"), (33, 4097, 512, 64, 40, 0, "gemv"),
     (16, 300, 1024, 32, 9, 4, "gemm"), (40, 300, 1024, 64, 11, 4, "auto"), (64, 520, 2048, 200, 64, 0, "auto"),
     (65, 520, 2048, 16, 9, 0, "auto"),
-    (100, 300, 1152, 16, 30, 4, "auto"),  # tile GEMM
-    (130, 513, 384, 48, 3, 0, "auto"), (200, 256, 4096, 128, 12, 4, "auto"), (300, 300, 1152, 8, 300, 0, "auto"),
-    (70, 300, 1024, 56, 6, 4, "gemv"), (700, 270, 1024, 16, 5, 0, "auto"), (530, 1000, 8320, 24, 3, 0, "auto"),
+    (100, 300, 1152, 16, 30, 4, "gemm"),  # tile GEMM
+    (130, 513, 384, 48, 3, 0, "gemm"), (200, 256, 4096, 128, 12, 4, "gemm"), (300, 300, 1152, 8, 300, 0, "gemm"),
+    (70, 300, 1024, 56, 6, 4, "gemv"), (700, 270, 1024, 16, 5, 0, "gemm"), (530, 1000, 8320, 24, 3, 0, "gemm"),
+    (64, 520, 2048, 72, 64, 0, "gemm"), (40, 300, 1024, 64, 11, 4, "gemm"), (80, 64, 2176, 24, 80, 0, "auto"),
+    (300, 40, 8192, 24, 9, 0, "auto"), (131, 33, 16512, 40, 131, 0, "auto"),  # several chunks of K
+    (2100, 16, 2048, 8, 30, 0, "auto"), (400, 48, 1280, 80, 3, 4, "auto"),
 ]
 
 
@@ -54,7 +57,8 @@ def test_parity(gpu_lib, M, N, K, r, n, per_mille, kernel, kind):
 
 @pytest.mark.parametrize("M,N,K,r,n,kernel", [(1, 96, 512, 8, 2, "auto"), (7, 80, 1024, 24, 5, "auto"),
                                               (16, 64, 2048, 16, 20, "auto"), (60, 288, 1024, 32, 7, "gemm"),
-                                              (150, 256, 1024, 40, 9, "auto"), (90, 96, 384, 8, 90, "auto")])
+                                              (150, 256, 1024, 40, 9, "gemm"), (90, 96, 384, 8, 90, "gemm"),
+                                              (90, 96, 2048, 8, 90, "auto")])
 def test_integers_are_exact(gpu_lib, M, N, K, r, n, kernel):
     """Integer operands whose every sum float32 holds: fp32 outputs are the oracle's, bit for bit."""
     import torch
@@ -74,8 +78,8 @@ def test_integers_are_exact(gpu_lib, M, N, K, r, n, kernel):
     assert np.array_equal(y.cpu().numpy().astype(np.float64), ref)
 
 
-@pytest.mark.parametrize("M,kernel", [(1, "auto"), (2, "auto"), (16, "auto"), (48, "gemm"), (64, "auto"), (90, "auto"),
-                                      (300, "auto")])
+@pytest.mark.parametrize("M,kernel", [(1, "gemv_mfma"), (2, "gemv_mfma"), (16, "gemv_mfma"), (90, "gemv_mfma"),
+                                      (48, "gemm"), (64, "gemm"), (90, "gemm"), (300, "gemm")])
 def test_no_adapter_is_the_plain_product(gpu_lib, M, kernel):
     """Rows outside [0, n), of any value: the plain product's bits."""
     import torch
@@ -85,12 +89,13 @@ def test_no_adapter_is_the_plain_product(gpu_lib, M, kernel):
     L1, L2 = factors(1, n, r, N, K)
     D = layer_to_dev(L, torch)
     plain = gpu_lib.linear_sparse(to_dev(x, torch), D["packed"], D["scales"], D["zeros"], D["row_ptr"], D["col"],
-                                  D["val"], kernel="gemv_mfma" if kernel == "auto" and M <= 16 else kernel)
+                                  D["val"], kernel=kernel)
     out = np.resize(np.array([-1, n, -2 ** 31, 2 ** 31 - 1, 1 << 20], np.int64), M)
     assert torch.equal(run_adapters(gpu_lib, torch, L, x, L1, L2, out, kernel=kernel), plain)
 
 
-@pytest.mark.parametrize("M,kernel", [(2, "auto"), (16, "auto"), (40, "gemm"), (64, "auto"), (300, "auto")])
+@pytest.mark.parametrize("M,kernel", [(2, "auto"), (16, "auto"), (40, "gemm"), (64, "gemm"), (100, "auto"),
+                                      (300, "gemm")])
 def test_an_adapters_infinities_stay_its_own(gpu_lib, M, kernel):
     """Infinities and NaN in one adapter's factors, in its scale, or in one row: every other row is as it was."""
     import torch
