@@ -664,11 +664,19 @@ hipError_t launch_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int
 }
 
 // ---------------------------------------------------------------------------
-// Largest value over the wave's 64 lanes, in all of them.
+// Largest value over the wave's 64 lanes, as a scalar: inside rows of 16 lanes, then across them (lane exchanges that cost
+// a vector instruction each; through LDS, with the exponentials in every round, 8191 rows of 160 took 10.5 us, not 5).
 __device__ __forceinline__ int wave_max(int v) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) v = max(v, __shfl_xor(v, off));
-  return v;
+  const auto step = [&](auto ctrl, auto rows) {
+    v = max(v, __builtin_amdgcn_update_dpp(v, v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+  };
+  step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});  // row_shr 1, 2, 4, 8
+  step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row_bcast 15 into rows 1 and 3,
+  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // 31 into rows 2 and 3
+  return __builtin_amdgcn_readlane(v, 63);
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -706,8 +714,7 @@ moe_route_kernel(const T* __restrict__ logits, int M, int E, int k, int renormal
     x[v] = e < E ? (float)in[e] : -INFINITY;
     key[v] = logit_key(x[v]);
   }
-  float top = 0.0f, chosen = 0.0f, p = 0.0f;  // of lane j: the j-th choice's
-  int mine = -1;
+  int mine = -1, value = kMasked, first = kMasked;  // of lane j: the j-th choice, its key; the first one's
   for (int j = 0; j < k; ++j) {
     int best = key[0];
 #pragma unroll
@@ -723,22 +730,21 @@ moe_route_kernel(const T* __restrict__ logits, int M, int E, int k, int renormal
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = v == place ? kMasked : key[v];
     }
-    const float value = key_logit(most);
-    if (j == 0) top = value;
-    const float w = expf(value - top);
-    chosen += w;
+    first = j == 0 ? most : first;
     if (lane == j) {
       mine = e;
-      p = w;
+      value = most;
     }
   }
-  float total = chosen;
+  const float top = first == kMasked ? 0.0f : key_logit(first);
+  const float p = mine < 0 ? 0.0f : expf(key_logit(value) - top);
+  float total = p;
   if (!renormalize) {
     total = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) total += x[v] == -INFINITY ? 0.0f : expf(x[v] - top);
-    total = wave_sum(total);
   }
+  total = wave_sum(total);
   if (lane < k) {
     experts[(int64_t)row * k + lane] = mine;
     weights[(int64_t)row * k + lane] = mine < 0 ? 0.0f : p / total;
