@@ -24,8 +24,9 @@ constexpr int kMoePairs = 32;       // (row, expert) pairs of an item
 constexpr int kMoeFew = 4;          // rows of a batch up to which the kernels for few rows run
 constexpr int kMoeRowHalves = 136;  // of a staged row: 128 and padding (16 rows of a fragment in distinct banks)
 
-// What some rows of x have to do, from their experts: the active experts in ascending order, each with its (row,
-// expert) pairs, row * k + slot, in order. A row that names an expert twice has it once, with the weights' sum.
+// What some rows of x have to do, from their experts: the active experts, those of the most pairs first (so that items
+// dealt out in turn make equal sums), each with its (row, expert) pairs, row * k + slot, in order. A row that names an
+// expert twice has it once, with the weights' sum.
 struct MoeLists {
   int32_t active, pad[3];             // experts
   uint16_t expert[kMoeMaxPairs];      // of the i-th active one,
@@ -65,7 +66,7 @@ __device__ __forceinline__ int sum_upto_64(int v, int lane) {
 struct MoeScratch {
   int16_t ids[kMoeMaxPairs];
   int32_t count[kMoeMaxExperts];
-  int32_t sums[kMoeWaves];
+  int32_t sums[kMoeWaves][3];
 };
 __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeArgs& a, int m0, int rows) {
   constexpr int T = 64 * kMoeWaves, PER = kMoeMaxPairs / T, EPER = kMoeMaxExperts / T;
@@ -98,21 +99,32 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
 #pragma unroll
   for (int i = 0; i < PER; ++i) made[i] = place[i] >= 0 ? w.count[w.ids[t + T * i]] : 0;  // pairs of the pair's expert
   // experts EPER t .. + EPER - 1: pairs, tiles beyond an expert's first, and active ones, in one sum (11, 6 and 11 bits)
+  // for each class of experts: of more than 16 pairs, of more than 4, the others
   const auto packed = [](int n) { return n == 0 ? 0 : n | ((n - 1) / kMoePairs) << 11 | 1 << 17; };
-  int own[EPER], sum = 0;
+  const auto class_of = [](int n) { return n > 16 ? 0 : (n > 4 ? 1 : 2); };
+  int own[EPER], sum[3] = {0, 0, 0}, before[3];
 #pragma unroll
   for (int i = 0; i < EPER; ++i) {
     own[i] = w.count[EPER * t + i];
-    sum += packed(own[i]);
-  }
-  const int upto = sum_upto_64(sum, lane);
-  if (lane == 63) w.sums[wave] = upto;
-  __syncthreads();
-  int before = upto - sum, total = 0;
 #pragma unroll
-  for (int v = 0; v < kMoeWaves; ++v) {
-    before += v < wave ? w.sums[v] : 0;
-    total += w.sums[v];
+    for (int c = 0; c < 3; ++c) sum[c] += class_of(own[i]) == c ? packed(own[i]) : 0;
+  }
+#pragma unroll
+  for (int c = 0; c < 3; ++c) {
+    const int upto = sum_upto_64(sum[c], lane);
+    if (lane == 63) w.sums[wave][c] = upto;
+    before[c] = upto - sum[c];
+  }
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int c = 0; c < 3; ++c) {
+    before[c] += total;
+#pragma unroll
+    for (int v = 0; v < kMoeWaves; ++v) {
+      before[c] += v < wave ? w.sums[v][c] : 0;
+      total += w.sums[v][c];
+    }
   }
   const auto put = [&](int at, int v) {
     l.start[at] = (uint16_t)(v & 2047);
@@ -121,10 +133,14 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
 #pragma unroll
   for (int i = 0; i < EPER; ++i)
     if (own[i] > 0) {
-      l.expert[before >> 17] = (uint16_t)(EPER * t + i);
-      put(before >> 17, before);
-      w.count[EPER * t + i] = before & 2047;  // where its pairs begin
-      before += packed(own[i]);
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+        if (class_of(own[i]) == c) {
+          l.expert[before[c] >> 17] = (uint16_t)(EPER * t + i);
+          put(before[c] >> 17, before[c]);
+          w.count[EPER * t + i] = before[c] & 2047;  // where its pairs begin
+          before[c] += packed(own[i]);
+        }
     }
   if (t == 0) {
     l.active = total >> 17;
