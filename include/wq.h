@@ -284,8 +284,9 @@ int wq_linear_lowrank(const uint16_t* x, int64_t M, int64_t K,
 
 /* Bytes of device workspace wq_linear_adapters needs: t [M, r rounded up to 32] fp16, the
  * fp32 partials of the K chunks it may be summed over, and the split-K workspace of
- * wq_linear_workspace_bytes(M, N, K). 0 for invalid sizes (r must be a
- * multiple of 8 up to 256). */
+ * wq_linear_workspace_bytes(M, N, K). Fewer rows can need more (they split K further): a
+ * workspace for several batches has the largest of their needs. 0 for invalid sizes (r must
+ * be a multiple of 8 up to 256). */
 size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 
 /*
@@ -306,8 +307,8 @@ size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64
  *  MFMA decode kernel.
  *  workspace: required for M >= 1, 256-byte aligned, wq_linear_adapters_workspace_bytes bytes;
  *  contents on entry do not matter.
- * t = s x . L1^T is accumulated in fp32 and rounded once to fp16 (it is an MFMA operand);
- * each output tile adds t . L2^T to its fp32 accumulators before the one store of y. An
+ * t = s x . L1^T is accumulated in fp32 and rounded once to fp16 (it is an MFMA operand;
+ * beyond 65504 it is infinite); each output tile adds t . L2^T to its fp32 accumulators before the one store of y. An
  * adapter's infinities and NaN reach only the rows that name it. Deterministic.
  */
 int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K,
@@ -329,19 +330,20 @@ int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K,
  *           by their sum.
  *  experts  [M, top_k] int32 out, weights [M, top_k] float32 out; where fewer than top_k
  *           experts are not masked, the last ones are -1 with weight 0.
- * M * E below 2^31. E or top_k beyond their limits: WQ_ERR_UNSUPPORTED.
+ * M up to 2^25, M * E below 2^31. E or top_k beyond their limits: WQ_ERR_UNSUPPORTED.
  */
 int wq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int64_t E, int64_t top_k, int32_t renormalize,
                  int32_t* experts, float* weights, void* stream);
 
-/* Bytes of device workspace wq_moe_experts needs (the inner activations, and the lists of
- * each 64 rows). 0 for invalid sizes. */
+/* Bytes of device workspace wq_moe_experts needs (the inner activations, beyond 4 rows each
+ * (row, expert) pair's sums, and lists of the pairs). More rows never need less. 0 for invalid
+ * sizes. */
 size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t top_k);
 
 /*
- * wq_moe_experts - a mixture-of-experts layer of 4-bit matrices for a few tokens (each 64 rows
- * read the matrices of the experts they name once; a long prompt is better served by a product
- * for each expert):
+ * wq_moe_experts - a mixture-of-experts layer of 4-bit matrices for a few tokens (of each 192
+ * rows, 1024 / top_k if that is fewer, each 32 that name an expert read its matrices once; a long
+ * prompt is better served by a product for each expert):
  *   y[m] = sum over j of weights[m, j] ((silu(x[m] . G_e^T) * (x[m] . U_e^T)) . D_e^T),
  *   e = experts[m, j],  silu(a) = a / (1 + exp(-a)).
  *  x        [M, H] fp16, 16-byte aligned.
@@ -354,11 +356,12 @@ size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t t
  *  H, I     multiples of 128 up to 65536, 2 H I below 2^31; M up to 65535 * 64, M * H below 2^31.
  *  group    128.   y  [M, H] out, fp16 or float32 (y_dtype), 4-byte aligned.
  *  workspace: required for M >= 1, 256-byte aligned, wq_moe_experts_workspace_bytes bytes;
- *  contents on entry do not matter.
+ *  contents on entry do not matter. It holds lists between the call's launches: calls that may
+ *  run at once (other streams, captured graphs) need one each.
  * Sums are fp32; the inner activations silu(..) * (..) are rounded once to fp16, an MFMA
- * operand (beyond 65504 they are infinite), y once. Two launches for up to 4 rows, else three. Deterministic: a fixed
- * order for the same experts (other rows in the batch may split a row's sums elsewhere, and so
- * round its last bits otherwise; their values never reach it).
+ * operand (beyond 65504 they are infinite), y once. Two launches for up to 4 rows, else three.
+ * Deterministic: a fixed order for the same experts (other rows in the batch may split a row's
+ * sums elsewhere, and so round its last bits otherwise; their values never reach it).
  */
 int wq_moe_experts(const uint16_t* x, int64_t M, int64_t H, const int32_t* experts, const float* weights,
                    int64_t top_k, int64_t E, const uint32_t* gate_up, const uint16_t* gate_up_scales,

@@ -27,7 +27,8 @@ constexpr int64_t kMaxAdapters = (int64_t)1 << 20;
 constexpr int64_t kMaxExperts = 1024;         // of a mixture-of-experts layer,
 constexpr int64_t kMaxTopK = 16;              // and of a row
 constexpr int64_t kMaxMoeWidth = 65536;       // channels: a few rows' offsets stay within 32 bits
-constexpr int64_t kMaxMoeRows = 65535 * 64;   // 64 rows a block, the grid's limit
+constexpr int64_t kMaxMoeRows = 65535 * 64;   // at least 64 rows a block, the grid's limit
+constexpr int64_t kMaxRouteRows = (int64_t)1 << 25;  // four a block of 256 threads: a grid has below 2^32
 constexpr int64_t kMaxOutliers = 16;          // fp16 outlier channels of the W4A8 product
 
 // t [M][r] fp16 of the low-rank branch, at the start of its workspace
@@ -412,7 +413,7 @@ int wq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int64_t E,
   if (M != 0 && (!logits || !experts || !weights)) return WQ_ERR_NULL;
   if (logits_dtype != WQ_F16 && logits_dtype != WQ_F32) return WQ_ERR_UNSUPPORTED;
   if (E > kMaxExperts || top_k > kMaxTopK) return WQ_ERR_UNSUPPORTED;
-  if (M < 0 || E < 1 || top_k < 1 || top_k > E || M >= kMax32 / E) return WQ_ERR_SHAPE;
+  if (M < 0 || M > kMaxRouteRows || E < 1 || top_k < 1 || top_k > E || M >= kMax32 / E) return WQ_ERR_SHAPE;
   if (!aligned(logits, logits_dtype == WQ_F32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4))
     return WQ_ERR_ALIGN;
   if (M == 0) return WQ_OK;

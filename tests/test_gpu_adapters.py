@@ -126,6 +126,65 @@ def test_an_adapters_infinities_stay_its_own(gpu_lib, M, kernel):
         assert not torch.isfinite(y[~keep].float()).all(), which
 
 
+@pytest.mark.parametrize("M,K", [(3, 512), (40, 1024), (300, 8192), (700, 2048)])
+def test_subnormal_inputs_and_factors(gpu_lib, M, K):
+    """fp16 values below 2^-14 count as all others do, in x and in L1 (t itself is brought back by the scale)."""
+    import torch
+    say(f"[adapters subnormal] M={M} K={K}")
+    N, n, r = 64, 4, 24
+    L = layer(11, N, K)
+    rng = np.random.default_rng(M)
+    L1, L2 = factors(5, n, r, N, K)
+    ids = rng.integers(0, n, M)
+    small = np.ldexp(rng.integers(-1023, 1024, (M, K)), -24).astype(np.float16)
+    scale = np.full(n, 2.0 ** 14, np.float32)
+    for x, a1 in ((small, L1), (workloads.random_x(M, M, K), np.ldexp(rng.integers(-1023, 1024, L1.shape), -24).astype(np.float16))):
+        y = run_adapters(gpu_lib, torch, L, x, a1, L2, ids, scale, out_dtype=torch.float32)
+        ref, bound = oracle.rows.linear_adapters(x, L["held"], a1, L2, ids, scale, rounded_weights=True)
+        assert worst(y, ref, bound, f16=False) <= 1.0
+
+
+def test_outputs_of_any_place(gpu_lib):
+    """An output that begins four bytes into its memory, the bytes around it as they were."""
+    import torch
+    L1, L2 = factors(6, 3, 16, 48, 512)
+    L = layer(12, 48, 512)
+    for M in (1, 5, 16, 70):
+        say(f"[adapters place] M={M}")
+        x, ids = workloads.random_x(M, M, 512), np.arange(M) % 4 - 1
+        for dtype, lead in ((torch.float32, 1), (torch.float16, 2)):
+            want = run_adapters(gpu_lib, torch, L, x, L1, L2, ids, out_dtype=dtype)
+            room = torch.full((M * 48 + 2 * lead,), 7.0, dtype=dtype, device="cuda")
+            out = room[lead:-lead].view(M, 48)
+            run_adapters(gpu_lib, torch, L, x, L1, L2, ids, out_dtype=dtype, out=out)
+            assert torch.equal(out, want) and (room[:lead] == 7).all() and (room[-lead:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [2, 64, 200])
+def test_factors_beyond_32_bits(gpu_lib, M):
+    """The last adapters of arrays of more than 2^32 bytes (and 2^31 elements)."""
+    import torch
+    N, K, n, r = 20480, 20480, 1700, 64
+    say(f"[adapters far] M={M}")
+    x = workloads.random_x(M, M, K)
+    far = [0, n // 2, n - 2, n - 1]
+    small1, small2 = factors(7, len(far), r, N, K)
+    L1 = torch.empty(n, r, K, dtype=torch.float16, device="cuda")
+    L2 = torch.empty(n, N, r, dtype=torch.float16, device="cuda")
+    assert L1.numel() > 2 ** 31 and L2.numel() > 2 ** 31
+    small1, small2 = to_dev(small1, torch), to_dev(small2, torch)
+    for i, a in enumerate(far):
+        L1[a], L2[a] = small1[i], small2[i]
+    which = torch.arange(M, device="cuda") % len(far)
+    packed = torch.zeros(N, K // 8, dtype=torch.int32, device="cuda")  # codes 0 of zero-point 0: no weights
+    s = torch.ones(N, K // 128, dtype=torch.float16, device="cuda")
+    xd = to_dev(x, torch)
+    args = xd, packed, s, torch.zeros_like(s)
+    y = gpu_lib.linear_adapters(*args, L1, L2, torch.tensor(far, device="cuda")[which].int())
+    assert torch.equal(y, gpu_lib.linear_adapters(*args, small1, small2, which.int()))
+    assert torch.isfinite(y.float()).all() and y.any(1).all()
+
+
 def test_rows_do_not_depend_on_their_neighbours_or_order(gpu_lib):
     """A permuted batch gives the permuted rows, whichever adapters then share a tile."""
     import torch

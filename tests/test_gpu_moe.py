@@ -5,8 +5,8 @@ import pytest
 
 import oracle
 import workloads
-from gpu_cases import say, to_dev
-from rows_cases import Moe, worst
+from gpu_cases import layer_to_dev, say, to_dev
+from rows_cases import Moe, factors, layer, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -169,6 +169,69 @@ def test_large_batches_of_small_layers(gpu_lib):
     assert worst(moe.run(gpu_lib, torch, x, e, w), ref, bound) <= 1.0
 
 
+@pytest.mark.parametrize("M", [2, 9, 60, 200])
+def test_weights_beyond_32_bits(gpu_lib, M):
+    """The last experts of arrays of more than 2^32 bytes, in turn with the first: the bits of a layer of just those."""
+    import torch
+    say(f"[experts far] M={M}")
+    H, I, E, k = 4096, 2048, 1024, 2
+    moe = Moe(torch, 8, 256, 128, 4)  # (of this size: its words fill the large arrays' rows again and again)
+    far = torch.tensor([0, E // 2, E - 2, E - 1], device="cuda")
+    big, small = [], []
+    for i, shape in enumerate([(E, 2 * I, H // 8), (E, 2 * I, H // 128), (E, 2 * I, H // 128),
+                               (E, H, I // 8), (E, H, I // 128), (E, H, I // 128)]):
+        src = moe.args[i].flatten()
+        t = torch.empty(shape, dtype=src.dtype, device="cuda")
+        n = t[0].numel()
+        own = torch.stack([src.roll(j).repeat(-(-n // src.numel()))[:n].view(shape[1:]) for j in range(4)])
+        for j in range(4):
+            t[far[j].item()] = own[j]
+        big.append(t)
+        small.append(own)
+    assert big[0].numel() * 4 > 2 ** 32 and big[3].numel() * 4 >= 2 ** 32
+    rng = np.random.default_rng(M)
+    x = to_dev((workloads.random_x(M, M, H).astype(np.float32) / 64).astype(np.float16), torch)
+    e, w = _pick(rng, M, 4, k, none=0.0)
+    w = to_dev(w, torch)
+    want = gpu_lib.moe_experts(x, to_dev(e, torch), w, *small)
+    got = gpu_lib.moe_experts(x, to_dev(far.cpu().numpy().astype(np.int32)[e], torch), w, *big)
+    assert torch.isfinite(want.float()).all() and want.any(1).all()
+    assert torch.equal(got, want)
+
+
+def test_subnormal_inputs(gpu_lib):
+    """fp16 values below 2^-14 in x count as all others do, and the inner activations of such sizes keep theirs."""
+    import torch
+    H, I, E, k = 256, 128, 3, 2
+    moe = Moe(torch, 10, H, I, E)
+    rng = np.random.default_rng(2)
+    for M in (2, 12, 60):
+        say(f"[experts subnormal] M={M}")
+        x = np.ldexp(rng.integers(-1023, 1024, (M, H)), -24).astype(np.float16)
+        x[M // 2:] = np.ldexp(rng.integers(-1023, 1024, (M - M // 2, H)), -18).astype(np.float16)
+        e, w = _pick(rng, M, E, k, none=0.0)
+        ref, bound = moe.reference(x, e, w)
+        assert worst(moe.run(gpu_lib, torch, x, e, w, out_dtype=torch.float32), ref, bound, f16=False) <= 1.0
+
+
+def test_outputs_of_any_place(gpu_lib):
+    """An output that begins four bytes into its memory, the bytes around it as they were."""
+    import torch
+    H, I, E, k = 384, 128, 5, 2
+    moe = Moe(torch, 11, H, I, E)
+    rng = np.random.default_rng(3)
+    for M in (1, 4, 5, 33):
+        say(f"[experts place] M={M}")
+        x = workloads.random_x(M, M, H)
+        e, w = _pick(rng, M, E, k)
+        for dtype, lead in ((torch.float32, 1), (torch.float16, 2)):
+            want = moe.run(gpu_lib, torch, x, e, w, out_dtype=dtype)
+            room = torch.full((M * H + 2 * lead,), 7.0, dtype=dtype, device="cuda")
+            out = room[lead:-lead].view(M, H)
+            moe.run(gpu_lib, torch, x, e, w, out_dtype=dtype, out=out)
+            assert torch.equal(out, want) and (room[:lead] == 7).all() and (room[-lead:] == 7).all()
+
+
 def test_layer_from_logits_in_a_graph(gpu_lib):
     """Route and experts captured together and replayed on other inputs, eager work between; two streams at once with
     workspaces of their own."""
@@ -214,6 +277,54 @@ def test_layer_from_logits_in_a_graph(gpu_lib):
     step(out, ws[0])
     torch.cuda.synchronize()
     assert torch.equal(out, got) and torch.equal(other, got)
+
+
+@pytest.mark.parametrize("M", [1, 4, 14, 90])
+def test_a_layer_with_adapters_and_experts(gpu_lib, M):
+    """A decoder block's second half as it is served: a 4-bit projection with each request's adapter, a router's logits
+    by another 4-bit layer, the choice, the experts; each step against the oracle on the step before's outputs, and the
+    whole in a graph, replayed on other inputs with eager work between."""
+    import torch
+    say(f"[block] M={M}")
+    K, H, I, E, k, n, r = 512, 256, 384, 16, 4, 5, 16
+    proj, router = layer(20, H, K, 4), layer(21, E, H, 0, 0.2)
+    P, R = layer_to_dev(proj, torch), layer_to_dev(router, torch)
+    moe = Moe(torch, 12, H, I, E)
+    L1, L2 = factors(13, n, r, H, K)
+    d1, d2 = to_dev(L1, torch), to_dev(L2, torch)
+    x = torch.zeros(M, K, dtype=torch.float16, device="cuda")
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+
+    def step():
+        h = gpu_lib.linear_adapters(x, P["packed"], P["scales"], P["zeros"], d1, d2, ids, None, P["row_ptr"], P["col"],
+                                    P["val"])
+        logits = gpu_lib.linear(h, R["packed"], R["scales"], R["zeros"], out_dtype=torch.float32)
+        experts, weights = gpu_lib.moe_route(logits, k)
+        return h, logits, experts, weights, gpu_lib.moe_experts(h, experts, weights, *moe.args)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    rng = np.random.default_rng(M)
+    for i in range(3):
+        xs, a = workloads.random_x(i, M, K), rng.integers(-1, n, M)
+        x.copy_(to_dev(xs, torch))
+        ids.copy_(to_dev(a.astype(np.int32), torch))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        assert all(torch.equal(g, t) for g, t in zip(got, step())), i
+        h, logits, e, w, y = (t.cpu().numpy() for t in got)
+        ref, bound = oracle.rows.linear_adapters(xs, proj["held"], L1, L2, a, rounded_weights=True)
+        assert worst(got[0], ref, bound) <= 1.0
+        _check_route((e, w.astype(np.float64)), logits, k, True)
+        ref, bound = moe.reference(h, e, w)
+        assert worst(got[4], ref, bound) <= 1.0
 
 
 def test_empty_batches_and_refusals(gpu_lib):

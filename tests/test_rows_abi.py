@@ -52,7 +52,7 @@ def route(lib, logits=A, dtype=1, M=4, E=8, k=2, renorm=1, experts=A, weights=A)
 @pytest.mark.parametrize("kw,status", [
     (dict(logits=None), -1), (dict(experts=None), -1), (dict(weights=None), -1), (dict(dtype=2), -4),
     (dict(E=1025), -4), (dict(k=17, E=20), -4), (dict(E=0), -2), (dict(k=0), -2), (dict(k=9), -2), (dict(M=-1), -2),
-    (dict(M=1 << 28), -2), (dict(logits=ODD), -3), (dict(logits=BYTE, dtype=0), -3), (dict(experts=ODD), -3),
+    (dict(M=1 << 28), -2), (dict(M=(1 << 25) + 1, E=1, k=1), -2), (dict(logits=ODD), -3), (dict(logits=BYTE, dtype=0), -3), (dict(experts=ODD), -3),
     (dict(weights=ODD), -3), (dict(M=0, logits=None, experts=None, weights=None), 0),
 ])
 def test_route_validation(lib, kw, status):  # noqa: F811
@@ -82,7 +82,7 @@ def test_experts_validation(lib, kw, status):  # noqa: F811
 def test_experts_workspace(lib):  # noqa: F811
     f = lib.wq_moe_experts_workspace_bytes
     last = 0
-    for M in (1, 2, 64, 65, 1000):
+    for M in range(1, 1000):
         n = f(M, 256, 384, 2)
         assert n >= M * 2 * 384 * 2 and n >= last
         last = n
