@@ -269,6 +269,7 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
   const uint32_t magic = magic_1024x2();
   const f16* frag = slot + min(r, 4 * XL - 1) * kMoeRowHalves + 32 * h;
   const int last = g0 + ng - 1;
+  constexpr int P = D >= 4 ? 2 : 1;
   uint4 wbuf[D][NW], xbuf[D][XL];
   uint4 s8, z8;
   int off;
@@ -286,16 +287,20 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
       if (i >= off) table[(i - off) * 16 * NW + h % NW * 16 + r] = as_u32(f16x2{s[i], (f16)((f16)1024.0f + z[i])});
     __builtin_amdgcn_wave_barrier();
   };
-  const auto fetch = [&](int i, int g) {
+  const auto fetch_w = [&](int i, int g) {
 #pragma unroll
     for (int j = 0; j < NW; ++j) wbuf[i][j] = *reinterpret_cast<const uint4*>(tiles.w[j] + 64 * g + tiles.w_off);
+  };
+  const auto fetch_x = [&](int i, int g) {
 #pragma unroll
     for (int j = 0; j < XL; ++j) xbuf[i][j] = *reinterpret_cast<const uint4*>(xs + 256 * g + xo[j]);
   };
-  const auto group = [&](int i, int u) {  // slot i, u-th of its unit
+  const auto group = [&](int u, int g) {  // the unit's u-th, group g
+    const int i = u % D;
 #pragma unroll
     for (int j = 0; j < XL; ++j)
       *reinterpret_cast<uint4*>(slot + (h + 4 * j) * kMoeRowHalves + 8 * r) = PERM ? perm_x8(xbuf[i][j]) : xbuf[i][j];
+    if (MT == 1) fetch_x(i, min(g + D, last));  // (of two tiles all, they would spill)
     uint4 xa[MT][4];
     uint32_t sz[NW];
 #pragma unroll
@@ -325,15 +330,23 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
   };
   fetch_sz(g0);
 #pragma unroll
-  for (int i = 0; i < D; ++i) fetch(i, min(g0 + i, last));
+  for (int i = 0; i < D; ++i) {
+    fetch_w(i, min(g0 + i, last));
+    fetch_x(i, min(g0 + i, last));
+  }
   int g = g0;
   for (; g + kMoeUnit <= last; g += kMoeUnit) {  // (a unit with another after it is whole)
     put_sz();
     fetch_sz(g + kMoeUnit);
 #pragma unroll
-    for (int u = 0; u < kMoeUnit; ++u) {
-      group(u % D, u);
-      fetch(u % D, min(g + u + D, last));
+    for (int u = 0; u < kMoeUnit; u += P) {
+#pragma unroll
+      for (int v = 0; v < P; ++v) group(u + v, g + u + v);
+#pragma unroll
+      for (int v = 0; v < P; ++v) {
+        fetch_w((u + v) % D, min(g + u + v + D, last));
+        if (MT > 1) fetch_x((u + v) % D, min(g + u + v + D, last));
+      }
       __builtin_amdgcn_sched_barrier(kSchedKeepGroups);  // the refill stays next to its consumption
     }
   }
@@ -341,9 +354,12 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
 #pragma unroll
   for (int u = 0; u < kMoeUnit; ++u) {
     if (g + u <= last) {
-      group(u % D, u);
+      group(u, g + u);
       if constexpr (D < kMoeUnit)
-        if (u + D < kMoeUnit) fetch(u % D, min(g + u + D, last));
+        if (u + D < kMoeUnit) {
+          fetch_w(u % D, min(g + u + D, last));
+          if (MT > 1) fetch_x(u % D, min(g + u + D, last));
+        }
     }
     __builtin_amdgcn_sched_barrier(kSchedKeepGroups);
   }
@@ -426,7 +442,8 @@ moe_rows_kernel(MoeArgs a) {
   const int K = UP ? a.H : a.I, N = UP ? a.I : a.H;
   constexpr int CH = UP ? 8 * NW : 16 * NW;  // channels of an item
   const int G = K >> 7, C = N / CH;
-  // items: (expert, channels, pairs), the pairs fastest
+  // items: (expert, eight channel places, pairs, one of the eight places): those that read the same weights are eight
+  // apart, blocks of one XCD, so that its L2 reads them once
   // (32 bits hold 1024 tiles of 2048 channels' items, and a block's groups: 64-bit divisions took 1 us here)
   const uint32_t items = (uint32_t)l.tile[active] * C, nb = gridDim.x;
   const uint32_t mine = items > blockIdx.x ? (items - blockIdx.x + nb - 1) / nb : 0;  // blockIdx.x, blockIdx.x + nb, ..
@@ -446,9 +463,14 @@ moe_rows_kernel(MoeArgs a) {
     const int before = __builtin_amdgcn_readfirstlane(l.tile[it.which]);
     const int n_tiles = __builtin_amdgcn_readfirstlane(l.tile[it.which + 1]) - before;
     const int rem = (int)item - before * C;
-    const int c = n_tiles == 1 ? rem : rem / n_tiles;
+    int c = rem, tile = 0;
+    if (n_tiles > 1) {
+      const int c8 = rem / (8 * n_tiles) * 8, n = min(8, C - c8), in = rem - c8 * n_tiles;
+      tile = in / n;
+      c = c8 + in - tile * n;
+    }
     it.c0 = CH * c;
-    it.first = __builtin_amdgcn_readfirstlane(l.start[it.which]) + kMoePairs * (rem - c * n_tiles);
+    it.first = __builtin_amdgcn_readfirstlane(l.start[it.which]) + kMoePairs * tile;
     it.count = min(kMoePairs, __builtin_amdgcn_readfirstlane(l.start[it.which + 1]) - it.first);
     MoeTiles<NW> tiles;
     int n[NW];
