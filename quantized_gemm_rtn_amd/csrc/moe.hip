@@ -4,13 +4,28 @@
 //   experts:  y = sum over the row's experts e of w_e ((silu(x G_e^T) * (x U_e^T)) D_e^T),
 //             silu(a) = a / (1 + exp(-a)), every matrix in 4 bits with (s, z) per 128 channels
 //
-// moe_up_kernel    one block for each active expert and 16 channels of its inner dimension: the
-//   16 rows of G_e and of U_e, four waves splitting K, for all rows of x that name the expert.
-//   h = silu(gate) * up is rounded once to fp16, the operand of the second product, and written
-//   in the order that product's lanes read it.
-// moe_down_kernel  one block for each 16 channels of the output: the 16 rows of D_e of every
-//   active expert, one after the other, dealt out in equal shares to the block's waves, so the
-//   sum over experts never leaves the block.
+// The layer's bound is the bytes of the experts that rows name: 9/16 of a byte a weight, read once for each 32 rows of an
+// expert (a copy of 2 + 2 GiB runs at 4.95 TB/s on this card; the floors below are at that rate).
+//
+// moe_rows_kernel     Both products, G_e and U_e together and then D_e. The work is items, (an expert, 64 rows of its
+//   weights, up to 32 of its (row, expert) pairs), dealt in turn to one block of eight waves a CU; a block's groups of 128
+//   channels are cut into equal shares for its waves, wherever an item begins or ends, and what waves share of an item is
+//   summed through LDS in the order of the waves. So all CUs have the same bytes to read, for any experts and sizes: one
+//   block for an expert and 16 channels took 403 us where 16 rows name eight experts of 4096 x 14336, this split 174
+//   (floor 151). Rows of x pass through a slot of LDS of the wave's own, which orders them as the matrix operand; nothing
+//   in the loop waits for another wave. The lists of who needs what are made by every block of the first product for itself
+//   (a launch of their own would be another wait for the whole card), and left for the second.
+//   h = silu(gate) * up is rounded once to fp16, the operand of the second product, and written in the order that
+//   product's lanes read it. The second product leaves each pair's sums in fp32, which moe_join_kernel weights and adds
+//   in the order of the row's slots.
+// moe_down_few_kernel The second product and the join for up to 4 rows: one block for 16 channels of the output, all
+//   experts' groups shared out among its waves, each with its sums in LDS: no third launch (one token of two experts of
+//   4096 x 14336: 31 + 17 us, 5.1 TB/s besides some 5 us a launch to begin and end; floor 38).
+//
+// What holds the large batches back (150 rows of four of 32 experts of 4096 x 1536: 79 + 45 + 5 us, floor 65) is the path
+// for 17 to 32 pairs: 3 TB/s of weights where up to 4 pairs run at 4.5. Neither its vector instructions (28 us of the 79 on
+// each SIMD), its matrix instructions (8 us), the rows of x that it reads nor the order of its instructions is the bound:
+// changing each made no difference. Cutting the shares by cost instead of by groups was slower (batch of 16: 193 us).
 #include "gemv_kernels.h"
 
 namespace wq {
@@ -259,7 +274,8 @@ struct __attribute__((packed, aligned(2))) EightHalves {
 // acc[i][j] += x . w[j]^T over groups g0 .. g0 + ng - 1, for 16 MT rows of x and NW tiles of
 // weights, by one wave: D groups are in flight; each group's rows of x pass through the wave's slot of LDS into the
 // order of the product's operand (4 XL rows; PERM: reordered to the codes' on the way), and a unit's (s, 1024 + z)
-// through its table, loaded a tile for each 16 lanes, eight groups at once at any alignment.
+// through its table, loaded a tile for each 16 lanes, eight groups at once at any alignment. Two groups' weights, the
+// halves of 128-byte lines, are asked for together (apart: 2 us more of 130).
 //  xs + xo[j] bytes: the lane's eight channels of group 0 of row lane / 16 + 4 j.
 template <int MT, int NW, int XL, int D, bool PERM>
 __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<NW>& tiles, const uint8_t* xs,
@@ -269,7 +285,7 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
   const uint32_t magic = magic_1024x2();
   const f16* frag = slot + min(r, 4 * XL - 1) * kMoeRowHalves + 32 * h;
   const int last = g0 + ng - 1;
-  constexpr int P = D >= 4 ? 2 : 1;
+  constexpr int P = D >= 4 ? 2 : 1;  // groups whose weights are asked for together
   uint4 wbuf[D][NW], xbuf[D][XL];
   uint4 s8, z8;
   int off;
@@ -414,7 +430,8 @@ struct MoeRowsLds {
 
 // One of the layer's two products, for all pairs: items dealt in turn to one block a CU, a block's groups (G an item)
 // in equal shares for its waves; what waves share of an item they join through LDS.
-// FEW: batches of up to kMoeFew rows, none of whose items has more pairs.
+// FEW: batches of up to kMoeFew rows, none of whose items has more pairs: 32 rows of weights an item and eight groups in
+// flight, since an item's rows of x are few.
 template <bool UP, bool FEW>
 __global__ void __launch_bounds__(64 * kMoeWaves)
 moe_rows_kernel(MoeArgs a) {
