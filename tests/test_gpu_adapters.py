@@ -126,6 +126,25 @@ def test_an_adapters_infinities_stay_its_own(gpu_lib, M, kernel):
         assert not torch.isfinite(y[~keep].float()).all(), which
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_drawn_sizes(gpu_lib, seed):
+    import torch
+    rng = np.random.default_rng(200 + seed)
+    M, N = int(np.exp(rng.uniform(0, np.log(600)))), int(np.exp(rng.uniform(0, np.log(1500))))
+    K, r, n = 128 * int(rng.integers(1, 34)), 8 * int(rng.integers(1, 33)), int(np.exp(rng.uniform(0, np.log(60))))
+    kind, kernel = rng.choice(["any", "runs", "one"]), rng.choice(["auto", "auto", "gemv", "gemm"])
+    per_mille = int(rng.choice([0, 0, 4]))
+    say(f"[adapters drawn] M={M} N={N} K={K} r={r} n={n} sparse={per_mille} kernel={kernel} rows={kind}")
+    L = layer(300 + seed, N, K, per_mille)
+    x = workloads.random_x(seed, M, K)
+    L1, L2 = factors(seed, n, r, N, K)
+    ids, scale = _rows(rng, M, n, kind), rng.uniform(-2.0, 2.0, n).astype(np.float32)
+    y = run_adapters(gpu_lib, torch, L, x, L1, L2, ids, scale, kernel=str(kernel))
+    ref, bound = oracle.rows.linear_adapters(x, L["held"], L1, L2, ids, scale, rounded_weights=True)
+    assert worst(y, ref, bound) <= 1.0
+    assert torch.equal(run_adapters(gpu_lib, torch, L, x, L1, L2, ids, scale, kernel=str(kernel)), y)
+
+
 @pytest.mark.parametrize("M,K", [(3, 512), (40, 1024), (300, 8192), (700, 2048)])
 def test_subnormal_inputs_and_factors(gpu_lib, M, K):
     """fp16 values below 2^-14 count as all others do, in x and in L1 (t itself is brought back by the scale)."""
@@ -142,6 +161,23 @@ def test_subnormal_inputs_and_factors(gpu_lib, M, K):
         y = run_adapters(gpu_lib, torch, L, x, a1, L2, ids, scale, out_dtype=torch.float32)
         ref, bound = oracle.rows.linear_adapters(x, L["held"], a1, L2, ids, scale, rounded_weights=True)
         assert worst(y, ref, bound, f16=False) <= 1.0
+
+
+@pytest.mark.parametrize("M,K,kernel", [(1, 512, "auto"), (9, 512, "auto"), (60, 1024, "gemm"), (60, 1024, "gemv"),
+                                        (500, 8192, "auto")])
+def test_workspaces_of_any_contents(gpu_lib, M, K, kernel):
+    """A workspace of NaN gives the same bits, also where rows, or all of them, name no adapter."""
+    import torch
+    say(f"[adapters workspace] M={M} K={K}")
+    N, n, r = 80, 5, 40
+    L = layer(13, N, K)
+    L1, L2 = factors(8, n, r, N, K)
+    x = workloads.random_x(M, M, K)
+    for ids in (np.arange(M) % n, np.arange(M) % (n + 2) - 1, np.full(M, -1)):
+        want = run_adapters(gpu_lib, torch, L, x, L1, L2, ids, kernel=kernel)
+        assert torch.isfinite(want.float()).all()
+        ws = torch.full((gpu_lib.linear_adapters_workspace_bytes(M, N, K, r),), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(run_adapters(gpu_lib, torch, L, x, L1, L2, ids, kernel=kernel, workspace=ws), want)
 
 
 def test_outputs_of_any_place(gpu_lib):

@@ -232,6 +232,47 @@ def test_outputs_of_any_place(gpu_lib):
             assert torch.equal(out, want) and (room[:lead] == 7).all() and (room[-lead:] == 7).all()
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_sizes(gpu_lib, seed):
+    """Rows up to three blocks of the lists, experts that many rows name and that none does."""
+    import torch
+    rng = np.random.default_rng(100 + seed)
+    H, I = (128 * int(rng.integers(1, 6)) for _ in range(2))
+    E, k = int(rng.integers(1, 25)), int(rng.integers(1, 9))
+    k = min(k, E)
+    M = int(np.exp(rng.uniform(0, np.log(500))))
+    say(f"[experts drawn] M={M} H={H} I={I} E={E} k={k}")
+    moe = Moe(torch, 30 + seed, H, I, E)
+    x = workloads.random_x(seed, M, H)
+    p = rng.dirichlet(np.full(E, 0.5)) + 1e-3
+    e = np.array([rng.choice(E, k, replace=False, p=p / p.sum()) for _ in range(M)]).reshape(M, k)
+    e[rng.random((M, k)) < 0.05] = -1
+    w = rng.uniform(-1, 1, (M, k)).astype(np.float32)
+    ref, bound = moe.reference(x, e, w)
+    y = moe.run(gpu_lib, torch, x, e, w)
+    assert worst(y, ref, bound) <= 1.0
+    assert torch.equal(moe.run(gpu_lib, torch, x, e, w), y)
+
+
+@pytest.mark.parametrize("M", [1, 4, 7, 70, 250])
+def test_workspaces_of_any_contents(gpu_lib, M):
+    """A workspace of NaN gives the same bits, also where rows, or all of them, name no expert."""
+    import torch
+    say(f"[experts workspace] M={M}")
+    H, I, E, k = 256, 128, 7, 3
+    moe = Moe(torch, 14, H, I, E)
+    rng = np.random.default_rng(M)
+    x = workloads.random_x(M, M, H)
+    for none in (0.0, 0.7, 1.0):
+        e, w = _pick(rng, M, E, k, none=none)
+        want = moe.run(gpu_lib, torch, x, e, w)
+        ref, bound = moe.reference(x, e, w)
+        assert worst(want, ref, bound) <= 1.0
+        ws = torch.full((gpu_lib.moe_experts_workspace_bytes(M, H, I, k),), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(moe.run(gpu_lib, torch, x, e, w, workspace=ws), want)
+        assert none < 1.0 or not want.any()
+
+
 def test_layer_from_logits_in_a_graph(gpu_lib):
     """Route and experts captured together and replayed on other inputs, eager work between; two streams at once with
     workspaces of their own."""
