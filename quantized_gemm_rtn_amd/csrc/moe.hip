@@ -34,7 +34,7 @@ constexpr int kMoeTokens = 192;     // rows of x that a block's lists hold; more
 constexpr int kMoeMaxPairs = 1024;  // of them, (row, expert) pairs
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeWaves = 8;        // of a block, one block a CU
-constexpr int kMoeUnit = 8;         // groups of 128 channels whose (s, z) a wave loads at once
+constexpr int kMoeUnit = 8;         // groups of 128 channels whose (s, z) a wave has in its table
 constexpr int kMoePairs = 32;       // (row, expert) pairs of an item
 constexpr int kMoeFew = 4;          // rows of a batch up to which the kernels for few rows run
 constexpr int kMoeRowHalves = 136;  // of a staged row: 128 and padding (16 rows of a fragment in distinct banks)
@@ -274,8 +274,9 @@ struct __attribute__((packed, aligned(2))) EightHalves {
 // acc[i][j] += x . w[j]^T over groups g0 .. g0 + ng - 1, for 16 MT rows of x and NW tiles of
 // weights, by one wave: D groups are in flight; each group's rows of x pass through the wave's slot of LDS into the
 // order of the product's operand (4 XL rows; PERM: reordered to the codes' on the way), and a unit's (s, 1024 + z)
-// through its table, loaded a tile for each 16 lanes, eight groups at once at any alignment. Two groups' weights, the
-// halves of 128-byte lines, are asked for together (apart: 2 us more of 130).
+// through its table, loaded a tile for each 16 lanes, at any alignment, for two units at once (for one, the rest of the
+// line has mostly left the L2 when the next unit asks for it: the batch of 16 561 instead of 543 MB, 4 us more). Two
+// groups' weights, the halves of 128-byte lines, are asked for together (apart: 2 us more of 130).
 //  xs + xo[j] bytes: the lane's eight channels of group 0 of row lane / 16 + 4 j.
 template <int MT, int NW, int XL, int D, bool PERM>
 __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<NW>& tiles, const uint8_t* xs,
@@ -287,17 +288,20 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
   const int last = g0 + ng - 1;
   constexpr int P = D >= 4 ? 2 : 1;  // groups whose weights are asked for together
   uint4 wbuf[D][NW], xbuf[D][XL];
-  uint4 s8, z8;
-  int off;
+  uint4 s8[2], z8[2];
   const auto fetch_sz = [&](int g) {
-    // eight from group g on, those of the array's end instead where it has fewer left
-    const uint32_t want = tiles.s_off + 2 * g, at = min(want, tiles.s_end - 16);
-    off = (int)(want - at) >> 1;
-    s8 = reinterpret_cast<const EightHalves*>(tiles.s + at)->v;
-    z8 = reinterpret_cast<const EightHalves*>(tiles.z + at)->v;
+    // eight from group g on and eight after them, those of the array's end instead where it has fewer left
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t at = min(tiles.s_off + 2 * g + 16 * i, tiles.s_end - 16);
+      s8[i] = reinterpret_cast<const EightHalves*>(tiles.s + at)->v;
+      z8[i] = reinterpret_cast<const EightHalves*>(tiles.z + at)->v;
+    }
   };
-  const auto put_sz = [&]() {
-    const f16x8 s = as_f16x8(s8), z = as_f16x8(z8);
+  const auto put_sz = [&](bool second, int g) {
+    const f16x8 s = as_f16x8(second ? s8[1] : s8[0]), z = as_f16x8(second ? z8[1] : z8[0]);
+    const uint32_t want = tiles.s_off + 2 * g;
+    const int off = (int)(want - min(want, tiles.s_end - 16)) >> 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i >= off) table[(i - off) * 16 * NW + h % NW * 16 + r] = as_u32(f16x2{s[i], (f16)((f16)1024.0f + z[i])});
@@ -351,9 +355,11 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
     fetch_x(i, min(g0 + i, last));
   }
   int g = g0;
+  bool second = false;
   for (; g + kMoeUnit <= last; g += kMoeUnit) {  // (a unit with another after it is whole)
-    put_sz();
-    fetch_sz(g + kMoeUnit);
+    put_sz(second, g);
+    if (second) fetch_sz(g + kMoeUnit);
+    second = !second;
 #pragma unroll
     for (int u = 0; u < kMoeUnit; u += P) {
 #pragma unroll
@@ -366,7 +372,7 @@ __device__ __forceinline__ void moe_stream(f32x4 (&acc)[MT][NW], const MoeTiles<
       __builtin_amdgcn_sched_barrier(kSchedKeepGroups);  // the refill stays next to its consumption
     }
   }
-  put_sz();
+  put_sz(second, g);
 #pragma unroll
   for (int u = 0; u < kMoeUnit; ++u) {
     if (g + u <= last) {
