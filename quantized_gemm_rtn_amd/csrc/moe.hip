@@ -11,7 +11,7 @@
 //   weights, up to 32 of its (row, expert) pairs), dealt in turn to one block of eight waves a CU; a block's groups of 128
 //   channels are cut into equal shares for its waves, wherever an item begins or ends, and what waves share of an item is
 //   summed through LDS in the order of the waves. So all CUs have the same bytes to read, for any experts and sizes: one
-//   block for an expert and 16 channels took 403 us where 16 rows name eight experts of 4096 x 14336, this split 174
+//   block for an expert and 16 channels took 403 us where 16 rows name eight experts of 4096 x 14336, this split 171
 //   (floor 151). Rows of x pass through a slot of LDS of the wave's own, which orders them as the matrix operand; nothing
 //   in the loop waits for another wave. The lists of who needs what are made by every block of the first product for itself
 //   (a launch of their own would be another wait for the whole card), and left for the second.
