@@ -1,7 +1,7 @@
 // Down-projections of low-rank adapters that each row of a batch names for itself, for gfx950:
 //   t[m] = fp16(s_a x[m] . L1_a^T),  a = adapter[m],
 // L1 [n, r, K] fp16, s [n] float32 (or 1). The product kernels then add t[m] . L2_a^T to each output tile's fp32
-// accumulators (adapters_add16 and adapters_add32, beside what they add for a branch that all rows share).
+// accumulators (adapters_up16 and adapters_add32, beside what they add for a branch that all rows share).
 // t [M, r rounded up to 32]: zeros beyond r; rows of no adapter are left as they are, and nothing reads them.
 //
 //  adapters_down_dot_kernel  (few rows) a block for each row and few components: dot products, the waves split K.

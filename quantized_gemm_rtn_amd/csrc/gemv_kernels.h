@@ -275,15 +275,27 @@ struct Windows {
 };
 
 // Fixed-order sum of the KW partial tiles through LDS and the single store; with NT
-// tiles per wave, tile j holds output channel n + 16j.
-template <int KW, int NT>
+// tiles per wave, tile j holds output channel n + 16j. AD: rows that have an adapter
+// then add its product, which one of the waves has (adapters.h).
+template <int KW, int NT, bool AD = false>
 __device__ __forceinline__ void reduce_store_tiles(f32x4 (&acc)[NT], int wave, int lane, int m0, int mrows, int n,
-                                                   int N, void* y, int y_f32) {
+                                                   int N, void* y, int y_f32, const AdapterTiles<NT>& ad = {}) {
+  static_assert(KW > 1 || !AD, "adapters are dealt to several waves");
+  const int h = lane >> 4;
   if constexpr (KW > 1) {
     __shared__ f32x4 red[KW - 1][NT][64];
+    __shared__ float up[AD ? NT : 1][4][64];  // (row 4 h + i, as red has it)
     if (wave > 0) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) red[wave - 1][j][lane] = acc[j];
+    }
+    if constexpr (AD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((ad.mine >> (4 * h + i)) & 1u) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) up[j][i][lane] = ad.add[j][i];
+        }
     }
     __syncthreads();
     if (wave != 0) return;
@@ -291,8 +303,13 @@ __device__ __forceinline__ void reduce_store_tiles(f32x4 (&acc)[NT], int wave, i
     for (int w = 0; w < KW - 1; ++w)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j] += red[w][j][lane];
+    if constexpr (AD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j][i] += (ad.named >> (4 * h + i)) & 1u ? up[j][i][lane] : 0.0f;
+    }
   }
-  const int h = lane >> 4;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int nj = n + 16 * j;
@@ -622,12 +639,14 @@ gemv_lds_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __restr
       for (int b = 0; b < kSparseBatch; ++b) add(more.c[b], more.weight(b, e, sp_e1));
     }
   }
-  // low-rank branch, once per output tile (wave 0, before the waves' sum)
   if constexpr (AD) {
     f32x4 a1[1] = {acc};
-    adapters_add16<KW, 1>(a1, lr_t, lr_up, lr_r, ad_row, lr_n, M, N, m0, n0, lane, wave);
-    acc = a1[0];
-  } else if (lr_r > 0 && wave == 0) {
+    const auto ad = adapters_up16<KW, 1>(lr_t, lr_up, lr_r, ad_row, lr_n, M, N, m0, n0, lane, wave);
+    reduce_store_tiles<KW, 1, true>(a1, wave, lane, m0, mrows, n, N, y, y_f32, ad);
+    return;
+  }
+  // low-rank branch, once per output tile (wave 0, before the waves' sum)
+  if (lr_r > 0 && wave == 0) {
     f32x4 a1[1] = {acc};
     lowrank_add16<1>(a1, lr_first, lr_t, lr_up, lr_r, M, N, m0, n0, lane);
     acc = a1[0];
@@ -868,10 +887,13 @@ gemv_ring_kernel(const f16* __restrict__ x, int M, int K, const uint32_t* __rest
       }
     }
   }
+  if constexpr (AD) {
+    const auto ad = adapters_up16<KW, NT>(lr_t, lr_up, lr_r, ad_row, lr_n, M, N, m0, n0, lane, wave);
+    reduce_store_tiles<KW, NT, true>(acc, wave, lane, m0, mrows, n0 + r, N, y, y_f32, ad);
+    return;
+  }
   // low-rank branch, once per output tile (wave 0, before the waves' sum)
-  if constexpr (AD)
-    adapters_add16<KW, NT>(acc, lr_t, lr_up, lr_r, ad_row, lr_n, M, N, m0, n0, lane, wave);
-  else if (lr_r > 0 && wave == 0)
+  if (lr_r > 0 && wave == 0)
     lowrank_add16<NT>(acc, lr_first, lr_t, lr_up, lr_r, M, N, m0, n0, lane);
   reduce_store_tiles<KW, NT>(acc, wave, lane, m0, mrows, n0 + r, N, y, y_f32);
 }
