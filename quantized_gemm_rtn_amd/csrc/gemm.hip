@@ -111,7 +111,6 @@ __device__ __forceinline__ void adapters_add32(f32x16 (&acc)[MT][NT], const Gemm
                                                int lane) {
   constexpr int UN = MT * NT <= 4 ? 4 : 1;  // (128 rows a wave: prompts, with an adapter or two a subtile)
   const int h = lane >> 5, c32 = lane & 31, r = a.lr_r, tr = (r + 31) & ~31;
-  int turn = 0;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int m = mbase + 32 * i + c32;
@@ -130,8 +129,7 @@ __device__ __forceinline__ void adapters_add32(f32x16 (&acc)[MT][NT], const Gemm
           ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
           const uint32_t same = (uint32_t)__ballot(id == ad) & left;
           left &= ~same;
-          members[v] = turn == slice ? same : 0;
-          turn = turn + 1 < a.ksplit ? turn + 1 : 0;
+          members[v] = (ad & (a.ksplit - 1)) == slice ? same : 0;  // (a power of two)
         }
         ads[v] = ad;
       }

@@ -40,3 +40,13 @@ def check(wq, M, N, K, r, n, per_mille, kernel, seeds=8):
 def test_decode_kernels(gpu_lib, M, N, K, r, n, per_mille):
     say(f"[neighbours decode] M={M} N={N} K={K} r={r} n={n}")
     check(gpu_lib, M, N, K, r, n, per_mille, "gemv")
+
+
+@pytest.mark.parametrize("M,N,K,r,n,per_mille", [
+    (40, 300, 1024, 16, 9, 0),      # slices of K, no two rows alike
+    (64, 520, 4096, 64, 64, 0), (64, 520, 4096, 24, 5, 4), (33, 96, 8192, 8, 33, 0),
+    (100, 300, 1152, 16, 30, 4), (100, 300, 4224, 16, 30, 0),  # tile GEMM, its slices
+    (200, 256, 4096, 32, 12, 4), (300, 300, 2048, 8, 300, 0)])
+def test_gemms(gpu_lib, M, N, K, r, n, per_mille):
+    say(f"[neighbours gemm] M={M} N={N} K={K} r={r} n={n}")
+    check(gpu_lib, M, N, K, r, n, per_mille, "gemm", seeds=4)
