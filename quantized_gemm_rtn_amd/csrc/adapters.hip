@@ -83,11 +83,51 @@ adapters_down_dot_kernel(const f16* __restrict__ x, int K, const f16* __restrict
 }
 
 constexpr int kRowWaves = 16;
-constexpr int kRowBatch = 4;  // pairs of 32-channel steps whose loads a wave issues together
+constexpr int kRowParts = 16;  // of a chunk of K, whose sums meet in pairs
+constexpr int kRowBatch = 4;   // pairs of 32-channel steps whose loads a wave issues together
+
+// Sums of consecutive parts, added in the pairs of a binary tree (a part that is left out counts as zero): the same
+// whether one wave adds all sixteen, or each of several its own and tree_sum those.
+struct PairSum {
+  f32x4 held[5] = {};  // of 1, 2, 4, 8, 16 parts
+  int n = 0;           // (uniform)
+  template <int L = 0>
+  __device__ __forceinline__ void add(f32x4 v) {
+    if constexpr (L < 4) {
+      if ((n >> L) & 1)
+        add<L + 1>(held[L] + v);
+      else
+        held[L] = v;
+    } else {
+      held[4] = v;
+    }
+    if constexpr (L == 0) ++n;
+  }
+  __device__ __forceinline__ f32x4 sum() const {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int l = 0; l < 5; ++l)
+      if ((n >> l) & 1) v = held[l] + v;
+    return v;
+  }
+};
+
+// v[0] .. v[per - 1], a power of two of them up to N, of each the lane's
+template <int N>
+__device__ __forceinline__ f32x4 tree_sum(const f32x4 (*v)[64], int per, int lane) {
+  if constexpr (N == 1) {
+    return v[0][lane];
+  } else {
+    f32x4 low = tree_sum<N / 2>(v, per, lane);
+    if (per >= N) low += tree_sum<N / 2>(v + N / 2, per, lane);
+    return low;
+  }
+}
 
 // The waves are dealt to the adapters that the block's 16 rows name: all sixteen split K for one adapter, each has an
 // adapter of its own from nine on. (Adapter after adapter, 96 rows of as many adapters took 250 us at K = 8192.) A
-// wave's steps come in pairs, whole 128-byte lines of its rows.
+// wave's steps come in pairs, whole 128-byte lines of its rows. How many waves an adapter has goes by the other rows, so
+// a chunk's sum is made of the same sixteen parts in the same order for any number of them: a row's bits are its own.
 __global__ void __launch_bounds__(64 * kRowWaves)
 adapters_down_kernel(const f16* __restrict__ x, int M, int K, const f16* __restrict__ L1,
                      const float* __restrict__ scale, int n, int r, const int32_t* __restrict__ adapter,
@@ -95,7 +135,7 @@ adapters_down_kernel(const f16* __restrict__ x, int M, int K, const f16* __restr
   const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
-  const int c_lo = blockIdx.z * chunk, c_hi = min(K, c_lo + chunk);
+  const int c_lo = blockIdx.z * chunk, steps = (min(K, c_lo + chunk) - c_lo) / 64;  // chunks are multiples of 64
   __shared__ f32x4 red[kRowWaves][64];
   const int id = adapter[min(m0 + q, M - 1)];
   const uint32_t all = (uint32_t)__ballot(m0 + q < M && (uint32_t)id < (uint32_t)n) & 0xFFFFu;
@@ -116,33 +156,42 @@ adapters_down_kernel(const f16* __restrict__ x, int M, int K, const f16* __restr
     }
     // rows of other adapters: a row that is read anyway
     const int row = (members >> q) & 1u ? q : __builtin_ctz(members);
-    const f16* xr = x + (int64_t)(m0 + row) * K + 8 * h;
-    const f16* lr = L1 + ((int64_t)a * r + min(j0 + q, r - 1)) * K + 8 * h;
+    const f16* xr = x + (int64_t)(m0 + row) * K + c_lo + 8 * h;
+    const f16* lr = L1 + ((int64_t)a * r + min(j0 + q, r - 1)) * K + c_lo + 8 * h;
+    const int len = (steps + kRowParts - 1) / kRowParts;  // steps of 64 channels of a part; the last parts may have none
+    const int s_lo = sub * (kRowParts >> shift) * len, s_hi = min(steps, (sub + 1) * (kRowParts >> shift) * len);
+    PairSum sums;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = c_lo + 64 * sub; c0 < c_hi; c0 += 64 * per * kRowBatch) {
+    int end = s_lo + len;  // of the part
+    for (int s = s_lo; s < s_hi; s += kRowBatch) {
       uint4 av[kRowBatch][2], bv[kRowBatch][2];
 #pragma unroll
       for (int i = 0; i < kRowBatch; ++i)
-        if (c0 + 64 * per * i < c_hi) {  // wave-uniform; chunks are multiples of 64
+        if (s + i < s_hi) {  // wave-uniform
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            av[i][u] = *reinterpret_cast<const uint4*>(xr + c0 + 64 * per * i + 32 * u);
-            bv[i][u] = *reinterpret_cast<const uint4*>(lr + c0 + 64 * per * i + 32 * u);
+            av[i][u] = *reinterpret_cast<const uint4*>(xr + 64 * (s + i) + 32 * u);
+            bv[i][u] = *reinterpret_cast<const uint4*>(lr + 64 * (s + i) + 32 * u);
           }
         }
 #pragma unroll
       for (int i = 0; i < kRowBatch; ++i)
-        if (c0 + 64 * per * i < c_hi) {
+        if (s + i < s_hi) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) acc = mfma_16x16x32(as_f16x8(av[i][u]), as_f16x8(bv[i][u]), acc);
+          if (s + i + 1 == end) {
+            sums.add(acc);
+            acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            end += len;
+          }
         }
     }
-    red[wave][lane] = acc;
+    if (s_hi > end - len) sums.add(acc);  // a last part that is shorter
+    red[wave][lane] = sums.sum();
   }
   __syncthreads();
   if (which >= count || sub != 0) return;
-  f32x4 acc = red[wave][lane];
-  for (int w = 1; w < per; ++w) acc += red[wave + w][lane];
+  const f32x4 acc = tree_sum<kRowWaves>(red + wave, per, lane);
   // row 4 h + i, component j0 + q
   const bool last = blockIdx.x == gridDim.x - 1;
   const float s = scale ? scale[a] : 1.0f;

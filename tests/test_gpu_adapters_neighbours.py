@@ -50,3 +50,12 @@ def test_decode_kernels(gpu_lib, M, N, K, r, n, per_mille):
 def test_gemms(gpu_lib, M, N, K, r, n, per_mille):
     say(f"[neighbours gemm] M={M} N={N} K={K} r={r} n={n}")
     check(gpu_lib, M, N, K, r, n, per_mille, "gemm", seeds=4)
+
+
+@pytest.mark.parametrize("M,N,K,r,n,kernel", [
+    (300, 40, 8192, 24, 9, "gemv"), (131, 33, 16512, 40, 131, "gemv"), (400, 48, 1280, 80, 3, "gemm"),
+    (2100, 16, 2048, 16, 30, "gemv"), (1100, 64, 256, 128, 20, "gemm"), (700, 270, 1152, 56, 5, "gemm")])
+def test_down_projection_of_many_rows(gpu_lib, M, N, K, r, n, kernel):
+    """(Its waves are dealt to the adapters of 16 rows: one to sixteen waves share K for a row.)"""
+    say(f"[neighbours down] M={M} N={N} K={K} r={r} n={n}")
+    check(gpu_lib, M, N, K, r, n, 0, kernel, seeds=4)
