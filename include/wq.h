@@ -306,10 +306,13 @@ size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64
  *  (ceil(M / 16) N K up to 2^27, with eight adapters or more 2^28), and a single row takes the
  *  MFMA decode kernel.
  *  workspace: required for M >= 1, 256-byte aligned, wq_linear_adapters_workspace_bytes bytes;
- *  contents on entry do not matter.
+ *  contents on entry do not matter. It holds t between the call's launches: calls that may run
+ *  at once (other streams, captured graphs) need one each.
  * t = s x . L1^T is accumulated in fp32 and rounded once to fp16 (it is an MFMA operand;
- * beyond 65504 it is infinite); each output tile adds t . L2^T to its fp32 accumulators before the one store of y. An
- * adapter's infinities and NaN reach only the rows that name it. Deterministic.
+ * beyond 65504 it is infinite); each output tile adds t . L2^T to its fp32 sums before the one
+ * store of y. An adapter's infinities and NaN reach only the rows that name it. Deterministic;
+ * at the same sizes and n_adapters (M up to 10^6) a row has the same bits whatever the other
+ * rows hold, which adapters they name and where it stands among them.
  */
 int wq_linear_adapters(const uint16_t* x, int64_t M, int64_t K,
                        const uint32_t* packed, const uint16_t* scales, const uint16_t* zeros,
@@ -351,8 +354,10 @@ size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t t
  *           that names an expert twice has it with the sum of both weights.
  *  weights  [M, top_k] float32.   top_k 1 to 16, E 1 to 1024 (WQ_ERR_UNSUPPORTED beyond).
  *  gate_up  [E, 2 I, H/8] uint32 as written by wq_pack, each expert's I rows of G and then its
- *           I rows of U; gate_up_scales, gate_up_zeros [E, 2 I, H/128] fp16.
- *  down     [E, H, I/8] uint32; down_scales, down_zeros [E, H, I/128] fp16.
+ *           I rows of U; gate_up_scales, gate_up_zeros [E, 2 I, H/128] fp16 as written by
+ *           wq_quantize_rtn (zero-points are integers from 0 to 15; others would be rounded).
+ *  down     [E, H, I/8] uint32; down_scales, down_zeros [E, H, I/128] fp16, as those.
+ *           There is no sparse term: the matrices are quantized with sparse_k = 0.
  *  H, I     multiples of 128 up to 65536, 2 H I below 2^31; M up to 65535 * 64, M * H below 2^31.
  *  group    128.   y  [M, H] out, fp16 or float32 (y_dtype), 4-byte aligned.
  *  workspace: required for M >= 1, 256-byte aligned, wq_moe_experts_workspace_bytes bytes;

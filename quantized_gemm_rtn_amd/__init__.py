@@ -423,7 +423,8 @@ def linear_adapters(x, packed, scales, zeros, L1, L2, adapter, adapter_scale=Non
     multiple of 8), ``adapter_scale`` float32 [n] (1 when omitted).
 
     ``workspace`` (uint8 device tensor of ``linear_adapters_workspace_bytes`` bytes) is
-    allocated per call when omitted."""
+    allocated per call when omitted; calls that may run at once need one each. A row's result
+    does not depend on the batch's other rows, only on its sizes."""
     import torch
     lib = load()
     f16, i32 = torch.float16, torch.int32
@@ -512,9 +513,10 @@ def moe_experts(x, experts, weights, gate_up, gate_up_scales, gate_up_zeros, dow
     ``x`` float16 [M, H]; ``experts`` int32 and ``weights`` float32 [M, top_k], as from
     ``moe_route`` (experts outside [0, E) stand for nothing); ``gate_up`` int32
     [E, 2 I, H / 8] (each expert's rows of G, then those of U) with scales and zero-points
-    [E, 2 I, H / 128]; ``down`` int32 [E, H, I / 8] with [E, H, I / 128]. ``workspace`` (uint8
-    device tensor of ``moe_experts_workspace_bytes`` bytes) is allocated per call when
-    omitted."""
+    [E, 2 I, H / 128]; ``down`` int32 [E, H, I / 8] with [E, H, I / 128]: each expert's as
+    ``quantize_rtn`` (no sparse entries) and ``pack`` give them, ``torch.stack``-ed.
+    ``workspace`` (uint8 device tensor of ``moe_experts_workspace_bytes`` bytes) is allocated
+    per call when omitted; calls that may run at once need one each."""
     import torch
     lib = load()
     f16, i32, f32 = torch.float16, torch.int32, torch.float32
