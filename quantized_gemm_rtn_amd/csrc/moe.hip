@@ -4,7 +4,7 @@
 //   experts:  y = sum over the row's experts e of w_e ((silu(x G_e^T) * (x U_e^T)) D_e^T),
 //             silu(a) = a / (1 + exp(-a)), every matrix in 4 bits with (s, z) per 128 channels
 //
-// The layer's bound is the bytes of the experts that rows name: 9/16 of a byte a weight, read once for each 32 rows of an
+// The layer's bound is the bytes of the experts that rows name: 17/32 of a byte a weight, read once for each 32 rows of an
 // expert (a copy of 2 + 2 GiB runs at 4.95 TB/s on this card; the floors below are at that rate).
 //
 // moe_rows_kernel     Both products, G_e and U_e together and then D_e. The work is items, (an expert, 64 rows of its
