@@ -6,6 +6,11 @@ namespace wq {
 
 constexpr int64_t kDotMinK = 12288;  // the single-row kernel from this K on (see launch_gemv)
 
+// The decode kernels stage a tile's scales and zero-points in LDS: those of 284 000 channels fit beside 16 rows' slots.
+bool gemv_fits(int64_t M, int64_t K, bool g64, bool adapters) {
+  return ring_fits(1, M <= 4 ? 1 : (M <= 8 ? 2 : 4), (g64 ? 2 : 1) * (K / kGroup), adapters);
+}
+
 hipError_t launch_gemv(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed,
                        const uint16_t* scales, const uint16_t* zeros, int64_t N, const int32_t* row_ptr,
                        const int32_t* col, const uint16_t* val, void* y, int y_f32, const LowRank& lr,

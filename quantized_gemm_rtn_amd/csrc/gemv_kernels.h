@@ -328,6 +328,16 @@ __device__ __forceinline__ void reduce_store_tiles(f32x4 (&acc)[NT], int wave, i
   }
 }
 
+// LDS of gemv_ring_kernel: each wave's slot of 4 xl rows of a group, and nt tiles' scales and zero-points, gs a row.
+inline int64_t ring_lds(int nt, int xl, int64_t gs) {
+  return (int64_t)nt * 16 * (gs + 1) * 4 + (int64_t)kGemvWaves * 4 * xl * 136 * 2;
+}
+// Whether a CU's 160 KB hold it beside what reduce_store_tiles has: three waves' partials of a tile, and with adapters
+// their products.
+inline bool ring_fits(int nt, int xl, int64_t gs, bool adapters) {
+  return ring_lds(nt, xl, gs) + nt * (3 * 1024 + (adapters ? 1024 : 0)) <= 160 * 1024;
+}
+
 template <int KW>
 __device__ __forceinline__ void reduce_store(f32x4 acc, int wave, int lane, int m0, int mrows, int n, int N,
                                              void* y, int y_f32) {

@@ -22,8 +22,7 @@ inline hipError_t launch_ring(const uint16_t* x, int64_t M, int64_t K, const uin
                               const uint16_t* scales, const uint16_t* zeros, int64_t N, const int32_t* row_ptr,
                               const int32_t* col, const uint16_t* val, void* y, int y_f32, const LowRank& lr,
                               hipStream_t stream) {
-  const size_t lds = (SZV == kSzInRegs ? 0 : (size_t)NT * 16 * (K / kGroup + 1) * 4) +
-                     (size_t)kGemvWaves * 4 * XL * 136 * 2;
+  const size_t lds = (size_t)ring_lds(SZV == kSzInRegs ? 0 : NT, XL, K / kGroup);
   return launch_rows(gemv_ring_kernel<kGemvWaves, kGemvRingDepth, XL, NT, SZV, SP, 4, false, AD>, lds, 16 * NT, x, M, K, packed,
                      scales, zeros, N, row_ptr, col, val, y, y_f32, lr, stream);
 }
@@ -88,7 +87,11 @@ hipError_t launch_gemv_mfma(const uint16_t* x, int64_t M, int64_t K, const uint3
   // the most blocks at most 15 % above the mean: 344 pairs of 11008 channels on 256
   // CUs, 1.49x, run faster as 688 single tiles)
   const int64_t pairs = ((N + 31) / 32) * ((M + 15) / 16);
-  const int nt = pairs >= kNumCu && (pairs + kNumCu - 1) / kNumCu * kNumCu * 100 <= 115 * pairs ? 2 : 1;
+  // (and their scales and zero-points fit: rows of 140 000 channels and more have one tile)
+  const int nt = pairs >= kNumCu && (pairs + kNumCu - 1) / kNumCu * kNumCu * 100 <= 115 * pairs &&
+                         ring_fits(2, xl, G, AD)
+                     ? 2
+                     : 1;
   // per-wave staging with (s, z) in registers, loaded per window of D groups with its
   // weights, when each wave has at most two windows (up to 4096 input channels):
   // 4096 x 4096 at M = 16, 8 and 4 9.7, 7.3 and 6.7 against 10.2, 7.6 and 7.1 us,

@@ -264,7 +264,9 @@ size_t wq_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 // Shapes that take the tile GEMM (a group count that is not a multiple of four)
 // keep the rule measured before these tiles: the decode kernel while the GEMM's
 // grid has fewer than 128 blocks.
+// Rows too long for the decode kernels' LDS take the GEMM.
 int wq_auto_kernel(int64_t M, int64_t N, int64_t K) {
+  if (!wq::gemv_fits(M, K, false, false)) return WQ_KERNEL_GEMM;
   if (M <= 16) return WQ_KERNEL_GEMV;
   if (M > 64 || N < 1 || K < kGroup || K % kGroup != 0) return WQ_KERNEL_GEMM;
   const wq::GemmPlanInfo p = wq::gemm_plan_info(M, N, K);
@@ -285,7 +287,8 @@ int wq_linear_sparse_bits(const uint16_t* x, int64_t M, int64_t K, const uint32_
   if (bits != 3 && bits != 4) return WQ_ERR_UNSUPPORTED;
   if (bits == 3 && !aligned(packed, 4)) return WQ_ERR_ALIGN;
   if (M == 0) return WQ_OK;
-  if (kernel == WQ_KERNEL_AUTO) kernel = wq_auto_kernel(M, N, K);
+  if (kernel == WQ_KERNEL_AUTO)
+    kernel = group == 64 && !wq::gemv_fits(M, K, true, false) ? WQ_KERNEL_GEMM : wq_auto_kernel(M, N, K);
   const int y_f32 = y_dtype == WQ_F32;
   const int32_t* rp = nnz > 0 ? row_ptr : nullptr;  // nnz == 0: the dense product
   wq::WFormat f;
@@ -368,6 +371,7 @@ namespace {
 // 34 / 29, 300 of 4096 x 4096 52 / 39; each row its own: 64 rows of 8192 x 3584 31 / 38, of 11008 x 4096 40 / 40, 96 of it
 // 72 / 78, 300 of 4096 x 4096 75 / 75, of 8192 x 3584 125 / 107. (Of many adapters rows of a batch may still name one.)
 int adapters_auto_kernel(int64_t M, int64_t N, int64_t K, int64_t n_adapters) {
+  if (!wq::gemv_fits(M, K, false, true)) return WQ_KERNEL_GEMM;
   return (M + 15) / 16 * N * K <= (int64_t)1 << (n_adapters < 8 ? 27 : 28) ? WQ_KERNEL_GEMV : wq_auto_kernel(M, N, K);
 }
 }  // namespace

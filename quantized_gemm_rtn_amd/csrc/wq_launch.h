@@ -133,6 +133,7 @@ struct WFormat {
 };
 
 // mfma_only: never the single-row kernel (the MFMA decode kernels at every M)
+bool gemv_fits(int64_t M, int64_t K, bool g64, bool adapters);  // whether the decode kernels take rows of K channels
 hipError_t launch_gemv(const uint16_t* x, int64_t M, int64_t K, const uint32_t* packed,
                        const uint16_t* scales, const uint16_t* zeros, int64_t N, const int32_t* row_ptr,
                        const int32_t* col, const uint16_t* val, void* y, int y_f32, const LowRank& lr,
