@@ -45,6 +45,7 @@ thread_local hipError_t last_hip_error = hipSuccess;
 
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return WQ_OK;
+  (void)hipGetLastError();  // (a call other than a launch has left it in HIP's own state)
   last_hip_error = e;
   return WQ_ERR_HIP;
 }

@@ -75,3 +75,19 @@ def test_adapters(gpu_lib, M, N, K):
             # t's sum and its rounding to fp16, and r terms more in float32
             most[m] += two.abs() @ (up + 2.0 ** -11 * (t.abs() + up) + 2.0 ** -25 + (2 * r + 8) * 2.0 ** -24 * t.abs())
     assert ((y[:, rows].double() - ref).abs() <= most).all()
+
+
+def test_a_kernel_that_does_not_fit(gpu_lib):
+    """Asked for by name it is an error, which leaves nothing behind in HIP's state or on the stream."""
+    import torch
+    say("[long rows, refused]")
+    N, K = 64, 2 ** 19
+    packed, s, z = layer(torch, N, K, 1)
+    x = torch.ones(4, K, dtype=torch.float16, device="cuda")
+    want = gpu_lib.linear(x, packed, s, z)
+    for _ in range(2):
+        with pytest.raises(gpu_lib.WQError):
+            gpu_lib.linear(x, packed, s, z, kernel="gemv")
+        assert (torch.zeros(8, device="cuda") == 0).all()
+        torch.cuda.synchronize()
+        assert torch.equal(gpu_lib.linear(x, packed, s, z), want)
