@@ -303,8 +303,8 @@ size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64
  *                 none. Rows in any order; rows of one adapter next to each other are faster.
  *  row_ptr / col / val / nnz as in wq_linear_sparse; row_ptr may be NULL when nnz == 0.
  *  kernel as in wq_linear_sparse_kernel, but AUTO keeps to the decode kernels also for more rows
- *  (ceil(M / 16) N K up to 2^27, with eight adapters or more 2^28), and a single row takes the
- *  MFMA decode kernel.
+ *  (ceil(M / 16) N K up to 3 2^26 and M N up to 2^20, with eight adapters or more twice and three
+ *  times that), and a single row takes the MFMA decode kernel.
  *  workspace: required for M >= 1, 256-byte aligned, wq_linear_adapters_workspace_bytes bytes;
  *  contents on entry do not matter. It holds t between the call's launches: calls that may run
  *  at once (other streams, captured graphs) need one each.

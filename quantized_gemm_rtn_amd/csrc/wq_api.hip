@@ -366,14 +366,33 @@ size_t wq_linear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64
 }
 
 namespace {
-// The decode kernels read the weights once for each 16 rows; their waves share out a tile's adapters, where the GEMM's
-// take a column's one after another. In us, decode kernels / GEMM, all rows of one adapter of rank 16: 96 rows of
-// 4096 x 4096 24.5 / 37, of 12000 x 1408 34 / 41, 300 of 4000 x 1408 35 / 40, 64 of 8192 x 3584 26 / 23, of 11008 x 4096
-// 34 / 29, 300 of 4096 x 4096 52 / 39; each row its own: 64 rows of 8192 x 3584 31 / 38, of 11008 x 4096 40 / 40, 96 of it
-// 72 / 78, 300 of 4096 x 4096 75 / 75, of 8192 x 3584 125 / 107. (Of many adapters rows of a batch may still name one.)
+// The decode kernels read and unpack the weights once for each 16 rows, and their waves share out a tile's adapters; the
+// GEMM does that once for 64 or 128, but takes a column's adapters one after another. So the decode kernels stay ahead
+// for more rows than without adapters, until the work (16 rows' tiles by N K) or the tiles' number (M N: a short K leaves
+// the GEMM little else to do) is too much. How many adapters a tile names is only on the device; of fewer than eight it
+// is few. In us, decode kernels / GEMM, rank 16, 17 layers of 128 to 28672 channels measured at 17 to 4096 rows:
+//                        rows of one adapter | of four in turn | each its own
+//   1024 x 1024,    512       18.5 / 24.2         19.9 / 32.4      21.1 / 110
+//                  2048       60.4 / 31.6         66.0 / 41.9      71.9 / 140
+//                  4096        102 / 28.8          117 / 41.9       142 / 155
+//   4096 x 512,     192       19.8 / 18.0         22.3 / 25.7      23.9 / 103
+//                   512       46.6 / 19.3         50.7 / 27.7      55.6 / 106
+//                  1024       87.6 / 22.5         96.2 / 31.0       106 / 110
+//   4096 x 4096,    128       26.5 / 34.3         28.0 / 37.9      30.8 / 67.2
+//                   256       45.7 / 39.0         48.7 / 41.6      53.6 / 68.7
+//                   512       82.6 / 47.0         89.0 / 49.0      96.4 / 77.2
+//   8192 x 3584,     64       26.9 / 24.0         28.0 / 24.3      31.6 / 37.5
+//   11008 x 4096,    64       34.6 / 30.4         37.1 / 31.0      40.9 / 39.7
+//   4096 x 14336,    48       39.5 / 33.3         40.2 / 33.9      45.7 / 40.8
+// Over all that was measured these bounds take 1.3 % more time than always the faster one for rows of one adapter and four
+// in turn, 4 % for rows of one and each its own (2^27 and 2^28 tiles by N K alone: 5 and 6 %). At worst, where rows name
+// but one of many adapters: 4096 x 512 at 512 rows, 46.6 for 19.3.
 int adapters_auto_kernel(int64_t M, int64_t N, int64_t K, int64_t n_adapters) {
   if (!wq::gemv_fits(M, K, false, true)) return WQ_KERNEL_GEMM;
-  return (M + 15) / 16 * N * K <= (int64_t)1 << (n_adapters < 8 ? 27 : 28) ? WQ_KERNEL_GEMV : wq_auto_kernel(M, N, K);
+  const bool few = n_adapters < 8;
+  const int64_t tiles = (M + 15) / 16;
+  if (tiles * N * K <= (int64_t)(few ? 3 : 6) << 26 && M * N <= (int64_t)(few ? 1 : 3) << 20) return WQ_KERNEL_GEMV;
+  return wq_auto_kernel(M, N, K);
 }
 }  // namespace
 
