@@ -344,9 +344,9 @@ int wq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int64_t E,
 size_t wq_moe_experts_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t top_k);
 
 /*
- * wq_moe_experts - a mixture-of-experts layer of 4-bit matrices for a few tokens (of each 192
- * rows, 1024 / top_k if that is fewer, each 32 that name an expert read its matrices once; a long
- * prompt is better served by a product for each expert):
+ * wq_moe_experts - a mixture-of-experts layer of 4-bit matrices for a few tokens (of each 512
+ * rows, 1024 / top_k if that is fewer, each 32 that name an expert read its matrices once; so a
+ * prompt takes two to three times what its operations would at the matrix units' rate):
  *   y[m] = sum over j of weights[m, j] ((silu(x[m] . G_e^T) * (x[m] . U_e^T)) . D_e^T),
  *   e = experts[m, j],  silu(a) = a / (1 + exp(-a)).
  *  x        [M, H] fp16, 16-byte aligned.

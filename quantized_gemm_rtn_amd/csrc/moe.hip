@@ -30,13 +30,21 @@
 
 namespace wq {
 
-constexpr int kMoeTokens = 192;     // rows of x that a block's lists hold; more come as further blocks
+// Rows of x that a block's lists hold; more come as further blocks, which read the weights again. As many as their
+// pairs allow, but where all of 1024 rows name one expert, whose pairs a block puts in order alone. In us, at most 192 /
+// 256 / 512 / 1024 rows: 256 rows, four of 32 experts of 4096 x 1536, 207 / 160 / 161 / 161; 512 rows, two of them, 251 /
+// 193 / 162 / 161; 512 rows, two of eight of 4096 x 14336, 1003 / 910 / 805 / 809; 1024 rows, one of 64 of 2048 x 1024,
+// 279 / 205 / 121 / 78; 1024 rows that all name the same of 16 of 1024 x 512, 87 / 77 / 76 / 91.
+constexpr int kMoeTokens = 512;
 constexpr int kMoeMaxPairs = 1024;  // of them, (row, expert) pairs
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeWaves = 8;        // of a block, one block a CU
 constexpr int kMoeUnit = 8;         // groups of 128 channels whose (s, z) a wave has in its table
 constexpr int kMoePairs = 32;       // (row, expert) pairs of an item
-constexpr int kMoeFew = 4;          // rows of a batch up to which the kernels for few rows run
+// Rows of a batch up to which the kernels for few rows run: as many as one load of a group brings (in us, these kernels /
+// the general ones, one and four rows: two of eight experts of 4096 x 14336 48.6 / 66.9 and 110 / 131, eight of 64 of
+// 2048 x 1024 19.6 / 30.4 and 46.5 / 43.9, six of 60 of 2176 x 1408 23.2 / 29.5 and 49.6 / 46.1).
+constexpr int kMoeFew = 4;
 constexpr int kMoeRowHalves = 136;  // of a staged row: 128 and padding (16 rows of a fragment in distinct banks)
 
 // What some rows of x have to do, from their experts: the active experts, those of the most pairs first (so that items
@@ -114,7 +122,8 @@ __device__ __forceinline__ void moe_lists(MoeLists& l, MoeScratch& w, const MoeA
 #pragma unroll
   for (int i = 0; i < PER; ++i) made[i] = place[i] >= 0 ? w.count[w.ids[t + T * i]] : 0;  // pairs of the pair's expert
   // experts EPER t .. + EPER - 1: pairs, tiles beyond an expert's first, and active ones, in one sum (11, 6 and 11 bits)
-  // for each class of experts: of more than 16 pairs, of more than 4, the others
+  // for each class of experts: of more than 16 pairs, of more than 4, the others, whose items take moe_rows_kernel's three
+  // ways of unequal length (16 rows through small experts 85.2 us, in the experts' own order 88.5, 150 drafted 134 and 138)
   const auto packed = [](int n) { return n == 0 ? 0 : n | ((n - 1) / kMoePairs) << 11 | 1 << 17; };
   const auto class_of = [](int n) { return n > 16 ? 0 : (n > 4 ? 1 : 2); };
   int own[EPER], sum[3] = {0, 0, 0}, before[3];

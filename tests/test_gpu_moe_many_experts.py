@@ -112,3 +112,16 @@ def test_a_layer_from_the_quantizer(gpu_lib):
     ref, bound = oracle.rows.moe_experts(x, e, w, *held)
     y = gpu_lib.moe_experts(to_dev(x, torch), to_dev(e.astype(np.int32), torch), to_dev(w, torch), *args)
     assert worst(y, ref, bound) <= 1.0
+
+
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("M,E,k", [(192, 9, 5), (205, 20, 5), (257, 20, 4), (341, 12, 3), (342, 12, 3), (512, 30, 2),
+                                   (513, 30, 2), (512, 5, 1), (1100, 40, 1)])
+def test_rows_around_a_block_of_lists(gpu_lib, M, E, k, same):
+    """As many rows as one block's lists hold (512, and 1024 pairs), one more, and several blocks of them; all on the same
+    experts, whose pairs then fill up to sixteen tiles, or spread."""
+    say(f"[experts lists] M={M} E={E} k={k} same={same}")
+    rng = np.random.default_rng(M + k)
+    x = workloads.random_x(M, M, H)
+    e = np.array([np.arange(k) if same else rng.permutation(E)[:k] for _ in range(M)])
+    check(gpu_lib, Codes(E + M, E), x, e, rng.uniform(0.05, 1.0, (M, k)), k)
