@@ -230,9 +230,20 @@ adapters_finish_kernel(const float* __restrict__ part, int chunks, int M, const 
   t[i] = (f16)v;
 }
 
-// Whether each row reads its adapter for itself: up to 64 MB in all, at worst from HBM. (The other kernel reads an adapter
-// once for 16 rows, but a wave alone reads it where they name many: in whole calls of 96 rows and 4096 x 4096, 16
-// components, 24 us where all rows name one adapter, 43 where each names its own.)
+// Whether each row reads its adapter for itself: up to 64 MB in all, at worst from HBM. The other kernel reads an adapter
+// once for 16 rows that name it, but a wave alone reads it where they name many. In us, whole calls of 128 channels by
+// this one / the other, rows of one adapter and each its own:
+//   16 components, K = 1024,   512 rows (16 MB)    8.8 /  9.0     9.8 / 25.8
+//                             2048      (64 MB)   18.1 / 12.3    19.8 / 30.1
+//                             4096     (128 MB)   33.5 / 20.2    36.1 / 39.5
+//                  K = 4096,   512      (64 MB)   15.2 / 13.7    18.7 / 31.4
+//                             1024     (128 MB)   24.4 / 17.7    28.0 / 50.9
+//                             2048     (256 MB)   43.3 / 24.3    47.6 / 89.6
+//                  K = 8192,   256      (64 MB)   19.2 / 16.5    30.6 / 33.6
+//                              512     (128 MB)   30.6 / 21.2    49.4 / 54.2
+//   64 components, K = 4096,   128      (64 MB)   11.9 / 12.9    18.8 / 31.0
+//                              512     (256 MB)   21.3 / 16.9    39.8 / 82.4
+// (So beyond the bound rows that each name their own would still be faster by themselves; prompts' rows come in runs.)
 static bool few_rows(int64_t M, int64_t K, int64_t r) { return M * r <= ((int64_t)1 << 25) / K; }
 static int64_t t_stride(int64_t r) { return (r + 31) / 32 * 32; }
 
